@@ -374,6 +374,81 @@ int dyra_solver_status(const dyra_spec* spec, const void* workspace, int64_t B, 
 int dyra_dense_ref(const void* X, const void* Wt, const void* bias, void* Y, int64_t n,
                    int64_t c1, int64_t c2, int32_t dtype, void* stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection.  Rows of all
+ * requests are concatenated; request b is rows [offsets[b], offsets[b + 1])
+ * and uses adapter a = slots_dev[b] of a pool of `slots` adapters; a value
+ * outside 0 .. slots - 1 (by convention -1) means none.  For a row t of it
+ *   H_t = X_t A_a^T                       (the first rank[a] of r columns)
+ *   Y_t = base_t + scale[a] H_t B_a^T     (base: the shared projection's output)
+ * and for a row without an adapter H_t = 0, Y_t = base_t.
+ *   slots: 1 .. DYRA_ADAPTER_MAX_SLOTS;  r: a multiple of 8, <= 128;
+ *   c1, c2: multiples of 8.
+ *   A: device [slots][r][c1], B: device [slots][c2][r], dtype.  What they hold
+ *   past an adapter's rank is not used (it may be anything, NaN included).
+ *   rank:  device int32[slots] in 0 .. r (values outside are clamped), or NULL: r.
+ *   scale: device float[slots], or NULL: 1.
+ */
+#define DYRA_ADAPTER_MAX_SLOTS 2048
+typedef struct {
+  int32_t slots, r;
+  int64_t c1, c2;
+  const void* A;
+  const void* B;
+  const int32_t* rank;
+  const float* scale;
+} dyra_adapters;
+
+/*
+ * Device workspace bytes of dyra_adapter_forward (backward = 0) or
+ * dyra_adapter_backward (backward = 1) for n rows of B requests.
+ * Errors: EINVAL, ESHAPE.
+ */
+int dyra_adapter_workspace_size(int32_t slots, int32_t r, int64_t c1, int64_t c2, int64_t n, int64_t B,
+                                int32_t dtype, int32_t backward, size_t* bytes);
+
+/*
+ * The adapters' forward pass (asynchronous on `stream`; no host
+ * synchronisation, so the offsets and slots may change between replays of a
+ * captured graph).
+ *   X: device [n][c1], rows ldx elements apart.  base: device [n][c2], rows
+ *   ldb apart, or NULL for zero.  Y: device [n][c2], rows ldy apart; may be
+ *   base itself (same pointer and stride), must not overlap X or the pool
+ *   otherwise.  Strides are multiples of 8 (bf16) or 4 (fp32) elements.
+ *   H: device float [n][r] that receives X A^T (0 past an adapter's rank and
+ *   in rows without one) for the backward pass, or NULL.
+ *   offsets_dev: device int32[B + 1], offsets[0] = 0, non-decreasing (empty
+ *   requests are allowed), offsets[B] = n; slots_dev: device int32[B].  The
+ *   kernels read offsets[1 .. B - 1] only, clamp them to 0 .. n, and touch no
+ *   memory out of range whatever they hold; offsets that decrease give
+ *   unspecified values in Y and H.  n and B may be 0 (no request: no adapter).
+ * bf16: H is accumulated in fp32 and enters the second product as two bf16
+ * terms, so Y is rounded once.  A request's result does not depend on the
+ * other requests of the call other than through the order of the partial
+ * sums.  Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
+ */
+int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int64_t ldx, const void* base, int64_t ldb,
+                         void* Y, int64_t ldy, float* H, int64_t n, int64_t B, const int32_t* offsets_dev,
+                         const int32_t* slots_dev, int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The adapters' backward pass, from the gradient dY of Y:
+ *   G_t = scale[a] dY_t B_a,   dX_t = dX_base_t + G_t A_a,
+ *   dA_a = sum over the rows of a's requests of G_t^T X_t,
+ *   dB_a = sum of scale[a] dY_t^T H_t.
+ *   H: device float [n][r] as the forward pass wrote it (needed for dA, dB).
+ *   dX_base: device [n][c1], the shared projection's input gradient, or NULL
+ *   for zero; dX: device [n][c1] (may be dX_base itself), or NULL: not wanted.
+ *   dA: device float [slots][r][c1], dB: device float [slots][c2][r], every
+ *   element written (0 past a rank and for adapters without rows); both or
+ *   neither may be NULL.  Sums are fp32 in a fixed order: the same call gives
+ *   the same bits.  Other arguments and errors as for dyra_adapter_forward.
+ */
+int dyra_adapter_backward(const dyra_adapters* ad, const void* X, int64_t ldx, const void* dY, int64_t lddy,
+                          const float* H, const void* dX_base, int64_t lddb, void* dX, int64_t lddx, float* dA,
+                          float* dB, int64_t n, int64_t B, const int32_t* offsets_dev, const int32_t* slots_dev,
+                          int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
+
 /* Static string naming a status code. */
 const char* dyra_status_string(int code);
 

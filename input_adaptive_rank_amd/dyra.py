@@ -61,6 +61,12 @@ class HostFactors(ctypes.Structure):
     _fields_ = [(f, ctypes.POINTER(ctypes.c_double)) for f in _FACTORS]
 
 
+class Adapters(ctypes.Structure):
+    _fields_ = [("slots", ctypes.c_int32), ("r", ctypes.c_int32), ("c1", ctypes.c_int64), ("c2", ctypes.c_int64),
+                ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -105,6 +111,11 @@ def lib():
             "dyra_workspace_size_varlen_als": [SP, I64, ctypes.POINTER(I64), I32, I32, ctypes.POINTER(SZ)],
             "dyra_forward_varlen_als": [SP, P, P, P, P, I64, ctypes.POINTER(I64), P, I32, ctypes.c_float, I32, I32,
                                         P, P, SZ, P],
+            "dyra_adapter_workspace_size": [I32, I32, I64, I64, I64, I64, I32, I32, ctypes.POINTER(SZ)],
+            "dyra_adapter_forward": [ctypes.POINTER(Adapters), P, I64, P, I64, P, I64, P, I64, I64, P, P, I32, P, SZ,
+                                     P],
+            "dyra_adapter_backward": [ctypes.POINTER(Adapters), P, I64, P, I64, P, P, I64, P, I64, P, P, I64, I64, P,
+                                      P, I32, P, SZ, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
