@@ -449,6 +449,70 @@ int dyra_adapter_backward(const dyra_adapters* ad, const void* X, int64_t ldx, c
                           float* dB, int64_t n, int64_t B, const int32_t* offsets_dev, const int32_t* slots_dev,
                           int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * The norms before and after a block, fused with the block's gate and the
+ * scale of the residual stream.  Per row, y the block's output, x the stream:
+ *   u  = post(y)                           y itself for DYRA_NORM_NONE
+ *   x' = residual_scale x + gate * u       gate 1 for DYRA_GATE_NONE
+ *   z  = pre(x')                           what the next block reads
+ * with norm(v) = weight * (v - mean) / sqrt(mean((v - mean)^2) + eps) + bias,
+ * mean 0 for DYRA_NORM_RMS.  All of it in fp32 per row; x' and z are rounded
+ * once each (z from the unrounded x').
+ *   c: a multiple of 8, <= DYRA_BLOCK_NORM_MAX_C.
+ *   weights, biases: device [c], dtype, or NULL (1, 0); post_* NULL for
+ *   DYRA_NORM_NONE.  gate: device [c] (CHANNEL) or [B][c] (REQUEST: row b for
+ *   the rows of request b), dtype; NULL for NONE.
+ */
+#define DYRA_NORM_NONE  0
+#define DYRA_NORM_RMS   1
+#define DYRA_NORM_LAYER 2
+#define DYRA_GATE_NONE    0
+#define DYRA_GATE_CHANNEL 1
+#define DYRA_GATE_REQUEST 2
+#define DYRA_BLOCK_NORM_MAX_C 16384
+typedef struct {
+  int64_t c;
+  int32_t pre, post;     /* pre: RMS or LAYER */
+  int32_t gate_kind;
+  float eps, residual_scale;
+  const void *pre_weight, *pre_bias, *post_weight, *post_bias, *gate;
+} dyra_block_norm;
+
+/*
+ * Forward (asynchronous on `stream`, no workspace).
+ *   x, y: device [n][c]; x_new, z: device [n][c], dtype.  Each of x_new and z
+ *   may be x or y (same pointer), not both the same; otherwise no output
+ *   overlaps another operand.
+ *   offsets_dev: device int32[B + 1], for DYRA_GATE_REQUEST only: offsets[0]
+ *   = 0, non-decreasing, offsets[B] = n.  The kernels read offsets[1 .. B - 1]
+ *   and stay in range whatever they hold.  n may be 0.
+ * Errors (before any HIP call): EINVAL, ESHAPE (c, n, or B = 0 with rows to
+ * gate); EHIP.
+ */
+int dyra_block_norm_forward(const dyra_block_norm* p, const void* x, const void* y, void* x_new, void* z, int64_t n,
+                            int64_t B, const int32_t* offsets_dev, int32_t dtype, void* stream);
+
+/*
+ * Backward: from dz and dx_new, the gradients that reach z and x' (dx_new
+ * NULL: zero), and the forward pass's x' (as stored) and y,
+ *   d = dx_new + pre^T(dz),  dx = residual_scale d,  dy = post^T(gate * d),
+ * and, each device float [c] (the REQUEST gate's [B][c]) or NULL if not
+ * wanted, every element written, the gradients of weights, biases and gate.
+ * The REQUEST gate's must be given.  Each of dx and dy may be x_new, y, dz or
+ * dx_new (same pointer), not both the same; otherwise no output overlaps
+ * another operand.  Sums over rows are fp32 in a fixed order: the same call
+ * gives the same bits.
+ *   workspace: device, >= dyra_block_norm_workspace_size bytes.
+ */
+typedef struct {
+  float *pre_weight, *pre_bias, *post_weight, *post_bias, *gate;
+} dyra_block_norm_grads;
+int dyra_block_norm_workspace_size(const dyra_block_norm* p, int64_t n, int64_t B, int32_t dtype, size_t* bytes);
+int dyra_block_norm_backward(const dyra_block_norm* p, const void* x_new, const void* y, const void* dz,
+                             const void* dx_new, void* dx, void* dy, const dyra_block_norm_grads* grads, int64_t n,
+                             int64_t B, const int32_t* offsets_dev, int32_t dtype, void* workspace, size_t ws_bytes,
+                             void* stream);
+
 /* Static string naming a status code. */
 const char* dyra_status_string(int code);
 

@@ -17,7 +17,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = shutil.which("hipcc") or os.path.join(ROCM, "bin", "hipcc")
 
 HOST_SOURCES = ["host_linalg.cpp", "prepare.cpp"]
-HIP_SOURCES = ["dyra_kernels.hip", "adapter_kernels.hip"]
+HIP_SOURCES = ["dyra_kernels.hip", "adapter_kernels.hip", "block_norm_kernels.hip"]
 HEADERS = ["host_linalg.h", "spec.h", "device_common.h", "gemm_engine.h"]
 
 HOST_FLAGS = ["-O3", "-fPIC", "-std=c++17", "-mavx2", "-mfma", "-Wall", "-Wno-unused-function"]

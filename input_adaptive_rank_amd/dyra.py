@@ -67,6 +67,17 @@ class Adapters(ctypes.Structure):
                 ("scale", ctypes.c_void_p)]
 
 
+class BlockNorm(ctypes.Structure):
+    _fields_ = [("c", ctypes.c_int64), ("pre", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+
+
+class BlockNormGrads(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("pre_weight", "pre_bias", "post_weight", "post_bias", "gate")]
+
+
 _lib = None
 
 
@@ -111,6 +122,10 @@ def lib():
             "dyra_workspace_size_varlen_als": [SP, I64, ctypes.POINTER(I64), I32, I32, ctypes.POINTER(SZ)],
             "dyra_forward_varlen_als": [SP, P, P, P, P, I64, ctypes.POINTER(I64), P, I32, ctypes.c_float, I32, I32,
                                         P, P, SZ, P],
+            "dyra_block_norm_forward": [ctypes.POINTER(BlockNorm), P, P, P, P, I64, I64, P, I32, P],
+            "dyra_block_norm_workspace_size": [ctypes.POINTER(BlockNorm), I64, I64, I32, ctypes.POINTER(SZ)],
+            "dyra_block_norm_backward": [ctypes.POINTER(BlockNorm), P, P, P, P, P, P, ctypes.POINTER(BlockNormGrads),
+                                         I64, I64, P, I32, P, SZ, P],
             "dyra_adapter_workspace_size": [I32, I32, I64, I64, I64, I64, I32, I32, ctypes.POINTER(SZ)],
             "dyra_adapter_forward": [ctypes.POINTER(Adapters), P, I64, P, I64, P, I64, P, I64, I64, P, P, I32, P, SZ,
                                      P],
