@@ -28,7 +28,6 @@ namespace {
 
 constexpr int MAX_SLOTS = 2048;   // the grouping kernel holds three counters per slot in LDS
 constexpr int GROUP_NT = 1024;
-constexpr int TR = 64;            // edge of the weight transposition tiles
 
 __host__ __device__ __forceinline__ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -50,190 +49,27 @@ struct Requests {
   }
 };
 
-// Rows in the order of their slots: perm[p] is the row at grouped position
-// p; a tile is a run of at most `tile` positions of one slot.
+// Rows in the order of their slots, in tiles of `tile` places that hold rows
+// of one slot: place i of tile t is row perm[t tile + i], -1 past its count.
 struct Tile {
-  int32_t slot, start, count, pad;
+  int32_t slot, count;
+};
+struct Chunk {   // a run of tiles of one adapter slot
+  int32_t slot, first, tiles, pad;
 };
 struct Grouped {
-  int32_t* perm;        // [n]
+  int32_t* perm;        // [tile_cap][tile]
   Tile* tiles;          // [tile_cap], count 0 past the last
-  Tile* chunks;         // [chunk_cap], runs of `chunk` positions (adapter slots only), or null
+  Chunk* chunks;        // [chunk_cap], tiles 0 past the last, or null
   int32_t* slot_chunk;  // [slots + 1] first chunk of each slot
-  int32_t tile, chunk, tile_cap, chunk_cap;
+  int32_t tile, chunk, tile_cap, chunk_cap;   // chunk: tiles of a chunk
 };
 
-// The row at place i of a tile, or -1.  The guards keep a position or a row
-// in range even where inconsistent offsets left part of perm unwritten.
-__device__ __forceinline__ int tile_row(const int32_t* perm, const Tile& t, int i, int n) {
-  const int pos = t.start + i;
-  if (i >= t.count || (unsigned)pos >= (unsigned)n) return -1;
-  const int row = perm[pos];
+// The row at place i of tile t, or -1.  The guard keeps a row in range even
+// where inconsistent offsets left a place unwritten.
+__device__ __forceinline__ int tile_row(const Grouped& g, int t, int i, int n) {
+  const int row = g.perm[(int64_t)t * g.tile + i];
   return (unsigned)row < (unsigned)n ? row : -1;
-}
-
-// ---------------------------------------------------------------------------
-// grouping (and, for a backward pass, the weights transposed)
-// ---------------------------------------------------------------------------
-
-// inclusive sums over the workgroup's threads of three counters
-__device__ __forceinline__ void scan3(int (&v)[3], int* wave_sums) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1)
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const int u = __shfl_up(v[q], d);
-      if (lane >= d) v[q] += u;
-    }
-  if (lane == 63)
-#pragma unroll
-    for (int q = 0; q < 3; ++q) wave_sums[wave * 3 + q] = v[q];
-  __syncthreads();
-  for (int w = 0; w < wave; ++w)
-#pragma unroll
-    for (int q = 0; q < 3; ++q) v[q] += wave_sums[w * 3 + q];
-  __syncthreads();
-}
-
-template <typename E>
-struct Transpose {   // src [slots][R][C] -> dst [slots][C][R], for the slots in use
-  const E* src;
-  E* dst;
-  int32_t R, C;
-  int32_t tiles_r, tiles_c;
-};
-
-template <typename E>
-__device__ void transpose_tile(const Transpose<E>& t, const Requests& q, int tile, char* lds) {
-  const int per = t.tiles_r * t.tiles_c;
-  const int slot = tile / per, rt = (tile % per) / t.tiles_c, ct = (tile % per) % t.tiles_c;
-  int used = 0;
-  for (int b = threadIdx.x; b < q.B; b += GROUP_NT) used |= q.slot[b] == slot && q.len(b) > 0;
-  if (!__syncthreads_or(used)) return;
-  E(*buf)[TR + 2] = reinterpret_cast<E(*)[TR + 2]>(lds);
-  const E* s = t.src + (int64_t)slot * t.R * t.C;
-  E* d = t.dst + (int64_t)slot * t.R * t.C;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < TR; i += GROUP_NT / 64) {
-    const int r = rt * TR + i, c = ct * TR + x;
-    if (r < t.R && c < t.C) buf[i][x] = s[(int64_t)r * t.C + c];
-  }
-  __syncthreads();
-  for (int i = y; i < TR; i += GROUP_NT / 64) {
-    const int c = ct * TR + i, r = rt * TR + x;
-    if (r < t.R && c < t.C) d[(int64_t)c * t.R + r] = buf[x][i];
-  }
-}
-
-// Sorts the requests by slot, stably, and lists the rows in that order.  A
-// stable order makes every sum over the rows of a slot the same from call to
-// call.  Each of the first `group_wgs` workgroups does the whole sort (a few
-// thousand cycles for up to 1024 requests) and writes its share of the row
-// list and of the tile lists, so no workgroup waits for another; the others
-// transpose weight tiles.
-template <typename E>
-__global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, int group_wgs, Transpose<E> ta,
-                                                         Transpose<E> tb, int tiles_a) {
-  __shared__ __attribute__((aligned(16))) char lds[TR * (TR + 2) * 4 > 4 * GROUP_NT * 4 + 16
-                                                       ? TR * (TR + 2) * 4
-                                                       : 4 * GROUP_NT * 4 + 16];
-  __shared__ int32_t run[MAX_SLOTS + 1], tile0[MAX_SLOTS + 1], chunk0[MAX_SLOTS + 1], start[MAX_SLOTS + 1];
-  __shared__ int wave_sums[3 * GROUP_NT / 64];
-  const int tid = threadIdx.x, wg = blockIdx.x;
-  if (wg >= group_wgs) {
-    const int t = wg - group_wgs;
-    if (t < tiles_a) transpose_tile(ta, q, t, lds);
-    else transpose_tile(tb, q, t - tiles_a, lds);
-    return;
-  }
-  const int B = q.count(), S = q.slots, stride = group_wgs * GROUP_NT;
-  // rows of each slot
-  for (int s = tid; s <= S; s += GROUP_NT) run[s] = 0;
-  __syncthreads();
-  for (int b = tid; b < B; b += GROUP_NT) {
-    const int len = q.len(b);
-    if (len) atomicAdd(&run[q.id(b)], len);
-  }
-  __syncthreads();
-  // first position, first tile and first chunk of each slot; thread t sums slots [t E, (t + 1) E)
-  constexpr int EACH = (MAX_SLOTS + 1 + GROUP_NT - 1) / GROUP_NT;
-  int own[EACH][3], sum[3] = {0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < EACH; ++e) {
-    const int s = tid * EACH + e, rows = s <= S ? run[s] : 0;
-    own[e][0] = rows;
-    own[e][1] = (rows + g.tile - 1) / g.tile;
-    own[e][2] = s < S && g.chunk ? (rows + g.chunk - 1) / g.chunk : 0;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) sum[k] += own[e][k];
-  }
-  int at[3] = {sum[0], sum[1], sum[2]};
-  scan3(at, wave_sums);
-#pragma unroll
-  for (int k = 0; k < 3; ++k) at[k] -= sum[k];
-#pragma unroll
-  for (int e = 0; e < EACH; ++e) {
-    const int s = tid * EACH + e;
-    if (s <= S) {
-      start[s] = run[s] = at[0];
-      tile0[s] = at[1];
-      chunk0[s] = at[2];
-    }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) at[k] += own[e][k];
-  }
-  __syncthreads();
-  // tile lists: position -> slot by bisection in tile0 / chunk0.  Slots
-  // without rows have no tile, so the last s with tile0[s] <= i is the one.
-  auto fill = [&](Tile* list, int cap, int size, const int32_t* first, int last_slot) {
-    for (int i = wg * GROUP_NT + tid; i < cap; i += stride) {
-      int a = 0, z = last_slot + 1;
-      while (z - a > 1) {
-        const int mid = (a + z) >> 1;
-        if (first[mid] <= i) a = mid;
-        else z = mid;
-      }
-      const int end = a < S ? start[a + 1] : q.n;
-      const int p = start[a] + (i - first[a]) * size;
-      list[i] = Tile{a, p, max(min(end - p, size), 0), 0};
-    }
-  };
-  fill(g.tiles, g.tile_cap, g.tile, tile0, S);
-  if (g.chunk) {
-    fill(g.chunks, g.chunk_cap, g.chunk, chunk0, S - 1);
-    for (int s = wg * GROUP_NT + tid; s <= S; s += stride) g.slot_chunk[s] = chunk0[s];
-  }
-  // rows, 1024 requests at a time
-  int32_t* ids = reinterpret_cast<int32_t*>(lds);
-  int32_t *lens = ids + GROUP_NT, *gpos = lens + GROUP_NT, *offs = gpos + GROUP_NT;   // offs has one more
-  for (int b0 = 0; b0 < B; b0 += GROUP_NT) {
-    const int nb = min(B - b0, GROUP_NT), b = b0 + tid;
-    __syncthreads();
-    const int id = tid < nb ? q.id(b) : S + 1, len = tid < nb ? q.len(b) : 0;
-    ids[tid] = id;
-    lens[tid] = len;
-    offs[tid] = tid < nb ? q.lo(b) : q.lo(b0 + nb);
-    if (tid == 0) offs[GROUP_NT] = q.lo(b0 + nb);
-    __syncthreads();
-    int before = 0;
-    if (tid < nb)
-      for (int u = 0; u < tid; ++u) before += ids[u] == id ? lens[u] : 0;
-    gpos[tid] = tid < nb ? run[id] + before : 0;
-    __syncthreads();
-    if (len) atomicAdd(&run[id], len);
-    const int lo = offs[0], hi = offs[nb];
-    for (int t = lo + wg * GROUP_NT + tid; t < hi; t += stride) {
-      int a = 0, z = nb;   // the last request starting at or before row t (empty ones before it share its start)
-      while (z - a > 1) {
-        const int mid = (a + z) >> 1;
-        if (offs[mid] <= t) a = mid;
-        else z = mid;
-      }
-      const int p = gpos[a] + (t - offs[a]);
-      if (t - offs[a] < lens[a] && (unsigned)p < (unsigned)q.n) g.perm[p] = t;
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -267,103 +103,372 @@ __device__ __forceinline__ void split2(float v, bf16_t& hi, float& rest) {
 }
 
 // ---------------------------------------------------------------------------
+// grouping, and weights laid out as matrix operands
+// ---------------------------------------------------------------------------
+
+// inclusive sums over the workgroup's threads of three counters
+__device__ __forceinline__ void scan3(int (&v)[3], int* wave_sums, int waves) {   // later waves hold zeros
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const int u = __shfl_up(v[q], d);
+      if (lane >= d) v[q] += u;
+    }
+  if (lane == 63)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) wave_sums[wave * 3 + q] = v[q];
+  __syncthreads();
+  for (int w = 0; w < min(wave, waves); ++w)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) v[q] += wave_sums[w * 3 + q];
+  __syncthreads();
+}
+
+// The weights of a slot as operands: block (rb, kb) is rows 16 rb .. + 15 and
+// columns KSTEP kb .. + KSTEP - 1 (the reduction) of a rows x ks matrix, one
+// 16-byte chunk of each lane, 1 KB in a row.  Read from the pool as it lies,
+// an operand is 16 pieces of 64 bytes a whole weight row apart, which one L2
+// channel may have to serve alone; packed it is one contiguous kilobyte.
+template <typename T>
+struct Pack {
+  const T* src;         // [slots][rows][ks], or [slots][ks][rows] if `across`; null: no job
+  T* dst;
+  int32_t rows, ks;
+  int32_t across;
+  int32_t by_k;         // block order: kb rows / 16 + rb, else rb ks / KSTEP + kb
+  int32_t wgs;          // workgroups per slot
+  __host__ __device__ int64_t blocks() const {
+    return ((rows + 15) / 16) * (int64_t)((ks + Step<T>::K - 1) / Step<T>::K);
+  }
+};
+
+constexpr int PACK_BLOCKS = 16;   // of a workgroup: one per wave, whose loads are one latency
+
+template <typename T>
+__device__ void pack_blocks(const Pack<T>& j, const Requests& q, int id) {
+  constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K;
+  const int slot = id / j.wgs, part = id % j.wgs;
+  int used = 0;
+  for (int b = threadIdx.x; b < q.B; b += GROUP_NT) used |= q.slot[b] == slot && q.len(b) > 0;
+  if (!__syncthreads_or(used)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int RB = (j.rows + 15) / 16, KB = (j.ks + KSTEP - 1) / KSTEP, total = RB * KB;
+  const T* src = j.src + (int64_t)slot * j.rows * j.ks;
+  T* dst = j.dst + (int64_t)slot * total * (64 * KPC) + lane * KPC;
+  const int end = min((part + 1) * PACK_BLOCKS, total);
+  for (int at = part * PACK_BLOCKS + wave; at < end; at += GROUP_NT / 64) {
+    const int rb = j.by_k ? at % RB : at / KB, kb = j.by_k ? at / RB : at % KB;
+    const int row = rb * 16 + i, k = kb * KSTEP + g * KPC;
+    uint4 v = zero4();
+    if (row < j.rows && k < j.ks) {
+      if (!j.across) {
+        v = *reinterpret_cast<const uint4*>(src + (int64_t)row * j.ks + k);
+      } else {
+        T e[KPC];
+#pragma unroll
+        for (int u = 0; u < KPC; ++u) e[u] = src[(int64_t)(k + u) * j.rows + row];
+        __builtin_memcpy(&v, e, 16);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + (int64_t)at * (64 * KPC)) = v;
+  }
+}
+
+// Sorts the requests by slot, stably, and lists the rows in that order.  A
+// stable order makes every sum over the rows of a slot the same from call to
+// call.  Each of the first `group_wgs` workgroups does the whole sort (a few
+// thousand cycles for up to 1024 requests) and writes its share of the row
+// list and of the tile lists, so no workgroup waits for another; the others
+// pack weights.
+template <typename T>
+__global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, int group_wgs, Pack<T> first,
+                                                         Pack<T> second, int first_wgs) {
+  __shared__ __attribute__((aligned(16))) int32_t ids[GROUP_NT], lens[GROUP_NT], gpos[GROUP_NT], offs[GROUP_NT + 1];
+  __shared__ int32_t run[MAX_SLOTS + 1], tile0[MAX_SLOTS + 1], chunk0[MAX_SLOTS + 1], rows_of[MAX_SLOTS + 1];
+  __shared__ int wave_sums[3 * GROUP_NT / 64];
+  const int tid = threadIdx.x, wg = blockIdx.x;
+  if (wg >= group_wgs) {
+    const int t = wg - group_wgs;
+    if (t < first_wgs) pack_blocks(first, q, t);
+    else pack_blocks(second, q, t - first_wgs);
+    return;
+  }
+  const int B = q.count(), S = q.slots, stride = group_wgs * GROUP_NT;
+  // rows of each slot
+  for (int s = tid; s <= S; s += GROUP_NT) rows_of[s] = 0;
+  __syncthreads();
+  for (int b = tid; b < B; b += GROUP_NT) {
+    const int len = q.len(b);
+    if (len) atomicAdd(&rows_of[q.id(b)], len);
+  }
+  __syncthreads();
+  // first tile and first chunk of each slot; thread t sums slots [t E, (t + 1) E)
+  constexpr int EACH = (MAX_SLOTS + 1 + GROUP_NT - 1) / GROUP_NT;
+  int own[EACH][3], sum[3] = {0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int s = tid * EACH + e, rows = s <= S ? rows_of[s] : 0, tiles = (rows + g.tile - 1) / g.tile;
+    own[e][0] = rows;
+    own[e][1] = tiles;
+    own[e][2] = s < S && g.chunk ? (tiles + g.chunk - 1) / g.chunk : 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] += own[e][k];
+  }
+  int at[3] = {sum[0], sum[1], sum[2]};
+  scan3(at, wave_sums, S / (64 * EACH) + 1);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) at[k] -= sum[k];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int s = tid * EACH + e;
+    if (s <= S) {
+      tile0[s] = at[1];
+      run[s] = at[1] * g.tile;   // the next free place of the slot
+      chunk0[s] = at[2];
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) at[k] += own[e][k];
+  }
+  __syncthreads();
+  // tile i belongs to the last slot s with tile0[s] <= i (slots without rows have no tile)
+  auto slot_of = [](const int32_t* from, int i, int last) {
+    int a = 0, z = last + 1;
+    while (z - a > 1) {
+      const int mid = (a + z) >> 1;
+      if (from[mid] <= i) a = mid;
+      else z = mid;
+    }
+    return a;
+  };
+  for (int i = wg * GROUP_NT + tid; i < g.tile_cap; i += stride) {
+    const int s = slot_of(tile0, i, S), left = rows_of[s] - (i - tile0[s]) * g.tile;
+    const int count = min(max(left, 0), g.tile);
+    g.tiles[i] = Tile{s, count};
+    if (count)
+      for (int u = count; u < g.tile; ++u) g.perm[(int64_t)i * g.tile + u] = -1;
+  }
+  if (g.chunk) {
+    for (int i = wg * GROUP_NT + tid; i < g.chunk_cap; i += stride) {
+      const int s = slot_of(chunk0, i, S - 1), k = (i - chunk0[s]) * g.chunk;
+      const int from = tile0[s] + k, tiles = min((rows_of[s] + g.tile - 1) / g.tile - k, g.chunk);
+      // inside the tile list, whatever inconsistent offsets add up to
+      g.chunks[i] = Chunk{s, from, from < 0 ? 0 : max(min(tiles, g.tile_cap - from), 0), 0};
+    }
+    for (int s = wg * GROUP_NT + tid; s <= S; s += stride) g.slot_chunk[s] = chunk0[s];
+  }
+  // rows, 1024 requests at a time
+  const int64_t places = (int64_t)g.tile_cap * g.tile;
+  for (int b0 = 0; b0 < B; b0 += GROUP_NT) {
+    const int nb = min(B - b0, GROUP_NT), b = b0 + tid;
+    __syncthreads();
+    const int id = tid < nb ? q.id(b) : S + 1, len = tid < nb ? q.len(b) : 0;
+    ids[tid] = id;
+    lens[tid] = len;
+    offs[tid] = tid < nb ? q.lo(b) : q.lo(b0 + nb);
+    if (tid == 0) offs[GROUP_NT] = q.lo(b0 + nb);
+    __syncthreads();
+    int before = 0;   // rows of the same slot in earlier requests
+    if (tid < nb) {
+      const int4 *i4 = reinterpret_cast<const int4*>(ids), *l4 = reinterpret_cast<const int4*>(lens);
+#pragma unroll 4
+      for (int u = 0; u < (tid >> 2); ++u) {
+        const int4 a = i4[u], l = l4[u];
+        before += (a.x == id ? l.x : 0) + (a.y == id ? l.y : 0) + (a.z == id ? l.z : 0) + (a.w == id ? l.w : 0);
+      }
+      for (int u = tid & ~3; u < tid; ++u) before += ids[u] == id ? lens[u] : 0;
+    }
+    gpos[tid] = tid < nb ? run[id] + before : 0;
+    __syncthreads();
+    if (len) atomicAdd(&run[id], len);
+    const int lo = offs[0], hi = offs[nb];
+    for (int t = lo + wg * GROUP_NT + tid; t < hi; t += stride) {
+      int a = 0, z = nb;   // the last request starting at or before row t (empty ones before it share its start)
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (offs[mid] <= t) a = mid;
+        else z = mid;
+      }
+      const int64_t p = (int64_t)gpos[a] + (t - offs[a]);
+      if (t - offs[a] < lens[a] && p >= 0 && p < places) g.perm[p] = t;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // shrink: P[ks][row][j] = sum over a slice of K of X[row][k] W_slot[j][k]
 // ---------------------------------------------------------------------------
 
 struct ShrinkArgs {
   const void* X;        // [n][ldx]
-  const void* W;        // [slots][r][K]
+  const void* W;        // [slots][r][K], or packed by k
   const int32_t* rank;  // or null: r
   const float* scale;   // or null: 1
   float* P;             // [KS][n][r]; columns past the rank are 0
+  const float* H;       // backward: [n][r], or null
+  void *Pf, *Hf;        // backward: P and scale H as left operands of the weight gradients, or null
   int64_t ldx, K;
-  int32_t n, r, slots, sub, tiles, KS;   // sub: row blocks of 16 RT rows a tile is cut into
+  int32_t n, r, slots, sub, tiles, KS, packed;   // sub: row blocks of 16 RT rows a tile is cut into
   Grouped g;
 };
 
 constexpr int SHRINK_WAVES = 8;
+constexpr int GRAD_TILE = 64;   // rows of a tile, but for the smallest forward passes
+
+// Operands of the weight gradients: 32 rows (half a tile) of 16 rank columns,
+// lane (i, g) holding rows 8 g .. 8 g + 7 of rank column i.  bf16: three
+// terms, hi + mid + lo, 1 KB each (2^-27 relative: the gradients are fp32 and
+// the other factor is exact in bf16).  fp32: rows 8 g .. + 3, then + 4 .. + 7.
+template <typename T> constexpr int grad_parts() { return sizeof(T) == 2 ? 3 : 2; }
+template <typename T>
+__device__ __forceinline__ char* grad_block(const void* base, int64_t half_tile, int c, int cts) {
+  return const_cast<char*>(reinterpret_cast<const char*>(base)) + (half_tile * cts + c) * (grad_parts<T>() * 1024);
+}
+
+// Puts rows 4 q4 .. 4 q4 + 3 of a 16-row block, rank column 16 c + i, there.
+template <typename T>
+__device__ __forceinline__ void put_grad_rows(void* base, int64_t half_tile, int c, int cts, int upper, int q4, int i,
+                                              f32x4 v) {
+  const int g = 2 * upper + (q4 >> 1), odd = q4 & 1;
+  char* to = grad_block<T>(base, half_tile, c, cts) + (g * 16 + i) * 16;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+      bf16_t h[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float rest;
+        split2(v[q], h[q], rest);
+        v[q] = rest;
+      }
+      *reinterpret_cast<uint2*>(to + term * 1024 + odd * 8) =
+          make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    }
+  } else {
+    *reinterpret_cast<f32x4*>(to + odd * 1024) = v;
+  }
+}
+
+// Four rows (4 q4 .. + 3 of a tile's 16-row block) of rank column 16 c + i:
+// P, and in a backward pass the operands of the weight gradients.
+template <typename T>
+__device__ __forceinline__ void shrink_out(const ShrinkArgs& p, float* P, f32x4 v, const int (&rows)[4], int tile,
+                                           int block, int c, int i, int q4, int rank, float scale) {
+  const int j = 16 * c + i;
+  f32x4 h = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = rows[q];
+    v[q] = row < 0 ? 0.f : v[q] * scale;
+    if (row >= 0 && j < p.r) P[(int64_t)row * p.r + j] = v[q];
+    if (p.Hf && row >= 0 && j < rank) h[q] = p.H[(int64_t)row * p.r + j] * scale;
+  }
+  if (p.Pf && 16 * c < rank) {
+    const int64_t half = (int64_t)tile * 2 + (block >> 1);
+    const int cts = (p.r + 15) >> 4;
+    put_grad_rows<T>(p.Pf, half, c, cts, block & 1, q4, i, v);
+    put_grad_rows<T>(p.Hf, half, c, cts, block & 1, q4, i, h);
+  }
+}
 
 // One workgroup: 16 RT rows of one slot, one of KS slices of K, which its
 // waves divide again; their sums meet in LDS.  A wave reads X straight into
 // matrix operands, each 16-byte load one operand of 16 rows; the weights come
 // from the L2, one operand per 16 rank columns for every RT operands of X.
+// The loads of the next U k-steps are in flight while the present ones are
+// multiplied.
 template <typename T, int RT, int CT>
-__global__ __launch_bounds__(SHRINK_WAVES * 64) void shrink_kernel(ShrinkArgs p) {
+__global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 4) void shrink_kernel(ShrinkArgs p) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, W = SHRINK_WAVES;
-  constexpr int U = RT + CT > 6 ? 2 : 4;   // k-steps whose loads are in flight together
+  constexpr int U = RT + CT > 5 ? 1 : 2;
   constexpr int CB = CT < 4 ? CT : 4;      // 16-column blocks joined at a time
   __shared__ float red[W][CB][256];
-  __shared__ int rows[16 * RT];
   const int tile = blockIdx.x / (p.sub * p.KS), rem = blockIdx.x % (p.sub * p.KS);
   const int sub = rem / p.KS, ks = rem % p.KS;
-  const Tile t = p.g.tiles[tile];
-  if (t.count <= sub * 16 * RT) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
-  if (tid < 16 * RT) rows[tid] = tile_row(p.g.perm, t, sub * 16 * RT + tid, p.n);
-  __syncthreads();
+  const Tile t = p.g.tiles[tile];
+  // the operands of the weight gradients are whole half tiles, zero past the rows
+  if (t.count <= (p.Pf ? sub * 16 * RT & ~31 : sub * 16 * RT)) return;
   const bool none = t.slot >= p.slots;
+  int row_of[RT];
+#pragma unroll
+  for (int a = 0; a < RT; ++a) row_of[a] = tile_row(p.g, tile, (sub * RT + a) * 16 + i, p.n);
   const int rank = none ? 0 : p.rank ? min(max(p.rank[t.slot], 0), p.r) : p.r;
-  const int nct = (rank + 15) >> 4;
+  const float scale = none || !p.scale ? 1.f : p.scale[t.slot];
+  const int nct = (rank + 15) >> 4, cts = (p.r + 15) >> 4;
   f32x4 acc[RT][CT] = {};
-  if (rank > 0) {
+  const int any = __shfl(row_of[0], 0);   // a row to read in the place of one that is not there
+  if (rank > 0 && any >= 0) {
     const T* xr[RT];
 #pragma unroll
-    for (int a = 0; a < RT; ++a) {
-      const int row = rows[16 * a + i];
-      xr[a] = reinterpret_cast<const T*>(p.X) + (int64_t)(row < 0 ? max(rows[0], 0) : row) * p.ldx + g * KPC;
-    }
+    for (int a = 0; a < RT; ++a)
+      xr[a] = reinterpret_cast<const T*>(p.X) + (int64_t)(row_of[a] < 0 ? any : row_of[a]) * p.ldx + g * KPC;
+    const int steps = (int)cdiv64(p.K, KSTEP), per = (steps + p.KS * W - 1) / (p.KS * W);
+    const int s0 = (ks * W + wave) * per, s1 = min(s0 + per, steps);
     const T* wr[CT];
+    const T* ws = reinterpret_cast<const T*>(p.W) + (p.packed ? (int64_t)t.slot * steps * cts * 64 * KPC + lane * KPC
+                                                              : (int64_t)t.slot * p.r * p.K + g * KPC);
+    const int wstep = p.packed ? cts * 64 * KPC : KSTEP;
 #pragma unroll
     for (int c = 0; c < CT; ++c)   // rows past the pool's r repeat the last one; their sums are dropped
-      wr[c] = reinterpret_cast<const T*>(p.W) + ((int64_t)t.slot * p.r + min(16 * c + i, p.r - 1)) * p.K + g * KPC;
-    const int64_t steps = cdiv64(p.K, KSTEP), per = cdiv64(steps, (int64_t)p.KS * W);
-    const int64_t s0 = ((int64_t)ks * W + wave) * per, s1 = s0 + per < steps ? s0 + per : steps;
-    for (int64_t s = s0; s < s1; s += U) {
-      uint4 xv[U][RT], wv[U][CT];
+      wr[c] = ws + (p.packed ? (int64_t)min(c, cts - 1) * 64 * KPC : (int64_t)min(16 * c + i, p.r - 1) * p.K);
+    struct Stage {
+      uint4 x[U][RT], w[U][CT];
+    };
+    auto load = [&](Stage& st, int s) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t k = (s + u) * KSTEP;
-        const bool ok = s + u < s1 && k + g * KPC < p.K;
+        const int k = (s + u) * KSTEP;
+        const bool ok = s + u < s1 && k + g * KPC < (int)p.K;
 #pragma unroll
-        for (int a = 0; a < RT; ++a) xv[u][a] = ok ? *reinterpret_cast<const uint4*>(xr[a] + k) : zero4();
+        for (int a = 0; a < RT; ++a) st.x[u][a] = ok ? *reinterpret_cast<const uint4*>(xr[a] + k) : zero4();
 #pragma unroll
         for (int c = 0; c < CT; ++c)
-          wv[u][c] = ok && c < nct ? *reinterpret_cast<const uint4*>(wr[c] + k) : zero4();
+          st.w[u][c] = ok && c < nct ? *reinterpret_cast<const uint4*>(wr[c] + (int64_t)(s + u) * wstep) : zero4();
       }
+    };
+    auto mul = [&](const Stage& st) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int c = 0; c < CT; ++c)
           if (c < nct)
 #pragma unroll
-            for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], xv[u][a], wv[u][c]);
+            for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], st.x[u][a], st.w[u][c]);
+    };
+    Stage even, odd;
+    if (s0 < s1) load(even, s0);
+    for (int s = s0; s < s1; s += 2 * U) {
+      load(odd, s + U);
+      mul(even);
+      load(even, s + 2 * U);
+      mul(odd);
     }
   }
   // join the waves: D[row][j] of a 16x16 block sits at lane j + 16 (row / 4), register row % 4
-  const float scale = none || !p.scale ? 1.f : p.scale[t.slot];
   float* P = p.P + (int64_t)ks * p.n * p.r;
 #pragma unroll
   for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int cb = 0; cb < CT; cb += CB) {
       if (16 * cb >= p.r) break;
-      __syncthreads();
+      if (a + cb) __syncthreads();
 #pragma unroll
       for (int c = 0; c < CB; ++c)
         if (cb + c < nct) *reinterpret_cast<f32x4*>(&red[wave][c][lane * 4]) = acc[a][cb + c];
       __syncthreads();
-      const int cols = min(p.r - 16 * cb, 16 * CB);
-      for (int e = tid; e < 16 * cols; e += W * 64) {
-        const int row16 = e / cols, j = e % cols, row = rows[16 * a + row16];
-        if (row < 0) continue;
-        float v = 0.f;
-        if (16 * cb + j < rank) {
-          const int at = ((j & 15) + 16 * (row16 >> 2)) * 4 + (row16 & 3);
+      // four rows of one column a thread: what one lane of the product holds
+      for (int e = tid; e < 64 * CB; e += W * 64) {
+        const int c = cb + (e >> 6), l = e & 63, j = 16 * c + (l & 15), q4 = l >> 4;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (j < rank)
 #pragma unroll
-          for (int w = 0; w < W; ++w) v += red[w][j >> 4][at];
-          v *= scale;
-        }
-        P[(int64_t)row * p.r + 16 * cb + j] = v;
+          for (int w = 0; w < W; ++w) v += *reinterpret_cast<const f32x4*>(&red[w][e >> 6][l * 4]);
+        int rows[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) rows[q] = __shfl(row_of[a], 4 * q4 + q);
+        shrink_out<T>(p, P, v, rows, tile, sub * RT + a, c, l & 15, q4, rank, scale);
       }
     }
 }
@@ -374,102 +479,132 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64) void shrink_kernel(ShrinkArgs p)
 
 struct ExpandArgs {
   const float* P;       // [KS][n][r]
-  const void* W;        // [slots][C][r]
+  const void* W;        // [slots][C][r], or packed by rows
   const int32_t* rank;  // or null: r
   const float* scale;   // or null: 1
   const void* base;     // [n][ldb], or null: 0
   void* out;            // [n][ldo]
   float* H;             // [n][r] receives the sum over ks of P, or null
   int64_t ldb, ldo, C;
-  int32_t n, r, slots, KS, tiles, col_blocks;
+  int32_t n, r, slots, KS, tiles, col_blocks, sub, packed;   // sub: row blocks of 16 RT rows a tile is cut into
   Grouped g;
 };
 
 constexpr int EXPAND_COLS = 256;   // columns of a workgroup, 64 of each wave
 
-// One workgroup: a tile of 16 RT rows, 256 columns.  P is summed over its
+// One workgroup: 16 RT rows of a tile, 256 columns.  P is summed over its
 // slices, scaled and put in LDS once: in bf16 as two terms, hi + lo, so that
 // Y carries no rounding but its own; the extra product is cheap beside the
-// row traffic.  Weights stay in registers for the whole tile.  The weight is
-// the left operand, so a lane's results are consecutive columns of one row:
-// left row i of the two products of 32 columns is column 8 (i / 4) + 4 h + i % 4
-// (h the product), which makes one 16-byte piece of the row.
+// row traffic.  Weights stay in registers for all the rows.  A product leaves
+// 4 columns of one row in a lane; through LDS (wave by wave, no barrier) the
+// results come to lanes that hold 16 bytes of a row, 8 lanes to a 128-byte
+// line, the form in which base is read and the result written.
 template <typename T, int RT, int NK>
 __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
   constexpr bool BF = sizeof(T) == 2;
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, TERMS = BF ? 2 : 1;
   constexpr int PITCH = NK * KSTEP * (int)sizeof(T) + 16;   // bytes of a row in LDS; 16 more spread the banks
+  constexpr int DP = 68;                 // floats of a row of 64 results in LDS, likewise
+  constexpr int LPR = 64 / KPC;          // lanes to a row of 64 columns
+  constexpr int RPI = 64 / LPR, PIECES = 16 / RPI;   // rows of a load; loads for 16 rows
   __shared__ __attribute__((aligned(16))) char hs[TERMS * 16 * RT * PITCH];
-  __shared__ int rows[16 * RT];
+  __shared__ __attribute__((aligned(16))) float ds[4][16 * DP];
   const int id = xcd_tile_id(blockIdx.x, gridDim.x);
-  const Tile t = p.g.tiles[id / p.col_blocks];
-  const int cb = id % p.col_blocks;
-  if (t.count <= 0) return;
+  const int cb = id % p.col_blocks, part = id / p.col_blocks, sub = part % p.sub, tile = part / p.sub;
+  const Tile t = p.g.tiles[tile];
+  if (t.count <= sub * 16 * RT) return;
   const bool none = t.slot >= p.slots;
   if (none && p.base == p.out && p.ldb == p.ldo && !(p.H && cb == 0)) return;   // in place: nothing to add
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
-  if (tid < 16 * RT) rows[tid] = tile_row(p.g.perm, t, tid, p.n);
-  __syncthreads();
+  int row_of[RT];
+#pragma unroll
+  for (int a = 0; a < RT; ++a) row_of[a] = tile_row(p.g, tile, (sub * RT + a) * 16 + i, p.n);
   const int rank = none ? 0 : p.rank ? min(max(p.rank[t.slot], 0), p.r) : p.r;
   const int nk = (rank + KSTEP - 1) / KSTEP;
-  if (p.H && cb == 0)
-    for (int e = tid; e < 16 * RT * p.r; e += 256) {
-      const int row = rows[e / p.r], j = e % p.r;
-      if (row < 0) continue;
-      float v = 0.f;
-      if (j < rank)
-        for (int ks = 0; ks < p.KS; ++ks) v += p.P[((int64_t)ks * p.n + row) * p.r + j];
-      p.H[(int64_t)row * p.r + j] = v;
+  const float scale = none || !p.scale ? 1.f : p.scale[t.slot];
+  const int64_t c0 = (int64_t)cb * EXPAND_COLS + wave * 64;
+  // weights of the wave's 64 columns: 4 left operands per k-step
+  const int nks = (p.r + KSTEP - 1) / KSTEP;
+  uint4 wv[4][NK];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int64_t col = c0 + 16 * h + i;
+    const T* wr = reinterpret_cast<const T*>(p.W) +
+                  (p.packed ? (((int64_t)t.slot * ((p.C + 15) >> 4) + ((c0 >> 4) + h)) * nks * 64 + lane) * KPC
+                            : ((int64_t)t.slot * p.C + col) * p.r + g * KPC);
+    const int wstep = p.packed ? 64 * KPC : KSTEP;
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+      wv[h][k] = k < nk && col < p.C && k * KSTEP + g * KPC < rank
+                     ? *reinterpret_cast<const uint4*>(wr + k * wstep)
+                     : zero4();
+  }
+  // the rows of base, all in flight before the first is needed
+  const int lr = lane / LPR, lc = (lane % LPR) * KPC;
+  const int64_t mine = c0 + lc;
+  uint4 bv[RT][PIECES];
+  int rv[RT][PIECES];
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int row = __shfl(row_of[a], q * RPI + lr);
+      rv[a][q] = mine < p.C ? row : -1;
+      bv[a][q] = rv[a][q] >= 0 && p.base
+                     ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.base) + (int64_t)row * p.ldb + mine)
+                     : zero4();
     }
-  if (rank > 0) {
-    const float scale = p.scale ? p.scale[t.slot] : 1.f;
-    const int wide = nk * KSTEP / 4;   // groups of 4 rank columns, zero past the pool's r
-    for (int e = tid; e < 16 * RT * wide; e += 256) {
-      const int rr = e / wide, j = (e % wide) * 4, row = rows[rr];
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (row >= 0 && j < p.r)
-        for (int ks = 0; ks < p.KS; ++ks) {
-          const float4 u = *reinterpret_cast<const float4*>(p.P + ((int64_t)ks * p.n + row) * p.r + j);
-          v[0] += u.x;
-          v[1] += u.y;
-          v[2] += u.z;
-          v[3] += u.w;
-        }
+  // P: thread tid takes rank columns 4 (tid % 16), + 64, ... of row tid / 16 of each 16-row block
+  const bool keep_h = p.H && cb == 0;
+  if (rank > 0 || keep_h) {
+    const int wide = max(nk * KSTEP, keep_h ? p.r : 0) >> 2;   // groups of 4 rank columns, zero past the rank
+    const int rr = tid >> 4;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] *= scale;
-      if constexpr (BF) {
-        bf16_t hi[4], lo[4];
+    for (int a = 0; a < RT; ++a) {
+      const int row = __shfl(row_of[a], rr);   // lanes 0 .. 15 hold the block's rows
+      for (int jj = tid & 15; jj < wide; jj += 16) {
+        const int j = jj * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (row >= 0 && j < rank)
+          for (int ks = 0; ks < p.KS; ++ks) {
+            const float4 u = *reinterpret_cast<const float4*>(p.P + ((int64_t)ks * p.n + row) * p.r + j);
+            v[0] += u.x;
+            v[1] += u.y;
+            v[2] += u.z;
+            v[3] += u.w;
+          }
+        if (keep_h && row >= 0 && j < p.r)
+          *reinterpret_cast<float4*>(p.H + (int64_t)row * p.r + j) = make_float4(v[0], v[1], v[2], v[3]);
+        if (j >= nk * KSTEP) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float rest;
-          split2(v[q], hi[q], rest);
-          lo[q] = f2bf(rest);
+        for (int q = 0; q < 4; ++q) v[q] *= scale;
+        char* to = hs + (16 * a + rr) * PITCH + j * (int)sizeof(T);
+        if constexpr (BF) {
+          bf16_t hi[4], lo[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float rest;
+            split2(v[q], hi[q], rest);
+            lo[q] = f2bf(rest);
+          }
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+          *reinterpret_cast<uint2*>(to + 16 * RT * PITCH) =
+              make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+        } else {
+          *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
         }
-        *reinterpret_cast<uint2*>(hs + rr * PITCH + j * 2) =
-            make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
-        *reinterpret_cast<uint2*>(hs + (16 * RT + rr) * PITCH + j * 2) =
-            make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
-      } else {
-        *reinterpret_cast<float4*>(hs + rr * PITCH + j * 4) = make_float4(v[0], v[1], v[2], v[3]);
       }
     }
   }
   __syncthreads();
-  const int64_t c0 = (int64_t)cb * EXPAND_COLS + wave * 64;
   if (c0 >= p.C) return;
-  // weights of the wave's 64 columns: 4 left operands per k-step
-  uint4 wv[4][NK];
+  if (rank & (KPC - 1)) {   // what the pool holds past a rank that ends inside a chunk is not used
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int64_t col = BF ? c0 + 32 * (h >> 1) + 8 * (i >> 2) + 4 * (h & 1) + (i & 3) : c0 + 16 * h + i;
-    const T* wr = reinterpret_cast<const T*>(p.W) + ((int64_t)t.slot * p.C + col) * p.r;
+    for (int h = 0; h < 4; ++h)
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const int j = k * KSTEP + g * KPC;
-      uint4 v = zero4();
-      if (k < nk && col < p.C && j < rank) {
-        v = *reinterpret_cast<const uint4*>(wr + j);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};   // what the pool holds past the rank is not used
+      for (int k = 0; k < NK; ++k) {
+        const int j = k * KSTEP + g * KPC;
+        uint32_t w[4] = {wv[h][k].x, wv[h][k].y, wv[h][k].z, wv[h][k].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (BF) {
@@ -479,35 +614,14 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
             if (j + q >= rank) w[q] = 0u;
           }
         }
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        wv[h][k] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      wv[h][k] = v;
-    }
   }
-  constexpr int PIECES = BF ? 2 : 4;   // 16-byte pieces of a row a lane holds: columns 32 a + 8 g, or 16 a + 4 g
+  float* d = ds[wave];
 #pragma unroll
   for (int a = 0; a < RT; ++a) {
-    if (16 * a >= t.count) break;
-    const int row = rows[16 * a + i];
-    uint4 bv[PIECES];
-#pragma unroll
-    for (int q = 0; q < PIECES; ++q) {
-      const int64_t col = c0 + q * (4 * KPC) + g * KPC;
-      bv[q] = row >= 0 && col < p.C && p.base
-                  ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.base) + (int64_t)row * p.ldb + col)
-                  : zero4();
-    }
-    f32x4 acc[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      if constexpr (BF) {
-        const uint32_t w0 = h & 1 ? bv[h >> 1].z : bv[h >> 1].x, w1 = h & 1 ? bv[h >> 1].w : bv[h >> 1].y;
-        acc[h] = f32x4{__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
-                       __uint_as_float(w1 & 0xffff0000u)};
-      } else {
-        acc[h] = __builtin_bit_cast(f32x4, bv[h]);
-      }
-    }
+    if ((sub * RT + a) * 16 >= t.count) break;
+    f32x4 acc[4] = {};
 #pragma unroll
     for (int k = 0; k < NK; ++k)
       if (k < nk) {
@@ -519,21 +633,31 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
           for (int h = 0; h < 4; ++h) Step<T>::mma(acc[h], wv[h][k], hv);
         }
       }
-    if (row < 0) continue;
+    // columns 16 h + 4 g .. + 3 of row i
+#pragma unroll
+    for (int h = 0; h < 4; ++h) *reinterpret_cast<f32x4*>(d + i * DP + 16 * h + 4 * g) = acc[h];
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
-      const int64_t col = c0 + q * (4 * KPC) + g * KPC;
-      if (col >= p.C) continue;
+      const float* s = d + (q * RPI + lr) * DP + lc;
+      const uint4& b = bv[a][q];
       uint4 o;
       if constexpr (BF) {
-        auto pair = [](float a, float b) { return (uint32_t)f2bf(a) | (uint32_t)f2bf(b) << 16; };
-        o = make_uint4(pair(acc[2 * q][0], acc[2 * q][1]), pair(acc[2 * q][2], acc[2 * q][3]),
-                       pair(acc[2 * q + 1][0], acc[2 * q + 1][1]), pair(acc[2 * q + 1][2], acc[2 * q + 1][3]));
+        const float4 u = *reinterpret_cast<const float4*>(s), w = *reinterpret_cast<const float4*>(s + 4);
+        auto pair = [](uint32_t x, float lo, float hi) {
+          return (uint32_t)f2bf(__uint_as_float(x << 16) + lo) |
+                 (uint32_t)f2bf(__uint_as_float(x & 0xffff0000u) + hi) << 16;
+        };
+        o = make_uint4(pair(b.x, u.x, u.y), pair(b.y, u.z, u.w), pair(b.z, w.x, w.y), pair(b.w, w.z, w.w));
       } else {
-        o = __builtin_bit_cast(uint4, acc[q]);
+        const float4 u = *reinterpret_cast<const float4*>(s);
+        o = make_uint4(__float_as_uint(__uint_as_float(b.x) + u.x), __float_as_uint(__uint_as_float(b.y) + u.y),
+                       __float_as_uint(__uint_as_float(b.z) + u.z), __float_as_uint(__uint_as_float(b.w) + u.w));
       }
-      *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (int64_t)row * p.ldo + col) = o;
+      if (rv[a][q] >= 0)
+        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (int64_t)rv[a][q] * p.ldo + mine) = o;
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -544,126 +668,137 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
 
 struct GradSide {
   const void* V;       // [n][ldv]
-  const float* P;      // [KS][n][r]
-  const float* scale;  // or null: 1
+  const void* Pf;      // left operands, written by the shrink
   float* part;         // [chunk_cap][r][C]
   int64_t ldv, C;
-  int32_t KS, col_blocks;
+  int32_t col_blocks;
 };
 struct GradArgs {
   GradSide side[2];
   const int32_t* rank;
   int32_t n, r, slots, chunk_cap, r_groups;
-  Grouped g;
+  Grouped g;           // tiles of 64 rows
 };
 
-constexpr int GRAD_TOK = 64;                  // rows staged together
 template <typename T> constexpr int grad_cols() { return sizeof(T) == 2 ? 128 : 64; }   // columns of a wave
 
-// One workgroup: a chunk of rows, 4 waves' columns, up to 16 CT rank columns.
-// The row factor (P) goes through LDS, rank-major and, for bf16 V, as three
-// bf16 terms (hi + mid + lo, 2^-27 relative: the gradients are fp32, and V is
-// exact in bf16).  V is read 8 rows by 8 columns per lane and transposed in
-// registers, so that each lane holds 8 consecutive rows of a column, the
-// reduction axis; operand e of a lane is column 8 i + e of the wave's 128.
+// One workgroup: a chunk of tiles, 4 waves' columns, up to 16 CT rank columns.
+// V is read 8 rows by 16 bytes per lane; bf16 is transposed in registers, so
+// that each lane holds 8 consecutive rows of a column, the reduction axis
+// (operand e of a lane is column 8 i + e of the wave's 128); fp32 products
+// take one row of each lane group as it is.  The row factors are operands
+// already; the four waves share them through LDS, a half tile at a time,
+// double-buffered.  Both are in flight a half tile ahead of the products.
 template <typename T, int CT>
-__global__ __launch_bounds__(256) void grad_kernel(GradArgs p) {
+__global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
   constexpr bool BF = sizeof(T) == 2;
-  constexpr int TERMS = BF ? 3 : 1, COLS = grad_cols<T>();
-  // bf16: [term][16 CT][GRAD_TOK + 8]; fp32: [GRAD_TOK][16 CT + 4]
-  constexpr int PITCH = BF ? GRAD_TOK + 8 : 16 * CT + 4;
-  __shared__ __attribute__((aligned(16))) T ps[BF ? TERMS * 16 * CT * PITCH : GRAD_TOK * PITCH];
-  __shared__ int rows[GRAD_TOK];
+  constexpr int COLS = grad_cols<T>(), PARTS = grad_parts<T>(), BYTES = CT * PARTS * 1024;
+  constexpr int NA = (BYTES / 16 + 255) / 256;   // 16-byte loads of a thread for a half tile's operands
+  __shared__ __attribute__((aligned(16))) char lds[2][BYTES];
   int id = blockIdx.x;
   const int per0 = p.side[0].col_blocks * p.r_groups * p.chunk_cap;
   const int which = id >= per0;
   id -= which ? per0 : 0;
   const GradSide& v = p.side[which];
-  const int cb = id % v.col_blocks, chunk = id / v.col_blocks % p.chunk_cap, rg = id / v.col_blocks / p.chunk_cap;
-  const Tile t = p.g.chunks[chunk];
-  if (t.count <= 0 || t.slot >= p.slots) return;
+  // the shrink before this kernel read V of side 0 from the first row to the
+  // last: going back from the last finds the most of it in the Infinity Cache
+  const int cb = id % v.col_blocks, chunk = p.chunk_cap - 1 - id / v.col_blocks % p.chunk_cap;
+  const int rg = id / v.col_blocks / p.chunk_cap;
+  const Chunk t = p.g.chunks[chunk];
+  if (t.tiles <= 0 || t.slot >= p.slots) return;
   const int rank = p.rank ? min(max(p.rank[t.slot], 0), p.r) : p.r;
   const int j0 = rg * 16 * CT;
   if (j0 >= rank) return;
-  const int nct = min((rank - j0 + 15) >> 4, CT);
-  const float scale = v.scale ? v.scale[t.slot] : 1.f;
+  const int nct = min((rank - j0 + 15) >> 4, CT), cts = (p.r + 15) >> 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t c0 = ((int64_t)cb * 4 + wave) * COLS, col = c0 + i * (COLS / 16);
-  const bool live = col < v.C;
   constexpr int E = COLS / 16;   // columns of a lane
+  const int64_t col = ((int64_t)cb * 4 + wave) * COLS + i * E;
+  const bool live = col < v.C;
+  const T* V = reinterpret_cast<const T*>(v.V) + col;
   f32x4 acc[CT][E] = {};
-  for (int p0 = 0; p0 < t.count; p0 += GRAD_TOK) {
-    __syncthreads();
-    if (tid < GRAD_TOK) rows[tid] = tile_row(p.g.perm, t, p0 + tid, p.n);
-    __syncthreads();
-    // P of the staged rows: one unit is 8 rows of one rank column
-    for (int u = tid; u < GRAD_TOK / 8 * 16 * CT; u += 256) {
-      const int j = u % (16 * CT), tok = u / (16 * CT) * 8;
-      float f[8];
+  // the second half of the last tile has no operands if it has no row
+  const int last_count = p.g.tiles[t.first + t.tiles - 1].count;
+  const int halves = t.tiles * 2 - (last_count <= 32 ? 1 : 0);
+  const int* perm = p.g.perm + (int64_t)t.first * GRAD_TILE + 8 * g;
+  const char* ops = grad_block<T>(v.Pf, (int64_t)t.first * 2, j0 >> 4, cts) + tid * 16;
+  const int bytes = nct * PARTS * 1024;
+
+  auto load_rows = [&](int (&rows)[8], int h) {
+    const int4* s = reinterpret_cast<const int4*>(perm + (int64_t)min(h, halves - 1) * 32);
+    const int4 a = s[0], b = s[1];
+    rows[0] = a.x, rows[1] = a.y, rows[2] = a.z, rows[3] = a.w;
+    rows[4] = b.x, rows[5] = b.y, rows[6] = b.z, rows[7] = b.w;
+  };
+  auto load_v = [&](uint4(&in)[8], const int (&rows)[8], int h) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int row = rows[tok + q];
-        f[q] = 0.f;
-        if (row >= 0 && j0 + j < rank)
-          for (int ks = 0; ks < v.KS; ++ks) f[q] += v.P[((int64_t)ks * p.n + row) * p.r + j0 + j];
-        f[q] *= scale;
-      }
-      if constexpr (BF) {
+    for (int e = 0; e < 8; ++e)
+      in[e] = h < halves && live && (unsigned)rows[e] < (unsigned)p.n
+                  ? *reinterpret_cast<const uint4*>(V + (int64_t)rows[e] * v.ldv)
+                  : zero4();
+  };
+  auto load_a = [&](uint4(&a)[NA], int h) {
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          bf16_t h[8];
+    for (int n = 0; n < NA; ++n)
+      a[n] = h < halves && tid * 16 + n * 4096 < bytes
+                 ? *reinterpret_cast<const uint4*>(ops + (int64_t)h * cts * (PARTS * 1024) + n * 4096)
+                 : zero4();
+  };
+  auto put_a = [&](const uint4(&a)[NA], int h) {
+#pragma unroll
+    for (int n = 0; n < NA; ++n)
+      if (tid * 16 + n * 4096 < bytes) *reinterpret_cast<uint4*>(&lds[h & 1][tid * 16 + n * 4096]) = a[n];
+  };
+  auto mul = [&](const uint4(&in)[8], int h) {
+    const char* a = &lds[h & 1][lane * 16];
+    if constexpr (BF) {
+      uint4 b[8];
+      transpose8x8_b16(in, b);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        if (c < nct)
+#pragma unroll
+          for (int u = 0; u < PARTS; ++u) {
+            const uint4 w = *reinterpret_cast<const uint4*>(a + (c * PARTS + u) * 1024);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mma16(acc[c][e], w, b[e]);
+          }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        if (c < nct)
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            float rest;
-            split2(f[q], h[q], rest);
-            f[q] = rest;
+            const float w = *reinterpret_cast<const float*>(a + (c * PARTS + (q >> 2)) * 1024 + (q & 3) * 4);
+            acc[c][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, __uint_as_float(in[q].x), acc[c][0], 0, 0, 0);
+            acc[c][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, __uint_as_float(in[q].y), acc[c][1], 0, 0, 0);
+            acc[c][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, __uint_as_float(in[q].z), acc[c][2], 0, 0, 0);
+            acc[c][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, __uint_as_float(in[q].w), acc[c][3], 0, 0, 0);
           }
-          *reinterpret_cast<uint4*>(&ps[(term * 16 * CT + j) * PITCH + tok]) =
-              make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
-                         h[6] | (uint32_t)h[7] << 16);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) ps[(tok + q) * PITCH + j] = f[q];
-      }
     }
+  };
+
+  uint4 even[8], odd[8], a[NA];
+  int rows[8];
+  load_rows(rows, 0);
+  load_a(a, 0);
+  load_v(even, rows, 0);
+  load_rows(rows, 1);
+  put_a(a, 0);
+  __syncthreads();
+  for (int h = 0; h < halves; h += 2) {
+    load_a(a, h + 1);
+    load_v(odd, rows, h + 1);
+    load_rows(rows, h + 2);
+    mul(even, h);
+    put_a(a, h + 1);
     __syncthreads();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {   // 32 rows each
-      uint4 in[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // bf16: rows 8 g + e; fp32: rows 4 e + g (one product per element of the chunk, four rows each)
-        const int row = rows[half * 32 + (BF ? 8 * g + e : 4 * e + g)];
-        in[e] = row >= 0 && live
-                    ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(v.V) + (int64_t)row * v.ldv + col)
-                    : zero4();
-      }
-      if constexpr (BF) {
-        uint4 b[8];
-        transpose8x8_b16(in, b);
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          if (c < nct)
-#pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              const uint4 a = *reinterpret_cast<const uint4*>(&ps[(term * 16 * CT + 16 * c + i) * PITCH + half * 32 + 8 * g]);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) mma16(acc[c][e], a, b[e]);
-            }
-      } else {
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-            if (c < nct) {
-              const float a = ps[(half * 32 + 4 * s + g) * PITCH + 16 * c + i];
-              acc[c][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, __uint_as_float(in[s].x), acc[c][0], 0, 0, 0);
-              acc[c][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, __uint_as_float(in[s].y), acc[c][1], 0, 0, 0);
-              acc[c][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, __uint_as_float(in[s].z), acc[c][2], 0, 0, 0);
-              acc[c][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, __uint_as_float(in[s].w), acc[c][3], 0, 0, 0);
-            }
-      }
+    if (h + 1 < halves) {
+      load_a(a, h + 2);
+      load_v(even, rows, h + 2);
+      load_rows(rows, h + 3);
+      mul(odd, h + 1);
+      put_a(a, h + 2);
+      __syncthreads();
     }
   }
   if (!live) return;
@@ -683,9 +818,9 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs p) {
 
 // Sums the chunks of each slot in order: dA[s][j][c], and dB[s][c][j]
 // (transposed through LDS).  Rows past a slot's rank, and slots without rows,
-// are zero.  One workgroup: 64 columns and 64 rank columns of one slot.
+// are zero.  One workgroup: 64 columns and 16 rank columns of one slot.
 struct JoinArgs {
-  const float* part[2];
+  const float* part[2];   // dB's, dA's
   float* out[2];
   int64_t C[2];
   int32_t blocks[2];
@@ -695,35 +830,41 @@ struct JoinArgs {
 };
 
 __global__ __launch_bounds__(256) void grad_join_kernel(JoinArgs p) {
-  __shared__ float buf[64][65];
+  __shared__ float buf[16][68];
   int id = blockIdx.x;
   const int which = id >= p.blocks[0];
   id -= which ? p.blocks[0] : 0;
   const int64_t C = p.C[which];
-  const int cbs = (int)cdiv64(C, 64), rbs = (p.r + 63) >> 6;
+  const int cbs = (int)cdiv64(C, 64), rbs = (p.r + 15) >> 4;
   const int cb = id % cbs, rb = id / cbs % rbs, slot = id / cbs / rbs;
   const int rank = p.rank ? min(max(p.rank[slot], 0), p.r) : p.r;
   const int lo = min(max(p.g.slot_chunk[slot], 0), p.chunk_cap), hi = min(p.g.slot_chunk[slot + 1], p.chunk_cap);
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  const int64_t c = (int64_t)cb * 64 + x;
-  const int64_t step = (int64_t)p.r * C;
-  for (int jj = y; jj < 64; jj += 4) {
-    const int j = rb * 64 + jj;
-    float v = 0.f;
-    if (j < rank && c < C) {
-      const float* s = p.part[which] + (int64_t)lo * step + (int64_t)j * C + c;
-      for (int k = lo; k < hi; ++k, s += step) v += *s;
+  const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4, j = rb * 16 + y;
+  const int64_t c = (int64_t)cb * 64 + x, step = (int64_t)p.r * C;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (j < rank && c < C) {
+    const float* s = p.part[which] + (int64_t)lo * step + (int64_t)j * C + c;
+#pragma unroll 8
+    for (int k = lo; k < hi; ++k, s += step) {
+      const float4 u = *reinterpret_cast<const float4*>(s);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
     }
-    if (which) buf[jj][x] = v;
-    else if (j < p.r && c < C) p.out[0][((int64_t)slot * p.r + j) * C + c] = v;
   }
-  if (!which) return;
+  if (which) {
+    if (j < p.r && c < C) *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
+    return;
+  }
+  *reinterpret_cast<float4*>(&buf[y][x]) = v;
   __syncthreads();
-  for (int cc = y; cc < 64; cc += 4) {
-    const int64_t oc = (int64_t)cb * 64 + cc;
-    const int j = rb * 64 + x;
-    if (oc < C && j < p.r) p.out[1][((int64_t)slot * C + oc) * p.r + j] = buf[x][cc];
-  }
+  // 4 rank columns of a column a thread
+  const int cc = threadIdx.x >> 2, j4 = (threadIdx.x & 3) * 4;
+  const int64_t oc = (int64_t)cb * 64 + cc;
+  if (oc < C && rb * 16 + j4 < p.r)
+    *reinterpret_cast<float4*>(p.out[0] + ((int64_t)slot * C + oc) * p.r + rb * 16 + j4) =
+        make_float4(buf[j4][cc], buf[j4 + 1][cc], buf[j4 + 2][cc], buf[j4 + 3][cc]);
 }
 
 // ---------------------------------------------------------------------------
@@ -732,11 +873,12 @@ __global__ __launch_bounds__(256) void grad_join_kernel(JoinArgs p) {
 
 // Sizes of a call: tile heights, splits and the workspace.
 struct Plan {
-  int tile, rt, sub;                // rows of a tile; 16-row blocks of a shrink workgroup; those per tile
-  int ks1, ks2;                     // slices of c1 (forward) / c2 (backward) in the shrink
-  int chunk;                        // rows of a gradient chunk (backward), else 0
+  int tile, rt, sub, ert;           // rows of a tile; 16-row blocks of a shrink workgroup, those per tile; of an expand one
+  int ks;                           // slices of the reduction in the shrink
+  int chunk;                        // tiles of a gradient chunk (backward), else 0
+  int packed;                       // weights are packed first
   int64_t tile_cap, chunk_cap;
-  size_t perm, tiles, chunks, slot_chunk, P, At, Bt, partA, partB, total;
+  size_t perm, tiles, chunks, slot_chunk, P, Ws, We, Pf, Hf, partA, partB, total;
 };
 
 int shrink_split(int64_t wgs, int64_t K, int dtype) {
@@ -748,34 +890,41 @@ int shrink_split(int64_t wgs, int64_t K, int dtype) {
 
 Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int64_t B, int dtype, bool backward) {
   Plan q{};
-  q.tile = n <= 512 ? 16 : 64;
-  q.rt = n <= 512 ? 1 : 2;
+  const bool small = n <= 512 && !backward;
+  q.tile = small ? 16 : GRAD_TILE;
+  q.rt = r > 32 && n >= 8192 ? 2 : 1;   // a weight operand serves RT blocks of 16 rows; 256 workgroups first
   q.sub = q.tile / (16 * q.rt);
+  q.ert = small ? 1 : 2;   // 2 against 1 and 4: 109, 114 and 113 us at 32928 x 4096, 19, 18 and 21 at 4099 x 4096
   const int64_t used = std::min(slots + 1, B + 1);   // slots with rows, "no adapter" among them
   q.tile_cap = n / q.tile + used + 1;
+  q.packed = backward || (n > 512 && n >= 64 * std::min(slots, B));
   const int64_t wgs = std::max<int64_t>(1, cdiv64(n, 16 * q.rt));
-  q.ks1 = shrink_split(wgs, c1, dtype);
-  q.ks2 = shrink_split(wgs, c2, dtype);
+  q.ks = backward ? 1 : shrink_split(wgs, c1, dtype);
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
     const size_t here = at;
     at += align256((size_t)bytes);
     return here;
   };
-  q.perm = take(4 * n);
+  q.perm = take(4 * q.tile_cap * q.tile);
   q.tiles = take((int64_t)sizeof(Tile) * q.tile_cap);
-  q.P = take(4 * n * r * (backward ? q.ks2 : q.ks1));
+  q.P = take(4 * n * r * q.ks);
+  if (q.packed) {
+    const int64_t kstep = dtype == DYRA_BF16 ? 32 : 16, kin = backward ? c2 : c1, kout = backward ? c1 : c2;
+    q.Ws = take(slots * cdiv64(r, 16) * cdiv64(kin, kstep) * 1024);
+    q.We = take(slots * cdiv64(kout, 16) * cdiv64(r, kstep) * 1024);
+  }
   if (backward) {
     const int cols = 4 * (dtype == DYRA_BF16 ? grad_cols<bf16_t>() : grad_cols<float>());
+    const int parts = dtype == DYRA_BF16 ? grad_parts<bf16_t>() : grad_parts<float>();
     const int64_t blocks = cdiv64(c1, cols) + cdiv64(c2, cols);
-    const int64_t chunks = std::max<int64_t>(1, 512 / blocks);
-    q.chunk = (int)std::max<int64_t>(GRAD_TOK, cdiv64(cdiv64(n, chunks), GRAD_TOK) * GRAD_TOK);
-    q.chunk_cap = n / q.chunk + std::min(slots, B) + 1;
-    q.chunks = take((int64_t)sizeof(Tile) * q.chunk_cap);
+    const int64_t most = std::max<int64_t>(1, 512 / blocks), chunks = std::max((most + 1) / 2, most - std::min(slots, B));
+    q.chunk = (int)std::max<int64_t>(1, cdiv64(cdiv64(n, GRAD_TILE), chunks));
+    q.chunk_cap = n / ((int64_t)q.chunk * GRAD_TILE) + std::min(slots, B) + 1;
+    q.chunks = take((int64_t)sizeof(Chunk) * q.chunk_cap);
     q.slot_chunk = take(4 * (slots + 1));
-    const int64_t esz = (int64_t)elem_bytes(dtype);
-    q.At = take(slots * r * c1 * esz);
-    q.Bt = take(slots * r * c2 * esz);
+    q.Pf = take(q.tile_cap * 2 * cdiv64(r, 16) * parts * 1024);
+    q.Hf = take(q.tile_cap * 2 * cdiv64(r, 16) * parts * 1024);
     q.partA = take(4 * q.chunk_cap * r * c1);
     q.partB = take(4 * q.chunk_cap * r * c2);
   }
@@ -801,7 +950,7 @@ Grouped grouped(const Plan& q, char* ws) {
   Grouped g{};
   g.perm = reinterpret_cast<int32_t*>(ws + q.perm);
   g.tiles = reinterpret_cast<Tile*>(ws + q.tiles);
-  g.chunks = reinterpret_cast<Tile*>(ws + q.chunks);
+  g.chunks = reinterpret_cast<Chunk*>(ws + q.chunks);
   g.slot_chunk = reinterpret_cast<int32_t*>(ws + q.slot_chunk);
   g.tile = q.tile;
   g.chunk = q.chunk;
@@ -810,14 +959,19 @@ Grouped grouped(const Plan& q, char* ws) {
   return g;
 }
 
-template <typename E>
-void launch_group(const Requests& rq, const Grouped& g, const Transpose<E>& ta, const Transpose<E>& tb,
-                  hipStream_t st) {
+template <typename T>
+Pack<T> pack_job(const void* src, void* dst, int64_t rows, int64_t ks, bool across, bool by_k) {
+  Pack<T> j{reinterpret_cast<const T*>(src), reinterpret_cast<T*>(dst), (int32_t)rows, (int32_t)ks, across, by_k, 0};
+  j.wgs = (int32_t)cdiv64(j.blocks(), PACK_BLOCKS);
+  return j;
+}
+
+template <typename T>
+void launch_group(const Requests& rq, const Grouped& g, const Pack<T>& a, const Pack<T>& b, hipStream_t st) {
   const int wgs = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv64(rq.n, 2 * GROUP_NT), 64));
-  const int64_t a = ta.src ? (int64_t)rq.slots * ta.tiles_r * ta.tiles_c : 0;
-  const int64_t b = tb.src ? (int64_t)rq.slots * tb.tiles_r * tb.tiles_c : 0;
-  hipLaunchKernelGGL((group_kernel<E>), dim3((unsigned)(wgs + a + b)), dim3(GROUP_NT), 0, st, rq, g, wgs, ta, tb,
-                     (int)a);
+  const int64_t na = a.src ? (int64_t)rq.slots * a.wgs : 0, nb = b.src ? (int64_t)rq.slots * b.wgs : 0;
+  hipLaunchKernelGGL((group_kernel<T>), dim3((unsigned)(wgs + na + nb)), dim3(GROUP_NT), 0, st, rq, g, wgs, a, b,
+                     (int)na);
 }
 
 template <typename T, int RT>
@@ -846,26 +1000,41 @@ void launch_expand_rt(const ExpandArgs& a, unsigned grid, hipStream_t st) {
 }
 
 template <typename T>
-void launch_expand(const ExpandArgs& a, int tile, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.tiles * a.col_blocks);
-  if (tile == 16) launch_expand_rt<T, 1>(a, grid, st);
-  else launch_expand_rt<T, 4>(a, grid, st);
+void launch_expand(const ExpandArgs& a, int ert, hipStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)a.tiles * a.sub * a.col_blocks);
+  if (ert == 1) launch_expand_rt<T, 1>(a, grid, st);
+  else launch_expand_rt<T, 2>(a, grid, st);
 }
 
 template <typename T>
 int forward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const void* base, int64_t ldb, void* Y,
                  int64_t ldy, float* H, const Requests& rq, const Plan& q, char* ws, hipStream_t st) {
   const Grouped g = grouped(q, ws);
-  const Transpose<T> no{};
-  launch_group<T>(rq, g, no, no, st);
+  const void *Ws = ad.A, *We = ad.B;
+  Pack<T> pa{}, pb{};
+  if (q.packed) {
+    pa = pack_job<T>(ad.A, ws + q.Ws, ad.r, ad.c1, false, true);
+    pb = pack_job<T>(ad.B, ws + q.We, ad.c2, ad.r, false, false);
+    Ws = pa.dst;
+    We = pb.dst;
+  }
+  launch_group<T>(rq, g, pa, pb, st);
   // with one slice the shrink writes H itself
-  float* P = H && q.ks1 == 1 ? H : reinterpret_cast<float*>(ws + q.P);
-  const ShrinkArgs sa{X, ad.A, ad.rank, nullptr, P, ldx, ad.c1, rq.n, ad.r, ad.slots, q.sub, (int32_t)q.tile_cap, q.ks1, g};
+  float* P = H && q.ks == 1 ? H : reinterpret_cast<float*>(ws + q.P);
+  const ShrinkArgs sa{X,     Ws,   ad.rank, nullptr,  P,     nullptr,             nullptr, nullptr,  ldx,
+                      ad.c1, rq.n, ad.r,    ad.slots, q.sub, (int32_t)q.tile_cap, q.ks,    q.packed, g};
   launch_shrink<T>(sa, q.rt, st);
-  const ExpandArgs ea{P,      ad.B, ad.rank, ad.scale, base,  Y,
-                      P == H ? nullptr : H, ldb, ldy, ad.c2, rq.n, ad.r, ad.slots, q.ks1, (int32_t)q.tile_cap,
-                      (int32_t)cdiv64(ad.c2, EXPAND_COLS), g};
-  launch_expand<T>(ea, q.tile, st);
+  const ExpandArgs ea{P,       We,
+                      ad.rank, ad.scale,
+                      base,    Y,
+                      P == H ? nullptr : H, ldb,
+                      ldy,     ad.c2,
+                      rq.n,    ad.r,
+                      ad.slots, q.ks,
+                      (int32_t)q.tile_cap, (int32_t)cdiv64(ad.c2, EXPAND_COLS),
+                      q.tile / (16 * q.ert), q.packed,
+                      g};
+  launch_expand<T>(ea, q.ert, st);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
@@ -881,51 +1050,58 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
                   const void* dXb, int64_t lddb, void* dX, int64_t lddx, float* dA, float* dB, const Requests& rq,
                   const Plan& q, char* ws, hipStream_t st) {
   const Grouped g = grouped(q, ws);
-  T* At = reinterpret_cast<T*>(ws + q.At);
-  T* Bt = reinterpret_cast<T*>(ws + q.Bt);
-  const auto blocks = [](int64_t v) { return (int32_t)cdiv64(v, TR); };
-  const Transpose<T> ta{dX ? reinterpret_cast<const T*>(ad.A) : nullptr, At, ad.r, (int32_t)ad.c1, blocks(ad.r),
-                        blocks(ad.c1)};
-  const Transpose<T> tb{reinterpret_cast<const T*>(ad.B), Bt, (int32_t)ad.c2, ad.r, blocks(ad.c2), blocks(ad.r)};
-  launch_group<T>(rq, g, ta, tb, st);
+  const Pack<T> pb = pack_job<T>(ad.B, ws + q.Ws, ad.r, ad.c2, true, true);
+  const Pack<T> pa = pack_job<T>(dX ? ad.A : nullptr, ws + q.We, ad.c1, ad.r, true, false);
+  launch_group<T>(rq, g, pb, pa, st);
   float* P = reinterpret_cast<float*>(ws + q.P);
   if (rq.n) {
-    const ShrinkArgs sa{dY, Bt, ad.rank, ad.scale, P, lddy, ad.c2, rq.n, ad.r, ad.slots, q.sub, (int32_t)q.tile_cap, q.ks2, g};
+    const ShrinkArgs sa{dY,      pb.dst, ad.rank, ad.scale, P,     dA ? H : nullptr,    dA ? ws + q.Pf : nullptr,
+                        dA ? ws + q.Hf : nullptr,  lddy,
+                        ad.c2,   rq.n,   ad.r,    ad.slots, q.sub, (int32_t)q.tile_cap, 1,
+                        1,       g};
     launch_shrink<T>(sa, q.rt, st);
   }
-  if (dX && rq.n) {
-    const ExpandArgs ea{P, At, ad.rank, nullptr, dXb, dX, nullptr, lddb, lddx, ad.c1, rq.n, ad.r, ad.slots, q.ks2,
-                        (int32_t)q.tile_cap, (int32_t)cdiv64(ad.c1, EXPAND_COLS), g};
-    launch_expand<T>(ea, q.tile, st);
-  }
   if (dA) {
-    float *pa = reinterpret_cast<float*>(ws + q.partA), *pb = reinterpret_cast<float*>(ws + q.partB);
+    float *pdA = reinterpret_cast<float*>(ws + q.partA), *pdB = reinterpret_cast<float*>(ws + q.partB);
     const int cols = 4 * grad_cols<T>();
     if (rq.n) {
-      GradArgs ga{{{X, P, nullptr, pa, ldx, ad.c1, q.ks2, (int32_t)cdiv64(ad.c1, cols)},
-                   {dY, H, ad.scale, pb, lddy, ad.c2, 1, (int32_t)cdiv64(ad.c2, cols)}},
+      GradArgs ga{{{dY, ws + q.Hf, pdB, lddy, ad.c2, (int32_t)cdiv64(ad.c2, cols)},
+                   {X, ws + q.Pf, pdA, ldx, ad.c1, (int32_t)cdiv64(ad.c1, cols)}},
                   ad.rank, rq.n, ad.r, ad.slots, (int32_t)q.chunk_cap, 1, g};
       if (ad.r <= 16) launch_grad<T, 1>(ga, st);
       else if (ad.r <= 32) launch_grad<T, 2>(ga, st);
       else launch_grad<T, 4>(ga, st);
     }
-    const int64_t rbs = cdiv64(ad.r, 64);
-    const int64_t b0 = cdiv64(ad.c1, 64) * rbs * ad.slots, b1 = cdiv64(ad.c2, 64) * rbs * ad.slots;
-    const JoinArgs ja{{pa, pb}, {dA, dB}, {ad.c1, ad.c2}, {(int32_t)b0, (int32_t)b1}, ad.rank, ad.r, ad.slots,
+    const int64_t rbs = cdiv64(ad.r, 16);
+    const int64_t b0 = cdiv64(ad.c2, 64) * rbs * ad.slots, b1 = cdiv64(ad.c1, 64) * rbs * ad.slots;
+    const JoinArgs ja{{pdB, pdA}, {dB, dA}, {ad.c2, ad.c1}, {(int32_t)b0, (int32_t)b1}, ad.rank, ad.r, ad.slots,
                       (int32_t)q.chunk_cap, g};
     hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(b0 + b1)), dim3(256), 0, st, ja);
+  }
+  if (dX && rq.n) {
+    const ExpandArgs ea{P,       pa.dst,
+                        ad.rank, nullptr,
+                        dXb,     dX,
+                        nullptr, lddb,
+                        lddx,    ad.c1,
+                        rq.n,    ad.r,
+                        ad.slots, 1,
+                        (int32_t)q.tile_cap, (int32_t)cdiv64(ad.c1, EXPAND_COLS),
+                        q.tile / (16 * q.ert), 1,
+                        g};
+    launch_expand<T>(ea, q.ert, st);
   }
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
 // every grid of a call fits a launch
 bool grids_fit(const dyra_adapters& ad, const Plan& q, bool backward) {
-  const int64_t most = INT_MAX;
-  const int64_t c = std::max(ad.c1, ad.c2);
-  if (q.tile_cap * q.sub * std::max(q.ks1, q.ks2) > most || q.tile_cap * cdiv64(c, EXPAND_COLS) > most) return false;
+  const int64_t most = INT_MAX, c = std::max(ad.c1, ad.c2);
+  const int64_t packs = (cdiv64(ad.c1, 16) + cdiv64(ad.c2, 16)) * cdiv64(ad.r, 16) / PACK_BLOCKS + 2;
+  if (q.tile_cap * q.sub * q.ks > most || q.tile_cap * 4 * cdiv64(c, EXPAND_COLS) > most) return false;
+  if (q.packed && packs * ad.slots + 64 > most) return false;
   if (!backward) return true;
-  const int64_t rbs = cdiv64(ad.r, TR);
-  return (cdiv64(ad.c1, TR) + cdiv64(ad.c2, TR)) * rbs * ad.slots + 64 <= most &&
+  return (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots <= most &&
          (cdiv64(ad.c1, 256) + cdiv64(ad.c2, 256)) * 2 * q.chunk_cap <= most;
 }
 
