@@ -25,6 +25,7 @@ Tensors (GPU, bf16 or fp32, one type throughout):
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -34,31 +35,8 @@ MAX_SLOTS = 2048   # DYRA_ADAPTER_MAX_SLOTS
 _DTYPES = {torch.bfloat16: D.DT_BF16, torch.float32: D.DT_F32}
 
 
-def _rows(t, name, n, c, dtype, device):
-    """Pointer and row stride of an [n][c] operand whose rows are dense."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    if t.shape != (n, c):
-        raise ValueError(f"{name} must have shape {(n, c)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not n:
-        return None, c
-    ld, one = t.stride()
-    p = t.data_ptr()
-    if n == 1:
-        ld = c
-    if (one != 1 and c > 1) or ld < c or (ld * t.element_size() | p) & 15:
-        raise ValueError(f"{name}: rows must be dense, 16-byte aligned and not overlapping (strides {t.stride()})")
-    return p, ld
-
-
-def _flat(t, name, shape, dtype, device):
-    """Pointer of a contiguous tensor of exactly this shape, or None."""
-    if t is None:
-        return None
+def _expect(t, name, shape, dtype, device):
+    """Raises ValueError unless t is a tensor of this shape and type on device."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.shape != shape:
@@ -67,6 +45,31 @@ def _flat(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows(t, name, n, c, dtype, device):
+    """Pointer and row stride of an [n][c] operand whose rows are dense."""
+    _expect(t, name, (n, c), dtype, device)
+    p = t.data_ptr()
+    if t.is_contiguous():
+        ld = c
+    else:
+        ld, one = t.stride()
+        if n == 1:
+            ld = c
+        if one != 1 or ld < c or ld * t.element_size() & 15:
+            raise ValueError(f"{name}: rows must be dense, 16-byte aligned and not overlapping "
+                             f"(strides {t.stride()})")
+    if p & 15:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    return p, ld
+
+
+def _flat(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor of exactly this shape, or None."""
+    if t is None:
+        return None
+    _expect(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -115,8 +118,9 @@ def _pool(X, A, B, offsets, slots, rank, scale):
             _flat(slots, "slots", (B0,), torch.int32, dev))
 
 
+@functools.lru_cache(maxsize=1024)
 def adapter_workspace_size(slots: int, r: int, c1: int, c2: int, n: int, requests: int, dtype, backward=False) -> int:
-    """Workspace bytes of a call with these sizes; dtype: a torch or library type."""
+    """Workspace bytes of a call with these sizes (0: it needs none); dtype: a torch or library type."""
     need = ctypes.c_size_t()
     D._check("dyra_adapter_workspace_size",
              D.lib().dyra_adapter_workspace_size(slots, r, c1, c2, n, requests, _DTYPES.get(dtype, dtype),
@@ -128,7 +132,9 @@ def _workspace(workspace, ad, n, requests, dt, backward, device, stream):
     """Pointer, bytes and owner of the workspace (a temporary one if none is given)."""
     need = adapter_workspace_size(ad.slots, ad.r, ad.c1, ad.c2, n, requests, dt, backward)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:
             workspace.record_stream(stream)   # the work outlives this call on a stream that is not the current one
     else:
@@ -139,12 +145,14 @@ def _workspace(workspace, ad, n, requests, dt, backward, device, stream):
 
 def _on(device, stream):
     """The stream's handle; the library launches on the current device."""
+    here = torch.cuda.current_device()
+    if here != device.index:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{here}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        # the handle alone: making a Stream object of it takes as long as a small kernel's launch
+        return torch._C._cuda_getCurrentRawStream(here)
+    if stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the tensors are on {device}")
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
     return stream.cuda_stream
 
 

@@ -662,6 +662,111 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
 }
 
 // ---------------------------------------------------------------------------
+// a few rows: both products in one launch
+// ---------------------------------------------------------------------------
+
+struct DirectArgs {
+  const void *X, *A, *B, *base;
+  const int32_t* rank;
+  const float* scale;
+  void* out;
+  float* H;
+  int64_t ldx, ldb, ldo, c1, c2;
+  int32_t r, col_blocks;
+  Requests q;
+};
+
+constexpr int DIRECT_NT = 512;   // threads and columns of a workgroup
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[Step<T>::KPC]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (sizeof(T) == 2) {
+      v[2 * q] = __uint_as_float(w[q] << 16);
+      v[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    } else {
+      v[q] = __uint_as_float(w[q]);
+    }
+  }
+}
+
+// One workgroup: one row, 512 columns.  Every workgroup of a row forms the
+// row's whole H again from the L2: r c1 weights, which one CU reads in about
+// a microsecond at r = 16, c1 = 4096, where two more launches cost several.
+// The waves are JG groups of 16 rank columns (JG 16 >= r) times W / JG parts
+// of c1; weights are read a row of A at a time, 1 KB a wave.
+template <typename T, int JG>
+__global__ __launch_bounds__(DIRECT_NT, 4) void direct_kernel(DirectArgs p) {
+  constexpr int KPC = Step<T>::KPC, W = DIRECT_NT / 64, KG = W / JG, JB = 16;
+  __shared__ float part[KG][JG * JB], hs[JG * JB];
+  const int row = blockIdx.x / p.col_blocks, cb = blockIdx.x % p.col_blocks;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, jg = wave % JG, kg = wave / JG;
+  // the row's request: as many as start at or before it, less one
+  int b = 0;
+  for (int b0 = 1; b0 < p.q.count(); b0 += DIRECT_NT)
+    b += __syncthreads_count(b0 + tid < p.q.count() && p.q.lo(b0 + tid) <= row);
+  const int slot = p.q.id(b);
+  const bool none = slot >= p.q.slots;
+  const int rank = none ? 0 : p.rank ? min(max(p.rank[slot], 0), p.r) : p.r;
+  const float scale = none || !p.scale ? 1.f : p.scale[slot];
+  const int64_t c = (int64_t)cb * DIRECT_NT + tid;
+  const T* x = reinterpret_cast<const T*>(p.X) + (int64_t)row * p.ldx;
+  float y = c < p.c2 && p.base ? TT<T>::to_f(reinterpret_cast<const T*>(p.base)[(int64_t)row * p.ldb + c]) : 0.f;
+  if (!none) {
+    const T* a = reinterpret_cast<const T*>(p.A) + ((int64_t)slot * p.r + jg * JB) * p.c1;
+    float acc[JB] = {};
+    for (int64_t k = (int64_t)(kg * 64 + lane) * KPC; k < p.c1; k += KG * 64 * KPC) {
+      float xv[KPC];
+      unpack<T>(*reinterpret_cast<const uint4*>(x + k), xv);
+      uint4 w[JB];
+#pragma unroll
+      for (int j = 0; j < JB; ++j)   // the rank is not waited for: its rows' sums are dropped below
+        w[j] = jg * JB + j < p.r ? *reinterpret_cast<const uint4*>(a + (int64_t)j * p.c1 + k) : zero4();
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        float wv[KPC];
+        unpack<T>(w[j], wv);
+#pragma unroll
+        for (int e = 0; e < KPC; ++e) acc[j] += xv[e] * wv[e];
+      }
+    }
+    // 16 sums over 64 lanes: each step halves what a lane holds, lane bits 5 .. 2 pick the value
+#pragma unroll
+    for (int half = JB / 2, d = 32; half >= 1; half >>= 1, d >>= 1)
+#pragma unroll
+      for (int q = 0; q < half; ++q) {
+        const float keep = lane & d ? acc[q + half] : acc[q], give = lane & d ? acc[q] : acc[q + half];
+        acc[q] = keep + __shfl_xor(give, d);
+      }
+    acc[0] += __shfl_xor(acc[0], 2);
+    acc[0] += __shfl_xor(acc[0], 1);
+    if ((lane & 3) == 0)
+      part[kg][jg * JB + (lane >> 5 & 1) * 8 + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = acc[0];
+    __syncthreads();
+    if (tid < JG * JB) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < KG; ++w) v += part[w][tid];
+      hs[tid] = tid < rank ? v : 0.f;
+    }
+    __syncthreads();
+  }
+  if (p.H && cb == 0 && tid < p.r) p.H[(int64_t)row * p.r + tid] = tid < rank ? hs[tid] : 0.f;
+  if (c >= p.c2) return;
+  const T* wb = reinterpret_cast<const T*>(p.B) + ((int64_t)slot * p.c2 + c) * p.r;
+  float d = 0.f;
+  for (int j = 0; j < rank; j += KPC) {
+    float wv[KPC];
+    unpack<T>(*reinterpret_cast<const uint4*>(wb + j), wv);
+#pragma unroll
+    for (int e = 0; e < KPC; ++e) d += j + e < rank ? hs[j + e] * wv[e] : 0.f;
+  }
+  reinterpret_cast<T*>(p.out)[(int64_t)row * p.ldo + c] = TT<T>::from_f(rank > 0 ? y + scale * d : y);
+}
+
+// ---------------------------------------------------------------------------
 // weight gradients: part[chunk][j][c] = sum over the chunk's rows of
 // s P[row][j] V[row][c]   (dA: P = G, V = X;  dB: P = s H, V = dY)
 // ---------------------------------------------------------------------------
@@ -877,6 +982,7 @@ struct Plan {
   int ks;                           // slices of the reduction in the shrink
   int chunk;                        // tiles of a gradient chunk (backward), else 0
   int packed;                       // weights are packed first
+  bool direct;                      // forward: one launch, no workspace
   int64_t tile_cap, chunk_cap;
   size_t perm, tiles, chunks, slot_chunk, P, Ws, We, Pf, Hf, partA, partB, total;
 };
@@ -890,6 +996,13 @@ int shrink_split(int64_t wgs, int64_t K, int dtype) {
 
 Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int64_t B, int dtype, bool backward) {
   Plan q{};
+  // One launch where its workgroups fit the card at once and what they read
+  // of A again and again stays small.  In graph replays, one launch against
+  // three: 4 rows of 4096 -> 4096 at r = 16 5.8 and 14.0 us, 64 rows 9.6 and
+  // 15.0, 32 rows at r = 64 (128 MiB of A) 16.3 and 18.3.
+  const int64_t direct_wgs = n * cdiv64(c2, DIRECT_NT);
+  q.direct = !backward && direct_wgs <= 512 && direct_wgs * r * c1 * (int64_t)elem_bytes(dtype) <= (int64_t)128 << 20;
+  if (q.direct) return q;
   const bool small = n <= 512 && !backward;
   q.tile = small ? 16 : GRAD_TILE;
   q.rt = r > 32 && n >= 8192 ? 2 : 1;   // a weight operand serves RT blocks of 16 rows; 256 workgroups first
@@ -1009,6 +1122,16 @@ void launch_expand(const ExpandArgs& a, int ert, hipStream_t st) {
 template <typename T>
 int forward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const void* base, int64_t ldb, void* Y,
                  int64_t ldy, float* H, const Requests& rq, const Plan& q, char* ws, hipStream_t st) {
+  if (q.direct) {
+    const int blocks = (int)cdiv64(ad.c2, DIRECT_NT);
+    const DirectArgs da{X, ad.A, ad.B, base, ad.rank, ad.scale, Y, H, ldx, ldb, ldy, ad.c1, ad.c2, ad.r, blocks, rq};
+    const dim3 grid((unsigned)(rq.n * blocks)), nt(DIRECT_NT);
+    if (ad.r <= 16) hipLaunchKernelGGL((direct_kernel<T, 1>), grid, nt, 0, st, da);
+    else if (ad.r <= 32) hipLaunchKernelGGL((direct_kernel<T, 2>), grid, nt, 0, st, da);
+    else if (ad.r <= 64) hipLaunchKernelGGL((direct_kernel<T, 4>), grid, nt, 0, st, da);
+    else hipLaunchKernelGGL((direct_kernel<T, 8>), grid, nt, 0, st, da);
+    return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
+  }
   const Grouped g = grouped(q, ws);
   const void *Ws = ad.A, *We = ad.B;
   Pack<T> pa{}, pb{};
@@ -1126,13 +1249,14 @@ extern "C" int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int6
   if (misaligned(ad->A, 15) || misaligned(ad->B, 15) || misaligned(ad->rank, 3) || misaligned(ad->scale, 3))
     return DYRA_EINVAL;
   if (n == 0) return DYRA_OK;
-  if (!X || !Y || !workspace || (B && (!offsets_dev || !slots_dev))) return DYRA_EINVAL;
+  if (!X || !Y || (B && (!offsets_dev || !slots_dev))) return DYRA_EINVAL;
   if (misaligned(X, 15) || misaligned(base, 15) || misaligned(Y, 15) || misaligned(H, 15) ||
       misaligned(workspace, 15) || misaligned(offsets_dev, 3) || misaligned(slots_dev, 3))
     return DYRA_EINVAL;
   if (bad_stride(ldx, ad->c1, dtype) || bad_stride(ldy, ad->c2, dtype) || (base && bad_stride(ldb, ad->c2, dtype)))
     return DYRA_ESHAPE;
   const Plan q = make_plan(ad->slots, ad->r, ad->c1, ad->c2, n, B, dtype, false);
+  if (q.total && !workspace) return DYRA_EINVAL;
   if (ws_bytes < q.total) return DYRA_EWORKSPACE;
   if (!grids_fit(*ad, q, false)) return DYRA_ESHAPE;
   const Requests rq{offsets_dev, slots_dev, (int32_t)n, (int32_t)B, ad->slots};

@@ -23,9 +23,10 @@ def _size(slots=4, r=16, c1=64, c2=96, n=100, B=7, dtype=BF16, backward=0):
     (dict(B=-1), -2),
 ])
 def test_workspace_size(kw, code):
-    rc, need = _size(**kw)
+    """(A few rows need no workspace; the thousand here do.)"""
+    rc, need = _size(**dict(dict(n=1000), **kw))
     assert rc == code
-    assert (need > 0) == (code == 0)
+    assert (need > 0) == (code == 0 and kw.get("n", 1000) > 0)
 
 
 def test_workspace_grows_with_the_backward_pass():
@@ -38,7 +39,7 @@ P = 1 << 12
 
 
 def _forward(slots=4, r=16, c1=64, c2=96, A=P, B=P, rank=None, scale=None, X=P, ldx=64, base=None, ldb=0, Y=P, ldy=96,
-             H=None, n=100, nb=7, off=P, ids=P, dtype=BF16, ws=P, ws_bytes=1 << 40):
+             H=None, n=1000, nb=7, off=P, ids=P, dtype=BF16, ws=P, ws_bytes=1 << 40):
     ad = D.Adapters(slots, r, c1, c2, A, B, rank, scale)
     return D.lib().dyra_adapter_forward(ad, X, ldx, base, ldb, Y, ldy, H, n, nb, off, ids, dtype, ws, ws_bytes, None)
 
