@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "../../include/dyra.h"
 #include "device_common.h"
@@ -372,6 +373,82 @@ __device__ __forceinline__ void shrink_out(const ShrinkArgs& p, float* P, f32x4 
   }
 }
 
+// Calls f with the number of 16-column blocks as a constant: n, rounded up to
+// a power of two, at most CT.
+template <int CT, class F>
+__device__ __forceinline__ void with_blocks(int n, F&& f) {
+  if constexpr (CT == 1) {
+    f(std::integral_constant<int, 1>());
+  } else {
+    if (n > CT / 2) f(std::integral_constant<int, CT>());
+    else with_blocks<CT / 2>(n, f);
+  }
+}
+
+// k-steps s0 .. s1 - 1 of a wave's RT row blocks by N weight blocks, the
+// operands of D - 1 steps in flight.  No load is conditional: behind a branch
+// the compiler could not count the loads in flight and would wait for all of
+// them.  Steps and rows past the end repeat the last, and the one step that K
+// may end in stands by itself.
+template <typename T, int RT, int N, int CT, int D>
+__device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* const (&xr)[RT], const T* w,
+                                             const ShrinkArgs& p, int i, int g, int s0, int s1, int cts) {
+  constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K;
+  const int wstep = p.packed ? cts * 64 * KPC : KSTEP;
+  int64_t wr[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c)   // rows past the pool's r repeat the last one; their sums are dropped
+    wr[c] = p.packed ? (int64_t)min(c, cts - 1) * 64 * KPC : (int64_t)min(16 * c + i, p.r - 1) * p.K;
+  const bool ragged = (int64_t)s1 * KSTEP > p.K && s0 < s1;
+  const int n = s1 - s0 - (ragged ? 1 : 0);
+  if (n > 0) {
+    uint4 x[D][RT], v[D][N];
+    auto load = [&](int d, int s) {
+      s = s0 + min(s, n - 1);
+#pragma unroll
+      for (int a = 0; a < RT; ++a) x[d][a] = *reinterpret_cast<const uint4*>(xr[a] + (int64_t)s * KSTEP);
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[d][c] = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)s * wstep);
+    };
+    auto mul = [&](int d) {
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], x[d][a], v[d][c]);
+    };
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load(d, d);
+    int s = 0;
+    for (; s + D <= n; s += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        load((d + D - 1) % D, s + d + D - 1);
+        mul(d);
+      }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (s + d < n) mul(d);
+  }
+  if (ragged) {
+    const int s = s1 - 1;
+    const bool in = (int64_t)s * KSTEP + g * KPC < p.K;
+    const int back = in ? 0 : g * KPC;   // lanes past K read the step's first chunk and use zeros
+    uint4 x[RT];
+#pragma unroll
+    for (int a = 0; a < RT; ++a) {
+      x[a] = *reinterpret_cast<const uint4*>(xr[a] + (int64_t)s * KSTEP - back);
+      x[a] = in ? x[a] : zero4();
+    }
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      uint4 v = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)s * wstep - (p.packed ? 0 : back));
+      v = in ? v : zero4();
+#pragma unroll
+      for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], x[a], v);
+    }
+  }
+}
+
 // One workgroup: 16 RT rows of one slot, one of KS slices of K, which its
 // waves divide again; their sums meet in LDS.  A wave reads X straight into
 // matrix operands, each 16-byte load one operand of 16 rows; the weights come
@@ -381,7 +458,6 @@ __device__ __forceinline__ void shrink_out(const ShrinkArgs& p, float* P, f32x4 
 template <typename T, int RT, int CT>
 __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 4) void shrink_kernel(ShrinkArgs p) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, W = SHRINK_WAVES;
-  constexpr int U = RT + CT > 5 ? 1 : 2;
   constexpr int CB = CT < 4 ? CT : 4;      // 16-column blocks joined at a time
   __shared__ float red[W][CB][256];
   const int tile = blockIdx.x / (p.sub * p.KS), rem = blockIdx.x % (p.sub * p.KS);
@@ -406,45 +482,12 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 4) void shrink_kern
       xr[a] = reinterpret_cast<const T*>(p.X) + (int64_t)(row_of[a] < 0 ? any : row_of[a]) * p.ldx + g * KPC;
     const int steps = (int)cdiv64(p.K, KSTEP), per = (steps + p.KS * W - 1) / (p.KS * W);
     const int s0 = (ks * W + wave) * per, s1 = min(s0 + per, steps);
-    const T* wr[CT];
-    const T* ws = reinterpret_cast<const T*>(p.W) + (p.packed ? (int64_t)t.slot * steps * cts * 64 * KPC + lane * KPC
-                                                              : (int64_t)t.slot * p.r * p.K + g * KPC);
-    const int wstep = p.packed ? cts * 64 * KPC : KSTEP;
-#pragma unroll
-    for (int c = 0; c < CT; ++c)   // rows past the pool's r repeat the last one; their sums are dropped
-      wr[c] = ws + (p.packed ? (int64_t)min(c, cts - 1) * 64 * KPC : (int64_t)min(16 * c + i, p.r - 1) * p.K);
-    struct Stage {
-      uint4 x[U][RT], w[U][CT];
-    };
-    auto load = [&](Stage& st, int s) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (s + u) * KSTEP;
-        const bool ok = s + u < s1 && k + g * KPC < (int)p.K;
-#pragma unroll
-        for (int a = 0; a < RT; ++a) st.x[u][a] = ok ? *reinterpret_cast<const uint4*>(xr[a] + k) : zero4();
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          st.w[u][c] = ok && c < nct ? *reinterpret_cast<const uint4*>(wr[c] + (int64_t)(s + u) * wstep) : zero4();
-      }
-    };
-    auto mul = [&](const Stage& st) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          if (c < nct)
-#pragma unroll
-            for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], st.x[u][a], st.w[u][c]);
-    };
-    Stage even, odd;
-    if (s0 < s1) load(even, s0);
-    for (int s = s0; s < s1; s += 2 * U) {
-      load(odd, s + U);
-      mul(even);
-      load(even, s + 2 * U);
-      mul(odd);
-    }
+    const T* wbase = reinterpret_cast<const T*>(p.W) + (p.packed ? (int64_t)t.slot * steps * cts * 64 * KPC + lane * KPC
+                                                                 : (int64_t)t.slot * p.r * p.K + g * KPC);
+    with_blocks<CT>(nct, [&](auto blocks) {
+      constexpr int N = decltype(blocks)::value;
+      shrink_slice<T, RT, N, CT, (RT * N > 4 ? 2 : 3)>(acc, xr, wbase, p, i, g, s0, s1, cts);
+    });
   }
   // join the waves: D[row][j] of a 16x16 block sits at lane j + 16 (row / 4), register row % 4
   float* P = p.P + (int64_t)ks * p.n * p.r;
@@ -474,6 +517,67 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 4) void shrink_kern
 }
 
 // ---------------------------------------------------------------------------
+// the gradients' chunks joined
+// ---------------------------------------------------------------------------
+
+// Sums the chunks of each slot in order: dA[s][j][c], and dB[s][c][j]
+// (transposed through LDS).  Rows past a slot's rank, and slots without rows,
+// are zero.  One workgroup: 64 columns and 16 rank columns of one slot.
+struct JoinArgs {
+  const float* part[2];   // dB's, dA's
+  float* out[2];
+  int64_t C[2];
+  int32_t blocks[2];
+  const int32_t* rank;
+  const int32_t* slot_chunk;
+  int32_t r, chunk_cap;
+};
+
+constexpr int JOIN_LDS = 16 * 68;
+
+__device__ __forceinline__ void join_block(const JoinArgs& p, int id, float* lds) {
+  const int which = id >= p.blocks[0];
+  id -= which ? p.blocks[0] : 0;
+  if (which && id >= p.blocks[1]) return;
+  const int64_t C = p.C[which];
+  const int cbs = (int)cdiv64(C, 64), rbs = (p.r + 15) >> 4;
+  const int cb = id % cbs, rb = id / cbs % rbs, slot = id / cbs / rbs;
+  const int rank = p.rank ? min(max(p.rank[slot], 0), p.r) : p.r;
+  const int lo = min(max(p.slot_chunk[slot], 0), p.chunk_cap), hi = min(p.slot_chunk[slot + 1], p.chunk_cap);
+  const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4, j = rb * 16 + y;
+  const int64_t c = (int64_t)cb * 64 + x, step = (int64_t)p.r * C;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (j < rank && c < C) {
+    const float* s = p.part[which] + (int64_t)lo * step + (int64_t)j * C + c;
+#pragma unroll 8
+    for (int k = lo; k < hi; ++k, s += step) {
+      const float4 u = *reinterpret_cast<const float4*>(s);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+  }
+  if (which) {
+    if (j < p.r && c < C) *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
+    return;
+  }
+  *reinterpret_cast<float4*>(&lds[y * 68 + x]) = v;
+  __syncthreads();
+  // 4 rank columns of a column a thread
+  const int cc = threadIdx.x >> 2, j4 = (threadIdx.x & 3) * 4;
+  const int64_t oc = (int64_t)cb * 64 + cc;
+  if (oc < C && rb * 16 + j4 < p.r)
+    *reinterpret_cast<float4*>(p.out[0] + ((int64_t)slot * C + oc) * p.r + rb * 16 + j4) =
+        make_float4(lds[j4 * 68 + cc], lds[(j4 + 1) * 68 + cc], lds[(j4 + 2) * 68 + cc], lds[(j4 + 3) * 68 + cc]);
+}
+
+__global__ __launch_bounds__(256) void grad_join_kernel(JoinArgs p) {
+  __shared__ __attribute__((aligned(16))) float lds[JOIN_LDS];
+  join_block(p, blockIdx.x, lds);
+}
+
+// ---------------------------------------------------------------------------
 // expand: out[row][c] = base[row][c] + sum_j scale P[row][j] W_slot[c][j]
 // ---------------------------------------------------------------------------
 
@@ -500,7 +604,7 @@ constexpr int EXPAND_COLS = 256;   // columns of a workgroup, 64 of each wave
 // results come to lanes that hold 16 bytes of a row, 8 lanes to a 128-byte
 // line, the form in which base is read and the result written.
 template <typename T, int RT, int NK>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p, JoinArgs join, int join_wgs) {
   constexpr bool BF = sizeof(T) == 2;
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, TERMS = BF ? 2 : 1;
   constexpr int PITCH = NK * KSTEP * (int)sizeof(T) + 16;   // bytes of a row in LDS; 16 more spread the banks
@@ -509,7 +613,10 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
   constexpr int RPI = 64 / LPR, PIECES = 16 / RPI;   // rows of a load; loads for 16 rows
   __shared__ __attribute__((aligned(16))) char hs[TERMS * 16 * RT * PITCH];
   __shared__ __attribute__((aligned(16))) float ds[4][16 * DP];
-  const int id = xcd_tile_id(blockIdx.x, gridDim.x);
+  static_assert(sizeof(ds) >= JOIN_LDS * sizeof(float), "the join's LDS");
+  // a backward pass joins the weight gradients in the same launch
+  if ((int)blockIdx.x < join_wgs) return join_block(join, blockIdx.x, ds[0]);
+  const int id = xcd_tile_id(blockIdx.x - join_wgs, gridDim.x - join_wgs);
   const int cb = id % p.col_blocks, part = id / p.col_blocks, sub = part % p.sub, tile = part / p.sub;
   const Tile t = p.g.tiles[tile];
   if (t.count <= sub * 16 * RT) return;
@@ -785,6 +892,7 @@ struct GradArgs {
   Grouped g;           // tiles of 64 rows
 };
 
+constexpr int CHUNK_TILES = 32;   // most tiles of a chunk: their rows are kept in LDS
 template <typename T> constexpr int grad_cols() { return sizeof(T) == 2 ? 128 : 64; }   // columns of a wave
 
 // One workgroup: a chunk of tiles, 4 waves' columns, up to 16 CT rank columns.
@@ -800,6 +908,7 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
   constexpr int COLS = grad_cols<T>(), PARTS = grad_parts<T>(), BYTES = CT * PARTS * 1024;
   constexpr int NA = (BYTES / 16 + 255) / 256;   // 16-byte loads of a thread for a half tile's operands
   __shared__ __attribute__((aligned(16))) char lds[2][BYTES];
+  __shared__ __attribute__((aligned(16))) int rows_of[CHUNK_TILES * GRAD_TILE];
   int id = blockIdx.x;
   const int per0 = p.side[0].col_blocks * p.r_groups * p.chunk_cap;
   const int which = id >= per0;
@@ -824,22 +933,17 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
   // the second half of the last tile has no operands if it has no row
   const int last_count = p.g.tiles[t.first + t.tiles - 1].count;
   const int halves = t.tiles * 2 - (last_count <= 32 ? 1 : 0);
-  const int* perm = p.g.perm + (int64_t)t.first * GRAD_TILE + 8 * g;
   const char* ops = grad_block<T>(v.Pf, (int64_t)t.first * 2, j0 >> 4, cts) + tid * 16;
   const int bytes = nct * PARTS * 1024;
 
-  auto load_rows = [&](int (&rows)[8], int h) {
-    const int4* s = reinterpret_cast<const int4*>(perm + (int64_t)min(h, halves - 1) * 32);
+  auto load_v = [&](uint4(&in)[8], int h) {
+    const int4* s = reinterpret_cast<const int4*>(rows_of + min(h, halves - 1) * 32 + 8 * g);
     const int4 a = s[0], b = s[1];
-    rows[0] = a.x, rows[1] = a.y, rows[2] = a.z, rows[3] = a.w;
-    rows[4] = b.x, rows[5] = b.y, rows[6] = b.z, rows[7] = b.w;
-  };
-  auto load_v = [&](uint4(&in)[8], const int (&rows)[8], int h) {
+    const int rows[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      in[e] = h < halves && live && (unsigned)rows[e] < (unsigned)p.n
-                  ? *reinterpret_cast<const uint4*>(V + (int64_t)rows[e] * v.ldv)
-                  : zero4();
+      in[e] = h < halves && live && rows[e] >= 0 ? *reinterpret_cast<const uint4*>(V + (int64_t)rows[e] * v.ldv)
+                                                 : zero4();
   };
   auto load_a = [&](uint4(&a)[NA], int h) {
 #pragma unroll
@@ -882,25 +986,22 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
     }
   };
 
+  for (int u = tid; u < halves * 32; u += 256) rows_of[u] = tile_row(p.g, t.first, u, p.n);
   uint4 even[8], odd[8], a[NA];
-  int rows[8];
-  load_rows(rows, 0);
   load_a(a, 0);
-  load_v(even, rows, 0);
-  load_rows(rows, 1);
+  __syncthreads();
+  load_v(even, 0);
   put_a(a, 0);
   __syncthreads();
   for (int h = 0; h < halves; h += 2) {
     load_a(a, h + 1);
-    load_v(odd, rows, h + 1);
-    load_rows(rows, h + 2);
+    load_v(odd, h + 1);
     mul(even, h);
     put_a(a, h + 1);
     __syncthreads();
     if (h + 1 < halves) {
       load_a(a, h + 2);
-      load_v(even, rows, h + 2);
-      load_rows(rows, h + 3);
+      load_v(even, h + 2);
       mul(odd, h + 1);
       put_a(a, h + 2);
       __syncthreads();
@@ -919,57 +1020,6 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
         *reinterpret_cast<float4*>(out + (int64_t)j * v.C + col + e) =
             make_float4(acc[c][e][q], acc[c][e + 1][q], acc[c][e + 2][q], acc[c][e + 3][q]);
     }
-}
-
-// Sums the chunks of each slot in order: dA[s][j][c], and dB[s][c][j]
-// (transposed through LDS).  Rows past a slot's rank, and slots without rows,
-// are zero.  One workgroup: 64 columns and 16 rank columns of one slot.
-struct JoinArgs {
-  const float* part[2];   // dB's, dA's
-  float* out[2];
-  int64_t C[2];
-  int32_t blocks[2];
-  const int32_t* rank;
-  int32_t r, slots, chunk_cap;
-  Grouped g;
-};
-
-__global__ __launch_bounds__(256) void grad_join_kernel(JoinArgs p) {
-  __shared__ float buf[16][68];
-  int id = blockIdx.x;
-  const int which = id >= p.blocks[0];
-  id -= which ? p.blocks[0] : 0;
-  const int64_t C = p.C[which];
-  const int cbs = (int)cdiv64(C, 64), rbs = (p.r + 15) >> 4;
-  const int cb = id % cbs, rb = id / cbs % rbs, slot = id / cbs / rbs;
-  const int rank = p.rank ? min(max(p.rank[slot], 0), p.r) : p.r;
-  const int lo = min(max(p.g.slot_chunk[slot], 0), p.chunk_cap), hi = min(p.g.slot_chunk[slot + 1], p.chunk_cap);
-  const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4, j = rb * 16 + y;
-  const int64_t c = (int64_t)cb * 64 + x, step = (int64_t)p.r * C;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (j < rank && c < C) {
-    const float* s = p.part[which] + (int64_t)lo * step + (int64_t)j * C + c;
-#pragma unroll 8
-    for (int k = lo; k < hi; ++k, s += step) {
-      const float4 u = *reinterpret_cast<const float4*>(s);
-      v.x += u.x;
-      v.y += u.y;
-      v.z += u.z;
-      v.w += u.w;
-    }
-  }
-  if (which) {
-    if (j < p.r && c < C) *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
-    return;
-  }
-  *reinterpret_cast<float4*>(&buf[y][x]) = v;
-  __syncthreads();
-  // 4 rank columns of a column a thread
-  const int cc = threadIdx.x >> 2, j4 = (threadIdx.x & 3) * 4;
-  const int64_t oc = (int64_t)cb * 64 + cc;
-  if (oc < C && rb * 16 + j4 < p.r)
-    *reinterpret_cast<float4*>(p.out[0] + ((int64_t)slot * C + oc) * p.r + rb * 16 + j4) =
-        make_float4(buf[j4][cc], buf[j4 + 1][cc], buf[j4 + 2][cc], buf[j4 + 3][cc]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1032,7 +1082,7 @@ Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int6
     const int parts = dtype == DYRA_BF16 ? grad_parts<bf16_t>() : grad_parts<float>();
     const int64_t blocks = cdiv64(c1, cols) + cdiv64(c2, cols);
     const int64_t most = std::max<int64_t>(1, 512 / blocks), chunks = std::max((most + 1) / 2, most - std::min(slots, B));
-    q.chunk = (int)std::max<int64_t>(1, cdiv64(cdiv64(n, GRAD_TILE), chunks));
+    q.chunk = (int)std::min<int64_t>(CHUNK_TILES, std::max<int64_t>(1, cdiv64(cdiv64(n, GRAD_TILE), chunks)));
     q.chunk_cap = n / ((int64_t)q.chunk * GRAD_TILE) + std::min(slots, B) + 1;
     q.chunks = take((int64_t)sizeof(Chunk) * q.chunk_cap);
     q.slot_chunk = take(4 * (slots + 1));
@@ -1104,19 +1154,28 @@ void launch_shrink(const ShrinkArgs& a, int rt, hipStream_t st) {
 }
 
 template <typename T, int RT>
-void launch_expand_rt(const ExpandArgs& a, unsigned grid, hipStream_t st) {
+void launch_expand_rt(const ExpandArgs& a, const JoinArgs& j, int join_wgs, unsigned grid, hipStream_t st) {
   const int nk = (a.r + Step<T>::K - 1) / Step<T>::K;
-  if (nk <= 1) hipLaunchKernelGGL((expand_kernel<T, RT, 1>), dim3(grid), dim3(256), 0, st, a);
-  else if (nk <= 2) hipLaunchKernelGGL((expand_kernel<T, RT, 2>), dim3(grid), dim3(256), 0, st, a);
-  else if (nk <= 4) hipLaunchKernelGGL((expand_kernel<T, RT, 4>), dim3(grid), dim3(256), 0, st, a);
-  else if constexpr (sizeof(T) == 4) hipLaunchKernelGGL((expand_kernel<T, RT, 8>), dim3(grid), dim3(256), 0, st, a);
+  const dim3 nt(256);
+  if (nk <= 1) hipLaunchKernelGGL((expand_kernel<T, RT, 1>), dim3(grid), nt, 0, st, a, j, join_wgs);
+  else if (nk <= 2) hipLaunchKernelGGL((expand_kernel<T, RT, 2>), dim3(grid), nt, 0, st, a, j, join_wgs);
+  else if (nk <= 4) hipLaunchKernelGGL((expand_kernel<T, RT, 4>), dim3(grid), nt, 0, st, a, j, join_wgs);
+  else if constexpr (sizeof(T) == 4)
+    hipLaunchKernelGGL((expand_kernel<T, RT, 8>), dim3(grid), nt, 0, st, a, j, join_wgs);
 }
 
+// join: the weight gradients' join of a backward pass, or null
 template <typename T>
-void launch_expand(const ExpandArgs& a, int ert, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.tiles * a.sub * a.col_blocks);
-  if (ert == 1) launch_expand_rt<T, 1>(a, grid, st);
-  else launch_expand_rt<T, 2>(a, grid, st);
+void launch_expand(const ExpandArgs& a, int ert, const JoinArgs* join, hipStream_t st) {
+  JoinArgs j{};
+  int wgs = 0;
+  if (join) {
+    j = *join;
+    wgs = (j.blocks[0] + j.blocks[1] + 7) & ~7;   // the XCDs of the others stay as they are
+  }
+  const unsigned grid = (unsigned)((int64_t)a.tiles * a.sub * a.col_blocks + wgs);
+  if (ert == 1) launch_expand_rt<T, 1>(a, j, wgs, grid, st);
+  else launch_expand_rt<T, 2>(a, j, wgs, grid, st);
 }
 
 template <typename T>
@@ -1157,7 +1216,7 @@ int forward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const void
                       (int32_t)q.tile_cap, (int32_t)cdiv64(ad.c2, EXPAND_COLS),
                       q.tile / (16 * q.ert), q.packed,
                       g};
-  launch_expand<T>(ea, q.ert, st);
+  launch_expand<T>(ea, q.ert, nullptr, st);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
@@ -1184,6 +1243,7 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
                         1,       g};
     launch_shrink<T>(sa, q.rt, st);
   }
+  JoinArgs join{};
   if (dA) {
     float *pdA = reinterpret_cast<float*>(ws + q.partA), *pdB = reinterpret_cast<float*>(ws + q.partB);
     const int cols = 4 * grad_cols<T>();
@@ -1197,9 +1257,10 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
     }
     const int64_t rbs = cdiv64(ad.r, 16);
     const int64_t b0 = cdiv64(ad.c2, 64) * rbs * ad.slots, b1 = cdiv64(ad.c1, 64) * rbs * ad.slots;
-    const JoinArgs ja{{pdB, pdA}, {dB, dA}, {ad.c2, ad.c1}, {(int32_t)b0, (int32_t)b1}, ad.rank, ad.r, ad.slots,
-                      (int32_t)q.chunk_cap, g};
-    hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(b0 + b1)), dim3(256), 0, st, ja);
+    join = JoinArgs{{pdB, pdA}, {dB, dA}, {ad.c2, ad.c1}, {(int32_t)b0, (int32_t)b1}, ad.rank, g.slot_chunk, ad.r,
+                    (int32_t)q.chunk_cap};
+    if (!dX || !rq.n)
+      hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(b0 + b1)), dim3(256), 0, st, join);
   }
   if (dX && rq.n) {
     const ExpandArgs ea{P,       pa.dst,
@@ -1212,7 +1273,7 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
                         (int32_t)q.tile_cap, (int32_t)cdiv64(ad.c1, EXPAND_COLS),
                         q.tile / (16 * q.ert), 1,
                         g};
-    launch_expand<T>(ea, q.ert, st);
+    launch_expand<T>(ea, q.ert, dA ? &join : nullptr, st);
   }
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
@@ -1224,7 +1285,8 @@ bool grids_fit(const dyra_adapters& ad, const Plan& q, bool backward) {
   if (q.tile_cap * q.sub * q.ks > most || q.tile_cap * 4 * cdiv64(c, EXPAND_COLS) > most) return false;
   if (q.packed && packs * ad.slots + 64 > most) return false;
   if (!backward) return true;
-  return (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots <= most &&
+  return (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots +
+                 q.tile_cap * 4 * cdiv64(ad.c1, EXPAND_COLS) + 8 <= most &&
          (cdiv64(ad.c1, 256) + cdiv64(ad.c2, 256)) * 2 * q.chunk_cap <= most;
 }
 
