@@ -314,7 +314,7 @@ struct ShrinkArgs {
   Grouped g;
 };
 
-constexpr int SHRINK_WAVES = 8;
+constexpr int SHRINK_WAVES = 4;
 constexpr int GRAD_TILE = 64;   // rows of a tile, but for the smallest forward passes
 
 // Operands of the weight gradients: 32 rows (half a tile) of 16 rank columns,
@@ -358,12 +358,16 @@ __device__ __forceinline__ void shrink_out(const ShrinkArgs& p, float* P, f32x4 
                                            int block, int c, int i, int q4, int rank, float scale) {
   const int j = 16 * c + i;
   f32x4 h = {0.f, 0.f, 0.f, 0.f};
+  if (p.Hf) {   // the four loads together: none is conditional
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = p.H[(int64_t)max(rows[q], 0) * p.r + min(j, p.r - 1)];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = rows[q] >= 0 && j < rank ? h[q] * scale : 0.f;
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int row = rows[q];
-    v[q] = row < 0 ? 0.f : v[q] * scale;
-    if (row >= 0 && j < p.r) P[(int64_t)row * p.r + j] = v[q];
-    if (p.Hf && row >= 0 && j < rank) h[q] = p.H[(int64_t)row * p.r + j] * scale;
+    v[q] = rows[q] < 0 ? 0.f : v[q] * scale;
+    if (rows[q] >= 0 && j < p.r) P[(int64_t)rows[q] * p.r + j] = v[q];
   }
   if (p.Pf && 16 * c < rank) {
     const int64_t half = (int64_t)tile * 2 + (block >> 1);
@@ -456,7 +460,7 @@ __device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* cons
 // The loads of the next U k-steps are in flight while the present ones are
 // multiplied.
 template <typename T, int RT, int CT>
-__global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 4) void shrink_kernel(ShrinkArgs p) {
+__global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kernel(ShrinkArgs p) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, W = SHRINK_WAVES;
   constexpr int CB = CT < 4 ? CT : 4;      // 16-column blocks joined at a time
   __shared__ float red[W][CB][256];
@@ -486,7 +490,7 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 4) void shrink_kern
                                                                  : (int64_t)t.slot * p.r * p.K + g * KPC);
     with_blocks<CT>(nct, [&](auto blocks) {
       constexpr int N = decltype(blocks)::value;
-      shrink_slice<T, RT, N, CT, (RT * N > 4 ? 2 : 3)>(acc, xr, wbase, p, i, g, s0, s1, cts);
+      shrink_slice<T, RT, N, CT, (RT * N > 8 ? 2 : 3)>(acc, xr, wbase, p, i, g, s0, s1, cts);
     });
   }
   // join the waves: D[row][j] of a 16x16 block sits at lane j + 16 (row / 4), register row % 4
@@ -1041,7 +1045,7 @@ int shrink_split(int64_t wgs, int64_t K, int dtype) {
   const int64_t steps = cdiv64(K, dtype == DYRA_BF16 ? 32 : 16);
   int64_t ks = cdiv64(512, wgs);                              // two workgroups per CU
   ks = std::min<int64_t>(ks, cdiv64(steps, 2 * SHRINK_WAVES));   // at least two k-steps per wave
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ks, 16));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ks, 4));   // more slices cost the expand more than they save
 }
 
 Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int64_t B, int dtype, bool backward) {
@@ -1061,7 +1065,7 @@ Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int6
   const int64_t used = std::min(slots + 1, B + 1);   // slots with rows, "no adapter" among them
   q.tile_cap = n / q.tile + used + 1;
   q.packed = backward || (n > 512 && n >= 64 * std::min(slots, B));
-  const int64_t wgs = std::max<int64_t>(1, cdiv64(n, 16 * q.rt));
+  const int64_t wgs = std::max<int64_t>(1, std::min(n, q.tile_cap * q.sub));
   q.ks = backward ? 1 : shrink_split(wgs, c1, dtype);
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
