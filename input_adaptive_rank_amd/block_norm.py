@@ -132,14 +132,20 @@ def block_norm_backward(x_new, y, dz, dx_new=None, pre="rms", post="none", pre_w
     if dx is not None and dy is not None:
         _apart(dx, "dx", [("dy", dy)])
     dx, dy = _output(dx, shape, dtype, dev, stream), _output(dy, shape, dtype, dev, stream)
-    grads = {"d_" + name: None if t is None else _output(None, t.shape, torch.float32, dev, stream)
-             for name, t in params}
+    # one allocation: a row for each vector, the gate's rows last
+    vectors = [name for name, t in params if t is not None and t.dim() == 1]
+    buf = _output(None, (len(vectors) + (nb if gate is not None and gate.dim() == 2 else 0), c), torch.float32, dev,
+                  stream)
+    rows_of = dict(zip(vectors, buf[:len(vectors)].unbind(0))) if vectors else {}
+    if gate is not None and gate.dim() == 2:
+        rows_of["gate"] = buf[len(vectors):]
+    grads = {"d_" + name: rows_of.get(name) for name, _ in params}
     g = D.BlockNormGrads(*[None if t is None else t.data_ptr() for t in grads.values()])
     need = ctypes.c_size_t()
     L = D.lib()
     D._check("dyra_block_norm_workspace_size", L.dyra_block_norm_workspace_size(p, n, nb, dt, need))
     if workspace is None:
-        workspace = _output(None, (max(need.value, 16),), torch.uint8, dev, stream)
+        workspace = _output(None, (need.value,), torch.uint8, dev, stream)
     else:
         D._expect_bytes(workspace, "workspace", need.value)
         D._expect_device([("workspace", workspace)], dev)

@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -37,19 +38,13 @@ def _run(cmd):
 def build(verbose: bool = False) -> str:
     """Compiles every source (always) and links libdyra.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
-    for src in HOST_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        out = _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-        if verbose and out:
-            print(out)
-        objs.append(obj)
-    for src in HIP_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        out = _run([HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-        if verbose and out:
-            print(out)
-        objs.append(obj)
+    cmds = [["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, s)] for s in HOST_SOURCES]
+    cmds += [[HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, s)] for s in HIP_SOURCES]
+    objs = [os.path.join(BUILD, s + ".o") for s in HOST_SOURCES + HIP_SOURCES]
+    with ThreadPoolExecutor(max_workers=min(4, os.cpu_count() or 1)) as pool:   # each compiler is a process of its own
+        for out in pool.map(_run, [cmd + ["-o", obj] for cmd, obj in zip(cmds, objs)]):
+            if verbose and out:
+                print(out)
     tmp = LIB + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp, "-lpthread"])
     os.replace(tmp, LIB)

@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "../../include/dyra.h"
 #include "device_common.h"
@@ -117,7 +118,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* lds, int& flip) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
   if constexpr (WPR > 1) {
-    const int wave = threadIdx.x >> 6, first = wave & ~(WPR - 1);
+    const int wave = threadIdx.x >> 6, first = wave / WPR * WPR;
     float* buf = lds + flip * (16 * 4);
     flip ^= 1;
     if ((threadIdx.x & 63) == 0)
@@ -547,7 +548,7 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormJoinArgs p) {
 bool misaligned(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How a row lies over lanes: waves, and chunks of 8 elements a lane.
+// How a row lies over lanes: waves (1 to 8, or 16), and chunks of 8 elements a lane.
 struct Shape {
   int waves, chunks;
 };
@@ -556,9 +557,8 @@ struct Shape {
 // the registers) only where 16 waves do not hold the row otherwise.
 Shape row_shape(int64_t c, int dtype) {
   const int wide = dtype == DYRA_BF16 ? (c > 512 ? 2 : 1) : (c > 8192 ? 2 : 1);
-  int w = 1;
-  while ((int64_t)w * 64 * 8 * wide < c) w *= 2;
-  return {w, wide};
+  const int w = (int)((c + 512 * wide - 1) / (512 * wide));
+  return {w <= 8 ? w : 16, wide};
 }
 
 struct Split {
@@ -580,10 +580,11 @@ Split split_rows(int64_t n, int rpb, int64_t most) {
 // registers' limit; more would only add partial rows.  Two of 4 waves a CU
 // measure the same, four 50 us against 43 (4099 x 4096, both norms, gate).
 constexpr int BWAVES = 8, BWGS = 256;
-// Forward: 4096 workgroups and 512 measure alike (44 and 45 us at 32928 x
-// 1024), 1024 50 us.
-constexpr int FWGS = 4096;
-int backward_rpb(int waves) { return waves >= BWAVES ? 1 : BWAVES / waves; }
+// Forward: up to 4 waves a row 4096 workgroups (25 us at 4099 x 4096; 512:
+// 25, 1024: 29), above two a CU, which is what fits (28 us at 2000 x 8192 with
+// 512, 34 with 4096).
+constexpr int forward_wgs(int waves) { return waves > 4 ? 512 : 4096; }
+constexpr int backward_rpb(int waves) { return waves > BWAVES / 2 ? 1 : BWAVES / waves; }
 Split backward_split(int64_t n, int waves) { return split_rows(n, backward_rpb(waves), BWGS); }
 
 int flags_of(const dyra_block_norm& p) {
@@ -646,57 +647,63 @@ NormArgs norm_args(const dyra_block_norm& p, int64_t n, int64_t B, const int32_t
   return a;
 }
 
-template <typename T>
-void launch_forward(NormArgs a, hipStream_t st) {
-  const Shape sh = row_shape(a.c, sizeof(T) == 2 ? DYRA_BF16 : DYRA_F32);
-  const int rpb = sh.waves >= 4 ? 1 : 4 / sh.waves;
-  const Split s = split_rows(a.n, rpb, FWGS);
+template <typename T, int WPR, int NCH>
+void launch_forward_shape(NormArgs a, hipStream_t st) {
+  constexpr int RPB = WPR >= 3 ? 1 : 4 / WPR;
+  const Split s = split_rows(a.n, RPB, forward_wgs(WPR));
   a.rows = s.rows;
-  const dim3 grid((unsigned)s.wgs), nt((unsigned)(sh.waves * rpb * 64));
+  hipLaunchKernelGGL((norm_forward_kernel<T, WPR, NCH, RPB>), dim3((unsigned)s.wgs), dim3(WPR * RPB * 64), 0, st, a);
+}
+
+template <typename T, int F, int WPR, int NCH>
+void launch_backward_shape(const NormArgs& a, const Split& s, hipStream_t st) {
+  constexpr int RPB = backward_rpb(WPR);
+  hipLaunchKernelGGL((norm_backward_kernel<T, WPR, NCH, RPB, F>), dim3((unsigned)s.wgs), dim3(WPR * RPB * 64), 0, st, a);
+}
+
+// Calls f(waves, chunks), as constants, of the shape.
+template <typename T, class Fn>
+void with_shape(const Shape& sh, Fn&& f) {
   constexpr int N = sizeof(T) == 2 ? 2 : 1;   // chunks of the wide shapes
+  auto at = [&](auto w, auto n) { f(w, n); };
+  using std::integral_constant;
+  const integral_constant<int, N> n{};
   switch (sh.waves) {
     case 1:
-      if (sh.chunks == 1) hipLaunchKernelGGL((norm_forward_kernel<T, 1, 1, 4>), grid, nt, 0, st, a);
-      else if constexpr (N == 2) hipLaunchKernelGGL((norm_forward_kernel<T, 1, 2, 4>), grid, nt, 0, st, a);
+      if (sh.chunks == 1) at(integral_constant<int, 1>(), integral_constant<int, 1>());
+      else if constexpr (N == 2) at(integral_constant<int, 1>(), n);
       break;
-    case 2: hipLaunchKernelGGL((norm_forward_kernel<T, 2, N, 2>), grid, nt, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((norm_forward_kernel<T, 4, N, 1>), grid, nt, 0, st, a); break;
-    case 8: hipLaunchKernelGGL((norm_forward_kernel<T, 8, N, 1>), grid, nt, 0, st, a); break;
+    case 2: at(integral_constant<int, 2>(), n); break;
+    case 3: at(integral_constant<int, 3>(), n); break;
+    case 4: at(integral_constant<int, 4>(), n); break;
+    case 5: at(integral_constant<int, 5>(), n); break;
+    case 6: at(integral_constant<int, 6>(), n); break;
+    case 7: at(integral_constant<int, 7>(), n); break;
+    case 8: at(integral_constant<int, 8>(), n); break;
     default:
       if constexpr (N == 1) {
         if (sh.chunks == 1) {
-          hipLaunchKernelGGL((norm_forward_kernel<T, 16, 1, 1>), grid, nt, 0, st, a);
+          at(integral_constant<int, 16>(), integral_constant<int, 1>());
           break;
         }
       }
-      hipLaunchKernelGGL((norm_forward_kernel<T, 16, 2, 1>), grid, nt, 0, st, a);
+      at(integral_constant<int, 16>(), integral_constant<int, 2>());
       break;
   }
 }
 
+template <typename T>
+void launch_forward(const NormArgs& a, hipStream_t st) {
+  with_shape<T>(row_shape(a.c, sizeof(T) == 2 ? DYRA_BF16 : DYRA_F32), [&](auto w, auto n) {
+    launch_forward_shape<T, decltype(w)::value, decltype(n)::value>(a, st);
+  });
+}
+
 template <typename T, int F>
 void launch_backward_f(const NormArgs& a, const Split& s, hipStream_t st) {
-  const Shape sh = row_shape(a.c, sizeof(T) == 2 ? DYRA_BF16 : DYRA_F32);
-  const dim3 grid((unsigned)s.wgs), nt((unsigned)(sh.waves * s.rpb * 64));
-  constexpr int N = sizeof(T) == 2 ? 2 : 1, W = BWAVES;
-  switch (sh.waves) {
-    case 1:
-      if (sh.chunks == 1) hipLaunchKernelGGL((norm_backward_kernel<T, 1, 1, W, F>), grid, nt, 0, st, a);
-      else if constexpr (N == 2) hipLaunchKernelGGL((norm_backward_kernel<T, 1, 2, W, F>), grid, nt, 0, st, a);
-      break;
-    case 2: hipLaunchKernelGGL((norm_backward_kernel<T, 2, N, W / 2, F>), grid, nt, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((norm_backward_kernel<T, 4, N, W / 4, F>), grid, nt, 0, st, a); break;
-    case 8: hipLaunchKernelGGL((norm_backward_kernel<T, 8, N, 1, F>), grid, nt, 0, st, a); break;
-    default:
-      if constexpr (N == 1) {
-        if (sh.chunks == 1) {
-          hipLaunchKernelGGL((norm_backward_kernel<T, 16, 1, 1, F>), grid, nt, 0, st, a);
-          break;
-        }
-      }
-      hipLaunchKernelGGL((norm_backward_kernel<T, 16, 2, 1, F>), grid, nt, 0, st, a);
-      break;
-  }
+  with_shape<T>(row_shape(a.c, sizeof(T) == 2 ? DYRA_BF16 : DYRA_F32), [&](auto w, auto n) {
+    launch_backward_shape<T, F, decltype(w)::value, decltype(n)::value>(a, s, st);
+  });
 }
 
 template <typename T>

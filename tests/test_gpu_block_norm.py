@@ -206,7 +206,8 @@ def test_every_kind_matches_the_oracle(pre, post, gate, biases):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("c", [8, 64, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384])
+@pytest.mark.parametrize("c", [8, 64, 512, 520, 1024, 1032, 2048, 2056, 2600, 4096, 4104, 4232, 5640,
+                               7000, 8192, 8200, 16384])
 def test_every_width_class(c, dtype):
     run(make([5, 4], c, "layer", "rms", "request", dtype, seed=c, biases=True), dtype)
     run(make([1], c, "rms", "none", "none", dtype, seed=c + 1, weights=False), dtype)
