@@ -88,10 +88,13 @@ OUTPUT_KERNEL = {0: "s6_lowrank_kernel (fused T V + L R_b + bias)",
 
 
 def kernel_source_hash():
+    """Of the sources the forward's kernels are built from (the adapters' and
+    the block norms' kernels are translation units of their own)."""
+    other = ("host_linalg.h", "adapter_kernels.hip", "block_norm_kernels.hip")
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "input_adaptive_rank_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".hip", ".h")) and f not in ("host_linalg.h",):
+        if f.endswith((".hip", ".h")) and f not in other:
             with open(os.path.join(csrc, f), "rb") as fh:
                 h.update(fh.read())
     return h.hexdigest()[:16]
