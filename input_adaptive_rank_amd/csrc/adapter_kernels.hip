@@ -136,7 +136,6 @@ __device__ __forceinline__ void scan3(int (&v)[3], int* wave_sums, int waves) { 
   for (int w = 0; w < min(wave, waves); ++w)
 #pragma unroll
     for (int q = 0; q < 3; ++q) v[q] += wave_sums[w * 3 + q];
-  __syncthreads();
 }
 
 // The weights of a slot as operands: block (rb, kb) is rows 16 rb .. + 15 and
@@ -211,10 +210,23 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, 
   const int B = q.count(), S = q.slots, stride = group_wgs * GROUP_NT;
   // rows of each slot
   for (int s = tid; s <= S; s += GROUP_NT) rows_of[s] = 0;
+  // 1024 requests at a time; the first are loaded once
+  int id, len;
+  auto load = [&](int b0) {
+    const int b = b0 + tid, end = min(b0 + GROUP_NT, B);
+    id = b < end ? q.id(b) : S + 1;
+    len = b < end ? q.len(b) : 0;
+    ids[tid] = id;
+    lens[tid] = len;
+    offs[tid] = q.lo(min(b, end));
+    if (tid == 0) offs[GROUP_NT] = q.lo(end);
+  };
+  load(0);
   __syncthreads();
-  for (int b = tid; b < B; b += GROUP_NT) {
-    const int len = q.len(b);
-    if (len) atomicAdd(&rows_of[q.id(b)], len);
+  if (len) atomicAdd(&rows_of[id], len);
+  for (int b = GROUP_NT + tid; b < B; b += GROUP_NT) {
+    const int more = q.len(b);
+    if (more) atomicAdd(&rows_of[q.id(b)], more);
   }
   __syncthreads();
   // first tile and first chunk of each slot; thread t sums slots [t E, (t + 1) E)
@@ -271,30 +283,35 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, 
     }
     for (int s = wg * GROUP_NT + tid; s <= S; s += stride) g.slot_chunk[s] = chunk0[s];
   }
-  // rows, 1024 requests at a time
+  // rows
   const int64_t places = (int64_t)g.tile_cap * g.tile;
+  const int wave = tid >> 6;
   for (int b0 = 0; b0 < B; b0 += GROUP_NT) {
-    const int nb = min(B - b0, GROUP_NT), b = b0 + tid;
-    __syncthreads();
-    const int id = tid < nb ? q.id(b) : S + 1, len = tid < nb ? q.len(b) : 0;
-    ids[tid] = id;
-    lens[tid] = len;
-    offs[tid] = tid < nb ? q.lo(b) : q.lo(b0 + nb);
-    if (tid == 0) offs[GROUP_NT] = q.lo(b0 + nb);
-    __syncthreads();
-    int before = 0;   // rows of the same slot in earlier requests
+    const int nb = min(B - b0, GROUP_NT);
+    if (b0) {
+      __syncthreads();
+      load(b0);
+      __syncthreads();
+    }
+    int before = 0;   // rows of the same slot in earlier requests of the wave
     if (tid < nb) {
       const int4 *i4 = reinterpret_cast<const int4*>(ids), *l4 = reinterpret_cast<const int4*>(lens);
 #pragma unroll 4
-      for (int u = 0; u < (tid >> 2); ++u) {
+      for (int u = wave * 16; u < (tid >> 2); ++u) {
         const int4 a = i4[u], l = l4[u];
         before += (a.x == id ? l.x : 0) + (a.y == id ? l.y : 0) + (a.z == id ? l.z : 0) + (a.w == id ? l.w : 0);
       }
       for (int u = tid & ~3; u < tid; ++u) before += ids[u] == id ? lens[u] : 0;
     }
-    gpos[tid] = tid < nb ? run[id] + before : 0;
-    __syncthreads();
-    if (len) atomicAdd(&run[id], len);
+    // one wave after the other takes its places: at 192 requests 2 us less than
+    // counting all earlier requests
+    for (int w = 0; w * 64 < nb; ++w) {
+      if (wave == w && tid < nb) {
+        gpos[tid] = run[id] + before;
+        if (len) atomicAdd(&run[id], len);
+      }
+      __syncthreads();
+    }
     const int lo = offs[0], hi = offs[nb];
     for (int t = lo + wg * GROUP_NT + tid; t < hi; t += stride) {
       int a = 0, z = nb;   // the last request starting at or before row t (empty ones before it share its start)
@@ -611,6 +628,12 @@ struct ExpandArgs {
 };
 
 constexpr int EXPAND_COLS = 256;   // columns of a workgroup, 64 of each wave
+// Row blocks that follow each other on one XCD, which takes all their columns
+// (P and the row list are in its L2 then).  An eighth of the list to each XCD
+// would leave the last ones the places past the last tile: 5003 x 4096 of 16
+// slots 24.5 us against 22.5, with runs of 1 and 4 22.8 and 22.3; 192 rows of 64
+// slots 27 against 26.5, 26.8 and 27.9.
+constexpr int XCD_RUN = 2;
 
 // One workgroup: 16 RT rows of a tile, 256 columns.  P is summed over its
 // slices, scaled and put in LDS once: in bf16 as two terms, hi + lo, so that
@@ -632,8 +655,9 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p, JoinArgs join
   static_assert(sizeof(ds) >= JOIN_LDS * sizeof(float), "the join's LDS");
   // a backward pass joins the weight gradients in the same launch
   if ((int)blockIdx.x < join_wgs) return join_block(join, blockIdx.x, ds[0]);
-  const int id = xcd_tile_id(blockIdx.x - join_wgs, gridDim.x - join_wgs);
-  const int cb = id % p.col_blocks, part = id / p.col_blocks, sub = part % p.sub, tile = part / p.sub;
+  const int id = blockIdx.x - join_wgs, at = (id >> 3) / p.col_blocks, cb = (id >> 3) % p.col_blocks;
+  const int part = (at / XCD_RUN * 8 + (id & 7)) * XCD_RUN + at % XCD_RUN, sub = part % p.sub, tile = part / p.sub;
+  if (tile >= p.tiles) return;
   const Tile t = p.g.tiles[tile];
   if (t.count <= sub * 16 * RT) return;
   const bool none = t.slot >= p.slots;
@@ -1152,20 +1176,18 @@ void launch_group(const Requests& rq, const Grouped& g, const Pack<T>& a, const 
                      (int)na);
 }
 
-template <typename T, int RT>
-void launch_shrink_rt(const ShrinkArgs& a, unsigned grid, hipStream_t st) {
-  const dim3 nt(SHRINK_WAVES * 64);
-  if (a.r <= 16) hipLaunchKernelGGL((shrink_kernel<T, RT, 1>), dim3(grid), nt, 0, st, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((shrink_kernel<T, RT, 2>), dim3(grid), nt, 0, st, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((shrink_kernel<T, RT, 4>), dim3(grid), nt, 0, st, a);
-  else hipLaunchKernelGGL((shrink_kernel<T, RT, 8>), dim3(grid), nt, 0, st, a);
+template <typename T, int RT, int CT>
+void launch_shrink_as(const ShrinkArgs& a, hipStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)a.tiles * a.sub * a.KS);
+  hipLaunchKernelGGL((shrink_kernel<T, RT, CT>), dim3(grid), dim3(SHRINK_WAVES * 64), 0, st, a);
 }
 
 template <typename T>
 void launch_shrink(const ShrinkArgs& a, int rt, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.tiles * a.sub * a.KS);
-  if (rt == 1) launch_shrink_rt<T, 1>(a, grid, st);
-  else launch_shrink_rt<T, 2>(a, grid, st);
+  if (a.r <= 16) launch_shrink_as<T, 1, 1>(a, st);
+  else if (a.r <= 32) launch_shrink_as<T, 1, 2>(a, st);
+  else if (a.r <= 64) rt == 1 ? launch_shrink_as<T, 1, 4>(a, st) : launch_shrink_as<T, 2, 4>(a, st);
+  else rt == 1 ? launch_shrink_as<T, 1, 8>(a, st) : launch_shrink_as<T, 2, 8>(a, st);
 }
 
 template <typename T, int RT>
@@ -1188,7 +1210,7 @@ void launch_expand(const ExpandArgs& a, int ert, const JoinArgs* join, hipStream
     j = *join;
     wgs = (j.blocks[0] + j.blocks[1] + 7) & ~7;   // the XCDs of the others stay as they are
   }
-  const unsigned grid = (unsigned)((int64_t)a.tiles * a.sub * a.col_blocks + wgs);
+  const unsigned grid = (unsigned)(cdiv64((int64_t)a.tiles * a.sub, 8 * XCD_RUN) * (8 * XCD_RUN) * a.col_blocks + wgs);
   if (ert == 1) launch_expand_rt<T, 1>(a, j, wgs, grid, st);
   else launch_expand_rt<T, 2>(a, j, wgs, grid, st);
 }
@@ -1297,11 +1319,11 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
 bool grids_fit(const dyra_adapters& ad, const Plan& q, bool backward) {
   const int64_t most = INT_MAX, c = std::max(ad.c1, ad.c2);
   const int64_t packs = (cdiv64(ad.c1, 16) + cdiv64(ad.c2, 16)) * cdiv64(ad.r, 16) / PACK_BLOCKS + 2;
-  if (q.tile_cap * q.sub * q.ks > most || q.tile_cap * 4 * cdiv64(c, EXPAND_COLS) > most) return false;
+  if (q.tile_cap * q.sub * q.ks > most || (q.tile_cap * 4 + 8 * XCD_RUN) * cdiv64(c, EXPAND_COLS) > most) return false;
   if (q.packed && packs * ad.slots + 64 > most) return false;
   if (!backward) return true;
   return (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots +
-                 q.tile_cap * 4 * cdiv64(ad.c1, EXPAND_COLS) + 8 <= most &&
+                 (q.tile_cap * 4 + 8 * XCD_RUN) * cdiv64(ad.c1, EXPAND_COLS) + 8 <= most &&
          (cdiv64(ad.c1, 256) + cdiv64(ad.c2, 256)) * 2 * q.chunk_cap <= most;
 }
 
