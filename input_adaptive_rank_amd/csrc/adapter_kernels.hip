@@ -418,84 +418,128 @@ __device__ __forceinline__ void with_blocks(int n, F&& f) {
   }
 }
 
-// k-steps s0 .. s1 - 1 of a wave's RT row blocks by N weight blocks, the
-// operands of D - 1 steps in flight.  No load is conditional: behind a branch
-// the compiler could not count the loads in flight and would wait for all of
-// them.  Steps and rows past the end repeat the last, and the one step that K
-// may end in stands by itself.
-template <typename T, int RT, int N, int CT, int D>
-__device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* const (&xr)[RT], const T* w,
-                                             const ShrinkArgs& p, int i, int g, int s0, int s1, int cts) {
-  constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K;
+// Lines u0 .. u1 - 1 (128 bytes of each row, two k-steps) of a wave's RT row
+// blocks by N weight blocks, the next line in flight.  Eight lanes load a row's
+// line; through LDS (of the wave alone, no barrier) its chunks come to the
+// lanes that hold them as operands.  Loaded straight into place, an operand is
+// 16 rows in 16 neighbouring lanes, and whichever 4 lanes the address unit
+// takes together want 4 lines: 32928 x 4096 at r = 64 97 us against 92, 5003 x
+// 4096 at r = 32 12.4 and 11.0, 1031 x 1024 in fp32 8.6 and 6.2.  Three lines
+// in flight spill.  No load is conditional: behind a branch the compiler could
+// not count the loads in flight and would wait for all of them.  Lines and
+// rows past the end repeat the last, and the one line that K may end in stands
+// by itself.
+template <typename T, int RT, int N, int CT>
+__device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* const (&xr)[RT][2], const T* w, char* lds,
+                                             const ShrinkArgs& p, int lane, int u0, int u1, int cts) {
+  constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, LINE = 2 * KSTEP, D = 2;
+  const int i = lane & 15, g = lane >> 4, chunk = lane & 7;
   const int wstep = p.packed ? cts * 64 * KPC : KSTEP;
   int64_t wr[N];
 #pragma unroll
   for (int c = 0; c < N; ++c)   // rows past the pool's r repeat the last one; their sums are dropped
     wr[c] = p.packed ? (int64_t)min(c, cts - 1) * 64 * KPC : (int64_t)min(16 * c + i, p.r - 1) * p.K;
-  const bool ragged = (int64_t)s1 * KSTEP > p.K && s0 < s1;
-  const int n = s1 - s0 - (ragged ? 1 : 0);
+  const bool ragged = (int64_t)u1 * LINE > p.K && u0 < u1;
+  const int n = u1 - u0 - (ragged ? 1 : 0);
+  // chunk c of row r lies at place c ^ (r / 2 % 8) of the row's 128 bytes: 16 lanes reach all banks either way
+  char* to[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) to[h] = lds + (8 * h + (lane >> 3)) * 128 + (chunk ^ (4 * h + (lane >> 4))) * 16;
+  const char* from[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) from[k] = lds + i * 128 + ((4 * k + g) ^ (i >> 1)) * 16;
+  auto put = [&](const u32x4(&x)[RT][2]) {
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int a = 0; a < RT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4*>(to[h] + a * 2048) = x[a][h];
+    __builtin_amdgcn_wave_barrier();
+  };
+  auto mul = [&](int k, const uint4(&v)[N]) {
+#pragma unroll
+    for (int a = 0; a < RT; ++a) {
+      const uint4 x = *reinterpret_cast<const uint4*>(from[k] + a * 2048);
+#pragma unroll
+      for (int c = 0; c < N; ++c) Step<T>::mma(acc[a][c], x, v[c]);
+    }
+  };
   if (n > 0) {
-    uint4 x[D][RT], v[D][N];
-    auto load = [&](int d, int s) {
-      s = s0 + min(s, n - 1);
+    u32x4 x[D][RT][2];
+    uint4 v[D][2][N];
+    auto load = [&](int d, int u) {
+      u = u0 + min(u, n - 1);
 #pragma unroll
-      for (int a = 0; a < RT; ++a) x[d][a] = *reinterpret_cast<const uint4*>(xr[a] + (int64_t)s * KSTEP);
+      for (int a = 0; a < RT; ++a)
 #pragma unroll
-      for (int c = 0; c < N; ++c) v[d][c] = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)s * wstep);
+        for (int h = 0; h < 2; ++h) x[d][a][h] = *reinterpret_cast<const u32x4*>(xr[a][h] + (int64_t)u * LINE);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+          v[d][k][c] = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)(2 * u + k) * wstep);
     };
-    auto mul = [&](int d) {
-#pragma unroll
-      for (int c = 0; c < N; ++c)
-#pragma unroll
-        for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], x[d][a], v[d][c]);
+    auto line = [&](int d) {
+      put(x[d]);
+      mul(0, v[d][0]);
+      mul(1, v[d][1]);
     };
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(d, d);
-    int s = 0;
-    for (; s + D <= n; s += D)
+    int u = 0;
+    for (; u + D <= n; u += D)
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        load((d + D - 1) % D, s + d + D - 1);
-        mul(d);
+        load((d + D - 1) % D, u + d + D - 1);
+        line(d);
       }
 #pragma unroll
     for (int d = 0; d < D - 1; ++d)
-      if (s + d < n) mul(d);
+      if (u + d < n) line(d);
   }
   if (ragged) {
-    const int s = s1 - 1;
-    const bool in = (int64_t)s * KSTEP + g * KPC < p.K;
-    const int back = in ? 0 : g * KPC;   // lanes past K read the step's first chunk and use zeros
-    uint4 x[RT];
+    const int64_t k0 = (int64_t)(u1 - 1) * LINE;
+    const bool in = k0 + chunk * KPC < p.K;   // lanes past K read the line's first chunk and use zeros
+    u32x4 x[RT][2];
 #pragma unroll
-    for (int a = 0; a < RT; ++a) {
-      x[a] = *reinterpret_cast<const uint4*>(xr[a] + (int64_t)s * KSTEP - back);
-      x[a] = in ? x[a] : zero4();
-    }
+    for (int a = 0; a < RT; ++a)
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      uint4 v = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)s * wstep - (p.packed ? 0 : back));
-      v = in ? v : zero4();
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 u = *reinterpret_cast<const u32x4*>(xr[a][h] + k0 - (in ? 0 : chunk * KPC)), none = {0u, 0u, 0u, 0u};
+        x[a][h] = in ? u : none;
+      }
+    put(x);
 #pragma unroll
-      for (int a = 0; a < RT; ++a) Step<T>::mma(acc[a][c], x[a], v);
+    for (int k = 0; k < 2; ++k) {
+      if (k0 + k * KSTEP >= p.K) break;
+      const bool has = k0 + k * KSTEP + g * KPC < p.K;
+      const int back = has || p.packed ? 0 : g * KPC;
+      uint4 v[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        v[c] = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)(2 * (u1 - 1) + k) * wstep - back);
+        v[c] = has ? v[c] : zero4();
+      }
+      mul(k, v);
     }
   }
 }
 
 // One workgroup: 16 RT rows of one slot, one of KS slices of K, which its
-// waves divide again; their sums meet in LDS.  A wave reads X straight into
-// matrix operands, each 16-byte load one operand of 16 rows; the weights come
-// from the L2, one operand per 16 rank columns for every RT operands of X.
-// The loads of the next U k-steps are in flight while the present ones are
-// multiplied.
+// waves divide again; their sums meet in LDS.  The weights come from the L2,
+// one operand per 16 rank columns for every RT operands of X.
 template <typename T, int RT, int CT>
 __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kernel(ShrinkArgs p) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, W = SHRINK_WAVES;
   constexpr int CB = CT < 4 ? CT : 4;      // 16-column blocks joined at a time
-  __shared__ float red[W][CB][256];
+  // a wave's lines of X, then its part of the sums
+  constexpr int WAVE_LDS = 1024 * (2 * RT > CB ? 2 * RT : CB);
+  __shared__ __attribute__((aligned(16))) char lds[W][WAVE_LDS];
+  auto red = [&](int w, int c, int l) { return reinterpret_cast<f32x4*>(lds[w]) + c * 64 + l; };
   const int tile = blockIdx.x / (p.sub * p.KS), rem = blockIdx.x % (p.sub * p.KS);
   const int sub = rem / p.KS, ks = rem % p.KS;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15;
+  const int g = lane >> 4;
   const Tile t = p.g.tiles[tile];
   // the operands of the weight gradients are whole half tiles, zero past the rows
   if (t.count <= (p.Pf ? sub * 16 * RT & ~31 : sub * 16 * RT)) return;
@@ -509,17 +553,21 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kern
   f32x4 acc[RT][CT] = {};
   const int any = __shfl(row_of[0], 0);   // a row to read in the place of one that is not there
   if (rank > 0 && any >= 0) {
-    const T* xr[RT];
+    const T* xr[RT][2];
 #pragma unroll
     for (int a = 0; a < RT; ++a)
-      xr[a] = reinterpret_cast<const T*>(p.X) + (int64_t)(row_of[a] < 0 ? any : row_of[a]) * p.ldx + g * KPC;
-    const int steps = (int)cdiv64(p.K, KSTEP), per = (steps + p.KS * W - 1) / (p.KS * W);
-    const int s0 = (ks * W + wave) * per, s1 = min(s0 + per, steps);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = __shfl(row_of[a], 8 * h + (lane >> 3));
+        xr[a][h] = reinterpret_cast<const T*>(p.X) + (int64_t)(row < 0 ? any : row) * p.ldx + (lane & 7) * KPC;
+      }
+    const int steps = (int)cdiv64(p.K, KSTEP), lines = (steps + 1) >> 1, per = (lines + p.KS * W - 1) / (p.KS * W);
+    const int u0 = (ks * W + wave) * per, u1 = min(u0 + per, lines);
     const T* wbase = reinterpret_cast<const T*>(p.W) + (p.packed ? (int64_t)t.slot * steps * cts * 64 * KPC + lane * KPC
                                                                  : (int64_t)t.slot * p.r * p.K + g * KPC);
     with_blocks<CT>(nct, [&](auto blocks) {
       constexpr int N = decltype(blocks)::value;
-      shrink_slice<T, RT, N, CT, (RT * N > 8 ? 2 : 3)>(acc, xr, wbase, p, i, g, s0, s1, cts);
+      shrink_slice<T, RT, N, CT>(acc, xr, wbase, lds[wave], p, lane, u0, u1, cts);
     });
   }
   // join the waves: D[row][j] of a 16x16 block sits at lane j + 16 (row / 4), register row % 4
@@ -529,10 +577,10 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kern
 #pragma unroll
     for (int cb = 0; cb < CT; cb += CB) {
       if (16 * cb >= p.r) break;
-      if (a + cb) __syncthreads();
+      if (a + cb) __syncthreads();   // the wave's own lines before it need none
 #pragma unroll
       for (int c = 0; c < CB; ++c)
-        if (cb + c < nct) *reinterpret_cast<f32x4*>(&red[wave][c][lane * 4]) = acc[a][cb + c];
+        if (cb + c < nct) *red(wave, c, lane) = acc[a][cb + c];
       __syncthreads();
       // four rows of one column a thread: what one lane of the product holds
       for (int e = tid; e < 64 * CB; e += W * 64) {
@@ -540,7 +588,7 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kern
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         if (j < rank)
 #pragma unroll
-          for (int w = 0; w < W; ++w) v += *reinterpret_cast<const f32x4*>(&red[w][e >> 6][l * 4]);
+          for (int w = 0; w < W; ++w) v += *red(w, e >> 6, l);
         int rows[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) rows[q] = __shfl(row_of[a], 4 * q4 + q);
@@ -1079,7 +1127,7 @@ struct Plan {
 int shrink_split(int64_t wgs, int64_t K, int dtype) {
   const int64_t steps = cdiv64(K, dtype == DYRA_BF16 ? 32 : 16);
   int64_t ks = cdiv64(512, wgs);                              // two workgroups per CU
-  ks = std::min<int64_t>(ks, cdiv64(steps, 2 * SHRINK_WAVES));   // at least two k-steps per wave
+  ks = std::min<int64_t>(ks, cdiv64(steps, 2 * SHRINK_WAVES));   // at least one line per wave
   return (int)std::max<int64_t>(1, std::min<int64_t>(ks, 4));   // more slices cost the expand more than they save
 }
 
