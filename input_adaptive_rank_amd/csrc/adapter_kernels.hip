@@ -193,7 +193,9 @@ __device__ void pack_blocks(const Pack<T>& j, const Requests& q, int id) {
 // call.  Each of the first `group_wgs` workgroups does the whole sort (a few
 // thousand cycles for up to 1024 requests) and writes its share of the row
 // list and of the tile lists, so no workgroup waits for another; the others
-// pack weights.
+// pack weights.  Bound by its dependent steps, one workgroup deep: 7 us at up to
+// 200 requests and 33000 rows, of which the packing (16 slots of 4096 x 32) and
+// the row list are hidden.
 template <typename T>
 __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, int group_wgs, Pack<T> first,
                                                          Pack<T> second, int first_wgs) {
@@ -527,7 +529,13 @@ __device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* cons
 
 // One workgroup: 16 RT rows of one slot, one of KS slices of K, which its
 // waves divide again; their sums meet in LDS.  The weights come from the L2,
-// one operand per 16 rank columns for every RT operands of X.
+// one operand per 16 rank columns for every RT operands of X.  Bound by the
+// rows: 32928 x 1024, r = 16 13.7 us (4.9 TB/s, X in the Infinity Cache);
+// 32928 x 4096, r = 64, with the gradients' operands 91 us (270 MB read, 50
+// written: 3.5 TB/s), where a tile's 512 KB of weights come from the L2 again
+// for every 32 rows and the last third of the workgroups is a second round.
+// Tiles of 64 rows with the weights in LDS were slower (125 us where this form
+// took 110), as was RT = 4.
 template <typename T, int RT, int CT>
 __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kernel(ShrinkArgs p) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, W = SHRINK_WAVES;
@@ -603,7 +611,10 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kern
 
 // Sums the chunks of each slot in order: dA[s][j][c], and dB[s][c][j]
 // (transposed through LDS).  Rows past a slot's rank, and slots without rows,
-// are zero.  One workgroup: 64 columns and 16 rank columns of one slot.
+// are zero.  One workgroup: 64 columns and 16 rank columns of one slot, so that
+// even one slot's join is spread over the card (13 us against 86 with a
+// workgroup to all rank columns, 4 slots of (1024 + 4096) x 64); it rides in the
+// expand's launch, beside rows that do not wait for it.
 struct JoinArgs {
   const float* part[2];   // dB's, dA's
   float* out[2];
@@ -690,6 +701,10 @@ constexpr int XCD_RUN = 2;
 // 4 columns of one row in a lane; through LDS (wave by wave, no barrier) the
 // results come to lanes that hold 16 bytes of a row, 8 lanes to a 128-byte
 // line, the form in which base is read and the result written.
+// Bound by base and result: 32928 x 4096, r = 16 100 us (540 MB, 5.4 TB/s); with
+// few rows a slot by the weights: 192 rows of 61 slots, 12288 columns, ranks to
+// 64, 26 us (about 65 MB).  A persistent form with the next tile's rows in flight
+// was slower (134 us; 33): its registers cost a workgroup per CU.
 template <typename T, int RT, int NK>
 __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p, JoinArgs join, int join_wgs) {
   constexpr bool BF = sizeof(T) == 2;
@@ -890,7 +905,8 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&v)[Step<T>::KPC])
 // row's whole H again from the L2: r c1 weights, which one CU reads in about
 // a microsecond at r = 16, c1 = 4096, where two more launches cost several.
 // The waves are JG groups of 16 rank columns (JG 16 >= r) times W / JG parts
-// of c1; weights are read a row of A at a time, 1 KB a wave.
+// of c1; weights are read a row of A at a time, 1 KB a wave.  Bound by latency:
+// 4 rows, 4096 -> 4096, r = 16 6.6 us.
 template <typename T, int JG>
 __global__ __launch_bounds__(DIRECT_NT, 4) void direct_kernel(DirectArgs p) {
   constexpr int KPC = Step<T>::KPC, W = DIRECT_NT / 64, KG = W / JG, JB = 16;
@@ -989,6 +1005,10 @@ template <typename T> constexpr int grad_cols() { return sizeof(T) == 2 ? 128 : 
 // take one row of each lane group as it is.  The row factors are operands
 // already; the four waves share them through LDS, a half tile at a time,
 // double-buffered.  Both are in flight a half tile ahead of the products.
+// Chunks keep the sums in order without atomics; their partial sums are joined
+// by join_block.  Bound by the rows' loads: X 32928 x 1024 and dY x 4096, r = 64
+// 84 us (337 MB, 4.0 TB/s) at two workgroups a CU, which the sums' registers
+// allow.
 template <typename T, int CT>
 __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
   constexpr bool BF = sizeof(T) == 2;

@@ -11,8 +11,8 @@
 // memory bounds both.  A row stays in registers from its load to its store
 // (fp32, rounded once), so each operand crosses memory once.  Measured, bf16:
 // forward 32928 x 1024 (layer norm, channel gate) 44 us, 6.1 TB/s; its
-// backward 85 + 5 us for the joined column sums, 4.5 TB/s; backward 4099 x
-// 4096 (both norms, a gate per request) 43 + 5 us, 4.2 TB/s.  A copy of the
+// backward 74 + 5 us for the joined column sums, 5.1 TB/s; backward 4099 x
+// 4096 (both norms, a gate per request) 44 + 5 us, 4.1 TB/s.  A copy of the
 // first size runs at 5.2 TB/s, of 2 GiB at 4.85.
 #include <hip/hip_runtime.h>
 
