@@ -467,37 +467,47 @@ __device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* cons
     }
   };
   if (n > 0) {
+    // The next line's weights are loaded with its rows, except where they would
+    // spill (r = 128, backward at 32928 rows: 349 us against 357).
+    constexpr bool AHEAD = RT * N < 16;
+    constexpr int DW = AHEAD ? D : 1;
     u32x4 x[D][RT][2];
-    uint4 v[D][2][N];
-    auto load = [&](int d, int u) {
+    uint4 v[DW][2][N];
+    auto load_w = [&](int d, int u) {
+      u = u0 + min(u, n - 1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+          v[d % DW][k][c] = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)(2 * u + k) * wstep);
+    };
+    auto load_x = [&](int d, int u) {
       u = u0 + min(u, n - 1);
 #pragma unroll
       for (int a = 0; a < RT; ++a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) x[d][a][h] = *reinterpret_cast<const u32x4*>(xr[a][h] + (int64_t)u * LINE);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int c = 0; c < N; ++c)
-          v[d][k][c] = *reinterpret_cast<const uint4*>(w + wr[c] + (int64_t)(2 * u + k) * wstep);
     };
     auto line = [&](int d) {
       put(x[d]);
-      mul(0, v[d][0]);
-      mul(1, v[d][1]);
+      mul(0, v[d % DW][0]);
+      mul(1, v[d % DW][1]);
     };
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d) load(d, d);
+    load_x(0, 0);
+    if (AHEAD) load_w(0, 0);
     int u = 0;
     for (; u + D <= n; u += D)
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        load((d + D - 1) % D, u + d + D - 1);
+        if (!AHEAD) load_w(d, u + d);
+        load_x((d + 1) % D, u + d + 1);
+        if (AHEAD) load_w((d + 1) % D, u + d + 1);
         line(d);
       }
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-      if (u + d < n) line(d);
+    if (u < n) {
+      if (!AHEAD) load_w(0, u);
+      line(0);
+    }
   }
   if (ragged) {
     const int64_t k0 = (int64_t)(u1 - 1) * LINE;
