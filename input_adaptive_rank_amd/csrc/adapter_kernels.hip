@@ -631,9 +631,20 @@ struct JoinArgs {
   int64_t C[2];
   int32_t blocks[2];
   const int32_t* rank;
-  const int32_t* slot_chunk;
-  int32_t r, chunk_cap;
+  int32_t r;
+  Grouped g;
 };
+
+// The chunks of a slot; one that is alone needs no join: its sums are the
+// gradients, which grad_kernel writes itself (1500 rows of 60 slots at r = 128
+// 250 us against 370, whose time is the 250 MB of gradients).
+__device__ __forceinline__ void slot_chunks(const Grouped& g, int slot, int& lo, int& hi) {
+  lo = min(max(g.slot_chunk[slot], 0), g.chunk_cap);
+  hi = min(g.slot_chunk[slot + 1], g.chunk_cap);
+}
+__device__ __forceinline__ bool lone_chunk(const Grouped& g, int slot, int lo, int hi) {
+  return hi - lo == 1 && g.chunks[lo].slot == slot && g.chunks[lo].tiles > 0;
+}
 
 constexpr int JOIN_LDS = 16 * 68;
 
@@ -645,11 +656,14 @@ __device__ __forceinline__ void join_block(const JoinArgs& p, int id, float* lds
   const int cbs = (int)cdiv64(C, 64), rbs = (p.r + 15) >> 4;
   const int cb = id % cbs, rb = id / cbs % rbs, slot = id / cbs / rbs;
   const int rank = p.rank ? min(max(p.rank[slot], 0), p.r) : p.r;
-  const int lo = min(max(p.slot_chunk[slot], 0), p.chunk_cap), hi = min(p.slot_chunk[slot + 1], p.chunk_cap);
+  int lo, hi;
+  slot_chunks(p.g, slot, lo, hi);
+  const bool lone = lone_chunk(p.g, slot, lo, hi);
+  if (lone && rb * 16 + 16 <= rank) return;
   const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4, j = rb * 16 + y;
   const int64_t c = (int64_t)cb * 64 + x, step = (int64_t)p.r * C;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (j < rank && c < C) {
+  if (j < rank && c < C && !lone) {
     const float* s = p.part[which] + (int64_t)lo * step + (int64_t)j * C + c;
 #pragma unroll 8
     for (int k = lo; k < hi; ++k, s += step) {
@@ -661,7 +675,7 @@ __device__ __forceinline__ void join_block(const JoinArgs& p, int id, float* lds
     }
   }
   if (which) {
-    if (j < p.r && c < C) *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
+    if (j < p.r && c < C && !(lone && j < rank)) *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
     return;
   }
   *reinterpret_cast<float4*>(&lds[y * 68 + x]) = v;
@@ -669,7 +683,7 @@ __device__ __forceinline__ void join_block(const JoinArgs& p, int id, float* lds
   // 4 rank columns of a column a thread
   const int cc = threadIdx.x >> 2, j4 = (threadIdx.x & 3) * 4;
   const int64_t oc = (int64_t)cb * 64 + cc;
-  if (oc < C && rb * 16 + j4 < p.r)
+  if (oc < C && rb * 16 + j4 < p.r && !(lone && rb * 16 + j4 < rank))
     *reinterpret_cast<float4*>(p.out[0] + ((int64_t)slot * C + oc) * p.r + rb * 16 + j4) =
         make_float4(lds[j4 * 68 + cc], lds[(j4 + 1) * 68 + cc], lds[(j4 + 2) * 68 + cc], lds[(j4 + 3) * 68 + cc]);
 }
@@ -995,6 +1009,7 @@ struct GradSide {
   const void* V;       // [n][ldv]
   const void* Pf;      // left operands, written by the shrink
   float* part;         // [chunk_cap][r][C]
+  float* out;          // side 0: dB [slots][C][r], side 1: dA [slots][r][C]
   int64_t ldv, C;
   int32_t col_blocks;
 };
@@ -1015,8 +1030,8 @@ template <typename T> constexpr int grad_cols() { return sizeof(T) == 2 ? 128 : 
 // take one row of each lane group as it is.  The row factors are operands
 // already; the four waves share them through LDS, a half tile at a time,
 // double-buffered.  Both are in flight a half tile ahead of the products.
-// Chunks keep the sums in order without atomics; their partial sums are joined
-// by join_block.  Bound by the rows' loads: X 32928 x 1024 and dY x 4096, r = 64
+// Chunks keep the sums in order without atomics; the partial sums of a slot
+// with several are joined by join_block.  Bound by the rows' loads: X 32928 x 1024 and dY x 4096, r = 64
 // 84 us (337 MB, 4.0 TB/s) at two workgroups a CU, which the sums' registers
 // allow.
 template <typename T, int CT>
@@ -1125,7 +1140,24 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
     }
   }
   if (!live) return;
-  float* out = v.part + (int64_t)chunk * p.r * v.C;
+  int lo, hi;
+  slot_chunks(p.g, t.slot, lo, hi);
+  const bool lone = lone_chunk(p.g, t.slot, lo, hi);
+  if (lone && !which) {   // dB: 4 rank columns of a column a store, zero past the rank
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const int j = j0 + 16 * c + 4 * g;
+      if (j >= rank) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const f32x4 a = acc[c][e];
+        *reinterpret_cast<float4*>(v.out + ((int64_t)t.slot * v.C + col + e) * p.r + j) =
+            make_float4(a[0], j + 1 < rank ? a[1] : 0.f, j + 2 < rank ? a[2] : 0.f, j + 3 < rank ? a[3] : 0.f);
+      }
+    }
+    return;
+  }
+  float* out = lone ? v.out + (int64_t)t.slot * p.r * v.C : v.part + (int64_t)chunk * p.r * v.C;
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -1363,8 +1395,8 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
     float *pdA = reinterpret_cast<float*>(ws + q.partA), *pdB = reinterpret_cast<float*>(ws + q.partB);
     const int cols = 4 * grad_cols<T>();
     if (rq.n) {
-      GradArgs ga{{{dY, ws + q.Hf, pdB, lddy, ad.c2, (int32_t)cdiv64(ad.c2, cols)},
-                   {X, ws + q.Pf, pdA, ldx, ad.c1, (int32_t)cdiv64(ad.c1, cols)}},
+      GradArgs ga{{{dY, ws + q.Hf, pdB, dB, lddy, ad.c2, (int32_t)cdiv64(ad.c2, cols)},
+                   {X, ws + q.Pf, pdA, dA, ldx, ad.c1, (int32_t)cdiv64(ad.c1, cols)}},
                   ad.rank, rq.n, ad.r, ad.slots, (int32_t)q.chunk_cap, 1, g};
       if (ad.r <= 16) launch_grad<T, 1>(ga, st);
       else if (ad.r <= 32) launch_grad<T, 2>(ga, st);
@@ -1372,8 +1404,7 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
     }
     const int64_t rbs = cdiv64(ad.r, 16);
     const int64_t b0 = cdiv64(ad.c2, 64) * rbs * ad.slots, b1 = cdiv64(ad.c1, 64) * rbs * ad.slots;
-    join = JoinArgs{{pdB, pdA}, {dB, dA}, {ad.c2, ad.c1}, {(int32_t)b0, (int32_t)b1}, ad.rank, g.slot_chunk, ad.r,
-                    (int32_t)q.chunk_cap};
+    join = JoinArgs{{pdB, pdA}, {dB, dA}, {ad.c2, ad.c1}, {(int32_t)b0, (int32_t)b1}, ad.rank, ad.r, g};
     if (!dX || !rq.n)
       hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(b0 + b1)), dim3(256), 0, st, join);
   }

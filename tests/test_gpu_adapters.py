@@ -146,6 +146,24 @@ def test_forward_and_backward_match_the_oracle(name, dtype):
     assert none_x is None and torch.equal(dA, grads[1]) and torch.equal(dB, grads[2])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("r", [16, 72])
+def test_gradients_of_slots_with_one_run_of_rows_and_with_many(r, dtype):
+    """Slots of a few rows beside slots of many, ranks that end inside a
+    block of 16 or of 4, into memory that held NaN."""
+    import torch
+    ranks = [r, 0, r - 3, r, 5, r - 8, r]
+    lens, ids = [3, 700, 64, 1, 20, 500, 9, 65], [0, 1, 2, 4, 1, 3, 5, 2]   # slot 6 has no row
+    case = make(lens, ids, 264, 520, r, 7, dtype, seed=r, ranks=ranks)
+    d = put(case, dtype)
+    _, H = run_forward(d, save_h=True)
+    dA = torch.full(d["A"].shape, float("nan"), dtype=torch.float32, device="cuda")
+    dB = torch.full(d["B"].shape, float("nan"), dtype=torch.float32, device="cuda")
+    grads = run_backward(d, H, dX_base=d["dX_base"], dA=dA, dB=dB)
+    torch.cuda.synchronize()
+    check_backward(case, dtype, grads, case["dX_base"], host(H))
+
+
 def test_many_requests_and_slots():
     """More requests than a workgroup sorts at once, more slots than rows of a tile."""
     import torch
