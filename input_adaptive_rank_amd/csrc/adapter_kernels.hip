@@ -675,7 +675,8 @@ __device__ __forceinline__ void join_block(const JoinArgs& p, int id, float* lds
     }
   }
   if (which) {
-    if (j < p.r && c < C && !(lone && j < rank)) *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
+    if (j < p.r && c < C && !(lone && j < rank))
+      *reinterpret_cast<float4*>(p.out[1] + ((int64_t)slot * p.r + j) * C + c) = v;
     return;
   }
   *reinterpret_cast<float4*>(&lds[y * 68 + x]) = v;
