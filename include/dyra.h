@@ -462,7 +462,7 @@ int dyra_adapter_backward(const dyra_adapters* ad, const void* X, int64_t ldx, c
  *   c: a multiple of 8, <= DYRA_BLOCK_NORM_MAX_C.
  *   weights, biases: device [c], dtype, or NULL (1, 0); post_* NULL for
  *   DYRA_NORM_NONE.  gate: device [c] (CHANNEL) or [B][c] (REQUEST: row b for
- *   the rows of request b), dtype; NULL for NONE.
+ *   the rows of request b; NULL or empty if B = 0), dtype; NULL for NONE.
  */
 #define DYRA_NORM_NONE  0
 #define DYRA_NORM_RMS   1

@@ -806,8 +806,6 @@ extern "C" int dyra_block_norm_backward(const dyra_block_norm* p, const void* x_
   a.dgate = g->gate;
   a.rows = q.s.rows;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == DYRA_BF16) launch_backward<bf16_t>(a, q.s, F, st);
-  else launch_backward<float>(a, q.s, F, st);
   NormJoinArgs j{};
   j.part = a.part;
   j.gpart = a.gpart;
@@ -822,10 +820,17 @@ extern "C" int dyra_block_norm_backward(const dyra_block_norm* p, const void* x_
   j.n = n;
   j.c = a.c;
   j.V = V;
-  j.wgs = (int)q.s.wgs;
+  j.wgs = n ? (int)q.s.wgs : 0;
   j.blocks = blocks;
   j.B = (int32_t)B;
   j.rows = q.s.rows;
+  // no rows: the row kernel, which would load a row of the gate that a call
+  // without requests does not have, has nothing to do, and the join writes zeros
+  bool wanted = n || requests;
+  for (const float* out : j.out) wanted = wanted || out;
+  if (!wanted) return DYRA_OK;
+  if (n && dtype == DYRA_BF16) launch_backward<bf16_t>(a, q.s, F, st);
+  else if (n) launch_backward<float>(a, q.s, F, st);
   hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)(blocks * (V + requests))), dim3(256), 0, st, j);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }

@@ -57,6 +57,15 @@ def test_backward_rejects_before_any_hip_call(kw, code):
     assert _backward(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(gate_kind=1, gate=P), dict(gate_kind=2, off=P),
+                                dict(gate_kind=2, gate=P, off=P), dict(gate_kind=2)])
+def test_backward_of_no_rows_launches_no_row_kernel(kw):
+    """Without rows only the join of wanted gradients is launched (a gate per
+    request may then have no row to load); with none wanted, nothing is, and
+    the call succeeds where there is no GPU."""
+    assert _backward(n=0, x_new=None, y=None, dz=None, dx=None, dy=None, grads=(None,) * 5, **kw) == 0
+
+
 def test_workspace_size():
     need = [ctypes.c_size_t() for _ in range(3)]
     L = D.lib()

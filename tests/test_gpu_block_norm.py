@@ -248,6 +248,23 @@ def test_no_rows():
         assert all(t is None or not t.any() for t in g.values())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("post", ["none", "rms"])
+def test_no_requests(post, dtype):
+    """A gate per request of no requests: no rows, a gate without rows, and
+    parameter gradients that are zero whatever the memory held."""
+    import torch
+    from input_adaptive_rank_amd import block_norm as BN
+    d, kw = put(make([0], 64, "rms", post, "request", dtype, seed=1, biases=True), dtype)
+    kw.update(gate=kw["gate"][:0].contiguous(), offsets=kw["offsets"][:1].contiguous())
+    assert all(t.shape == (0, 64) for t in BN.block_norm_forward(d["x"], d["y"], **kw))
+    g = BN.block_norm_backward(d["x_new"], d["y"], d["dz"], d["dx_new"], **kw)
+    torch.cuda.synchronize()
+    assert g["d_gate"].shape == g["dx"].shape == g["dy"].shape == (0, 64)
+    for k in PARAMS[:4]:
+        assert (g["d_" + k] is None) == (kw[k] is None) and (kw[k] is None or not g["d_" + k].any())
+
+
 def test_a_bad_row_spoils_only_itself():
     import torch
     from input_adaptive_rank_amd import block_norm as BN
