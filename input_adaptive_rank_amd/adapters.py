@@ -12,6 +12,9 @@ pool, by convention -1: none).  For a row t of a request with adapter a
 other).  Every step runs in libdyra.so's HIP kernels on the given stream; the
 calls do not synchronise, and offsets and slots are read on the device, so a
 captured graph may be replayed with other requests of the same total rows.
+Another stream than the current one is given as `stream`: results and
+workspace that are made here are then allocated on it, and the caller orders it
+after the work that makes the operands, and its own use of the results after it.
 
 Tensors (GPU, bf16 or fp32, one type throughout):
   X [n][c1], base / Y / dY [n][c2], dX_base / dX [n][c1]: rows may be further
@@ -134,9 +137,7 @@ def _workspace(workspace, ad, n, requests, dt, backward, device, stream):
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)   # the work outlives this call on a stream that is not the current one
+        workspace = _new((need,), torch.uint8, device, stream)
     else:
         D._expect_bytes(workspace, "workspace", need)
         D._expect_device([("workspace", workspace)], device)
@@ -156,12 +157,22 @@ def _on(device, stream):
     return stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """Memory of the stream that writes it.  A block of the current stream's
+    may have been freed with work still to come there, which `stream` would
+    not wait for; one of its own comes back to it in its own order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _output(t, shape, dtype, device, stream):
-    if t is not None:
-        return t
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """t, or a new tensor for a result, which the caller may use on the current stream."""
+    if t is None:
+        t = _new(shape, dtype, device, stream)
+        if stream is not None:
+            t.record_stream(torch.cuda.current_stream(device))
     return t
 
 

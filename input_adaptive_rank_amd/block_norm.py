@@ -15,7 +15,10 @@ decreasing).  Weights and biases are [c] or None (1 and 0).
 
 All tensors are on one GPU, bf16 or fp32 (one type throughout), contiguous;
 c is a multiple of 8 up to 16384.  Parameter gradients are float32.  Every step
-runs in libdyra.so's HIP kernels on the given stream, without synchronising.
+runs in libdyra.so's HIP kernels on the given stream, without synchronising;
+results and workspace that are made here are allocated on that stream, and the
+caller orders it after the work that makes the operands, and its own use of the
+results after it.
 """
 from __future__ import annotations
 
@@ -24,7 +27,7 @@ import ctypes
 import torch
 
 from . import dyra as D
-from .adapters import _DTYPES, _apart, _flat, _on, _output
+from .adapters import _DTYPES, _apart, _flat, _new, _on, _output
 
 MAX_C = 16384   # DYRA_BLOCK_NORM_MAX_C
 _KINDS = {"none": 0, "rms": 1, "layer": 2}
@@ -145,7 +148,7 @@ def block_norm_backward(x_new, y, dz, dx_new=None, pre="rms", post="none", pre_w
     L = D.lib()
     D._check("dyra_block_norm_workspace_size", L.dyra_block_norm_workspace_size(p, n, nb, dt, need))
     if workspace is None:
-        workspace = _output(None, (need.value,), torch.uint8, dev, stream)
+        workspace = _new((need.value,), torch.uint8, dev, stream)
     else:
         D._expect_bytes(workspace, "workspace", need.value)
         D._expect_device([("workspace", workspace)], dev)

@@ -121,3 +121,44 @@ def test_binding_operand_checks():
         AD._apart(wide[:5], "out", [("X", wide[4:])])
     AD._apart(wide[:5], "out", [("X", wide[5:]), ("base", None)])
     assert AD._same(wide[:, :64], wide[:, :64]) and not AD._same(wide[:, :64], wide[:, 8:72])
+
+
+def test_results_and_workspace_are_allocated_on_the_given_stream(monkeypatch):
+    """A block of the current stream's pool could be handed out with work on it
+    still pending there; only a result is for the current stream to use too."""
+    import contextlib
+
+    import torch
+    from input_adaptive_rank_amd import adapters as AD
+    current, other = object(), object()
+    at, made = [current], []
+
+    class Block:
+        def __init__(self, shape, dtype, device):
+            self.stream, self.recorded = at[-1], []
+            made.append(self)
+
+        def record_stream(self, stream):
+            self.recorded.append(stream)
+
+        def data_ptr(self):
+            return P
+
+        def numel(self):
+            return 1
+
+    @contextlib.contextmanager
+    def on(stream):
+        at.append(stream)
+        yield
+        at.pop()
+
+    monkeypatch.setattr(torch, "empty", Block)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    ad = D.Adapters(4, 16, 64, 96, P, P, None, None)
+    for stream in (None, other):
+        out = AD._output(None, (1000, 96), torch.bfloat16, "cuda:0", stream)
+        assert AD._workspace(None, ad, 1000, 7, BF16, 1, "cuda:0", stream)[2] is made[-1]
+        assert out.recorded == ([] if stream is None else [current]) and made[-1].recorded == []
+    assert [b.stream for b in made] == [current, current, other, other]

@@ -332,3 +332,33 @@ def test_another_stream():
     s.synchronize()
     assert torch.equal(got, want)
     assert all(torch.equal(a, b) for a, b in zip(other, grads))
+
+
+def test_another_stream_leaves_memory_that_is_still_in_use():
+    """Blocks of the sizes that a call allocates, just freed on the current
+    stream with their readers still to run there, are not written by a call on
+    another stream."""
+    import torch
+    from input_adaptive_rank_amd import adapters as AD
+    n, c, r = 4096, 1024, 16
+    case = make([3000, n - 3000], [0, 1], c, c, r, 2, BF16, seed=14)
+    d = put(case, BF16)
+    want, H = run_forward(d, base=d["base"], save_h=True)
+    grads = run_backward(d, H)
+    s, a = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    b = torch.empty_like(a)
+    sizes = [2 * n * c, 4 * n * r] + [AD.adapter_workspace_size(2, r, c, c, n, 2, BF16, back) for back in (0, 1)]
+    old = [torch.full((size,), 3, dtype=torch.uint8, device="cuda") for size in sizes]
+    kept = [torch.empty_like(t) for t in old]
+    torch.cuda.synchronize()
+    for _ in range(50):   # some 70 ms on the current stream, then the readers
+        torch.mm(a, a, out=b)
+    for t, k in zip(old, kept):
+        torch.add(t, 1, out=k)
+    del t, old
+    got, h = run_forward(d, base=d["base"], save_h=True, stream=s)
+    other = run_backward(d, h, stream=s)
+    torch.cuda.synchronize()
+    assert all(bool((k == 4).all()) for k in kept)
+    assert torch.equal(got, want) and torch.equal(h, H)
+    assert all(torch.equal(p, q) for p, q in zip(other, grads))

@@ -393,3 +393,31 @@ def test_another_stream():
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(g[k] is None or torch.equal(g[k], g0[k]) for k in g)
+
+
+def test_another_stream_leaves_memory_that_is_still_in_use():
+    """Blocks of the sizes that a call allocates, just freed on the current
+    stream with their readers still to run there, are not written by a call on
+    another stream."""
+    import torch
+    from input_adaptive_rank_amd import block_norm as BN
+    n, c = 4096, 1024
+    d, kw = put(make([n], c, "rms", "rms", "channel", BF16, seed=12), BF16)
+    want = BN.block_norm_forward(d["x"], d["y"], **kw)
+    g0 = BN.block_norm_backward(d["x_new"], d["y"], d["dz"], **kw)
+    s, a = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    b = torch.empty_like(a)
+    old = [torch.full((size,), 3, dtype=torch.uint8, device="cuda") for size in (2 * n * c, 2 * n * c, 3 * 4 * c, 4 << 20)]
+    kept = [torch.empty_like(t) for t in old]
+    torch.cuda.synchronize()
+    for _ in range(50):   # some 70 ms on the current stream, then the readers
+        torch.mm(a, a, out=b)
+    for t, k in zip(old, kept):
+        torch.add(t, 1, out=k)
+    del t, old
+    got = BN.block_norm_forward(d["x"], d["y"], stream=s, **kw)
+    g = BN.block_norm_backward(d["x_new"], d["y"], d["dz"], stream=s, **kw)
+    torch.cuda.synchronize()
+    assert all(bool((k == 4).all()) for k in kept)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert all(g[k] is None or torch.equal(g[k], g0[k]) for k in g)
