@@ -426,7 +426,8 @@ int dyra_adapter_workspace_size(int32_t slots, int32_t r, int64_t c1, int64_t c2
  * bf16: H is accumulated in fp32 and enters the second product as two bf16
  * terms, so Y is rounded once.  A request's result does not depend on the
  * other requests of the call other than through the order of the partial
- * sums.  Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
+ * sums.  Errors (before any HIP call): EINVAL, ESHAPE (sizes as above, or a
+ * launch would have 2^32 threads, from about 2^28 rows), EWORKSPACE; EHIP.
  */
 int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int64_t ldx, const void* base, int64_t ldb,
                          void* Y, int64_t ldy, float* H, int64_t n, int64_t B, const int32_t* offsets_dev,
@@ -504,6 +505,8 @@ int dyra_block_norm_forward(const dyra_block_norm* p, const void* x, const void*
  * another operand.  Sums over rows are fp32 in a fixed order: the same call
  * gives the same bits.
  *   workspace: device, >= dyra_block_norm_workspace_size bytes.
+ * Errors as forward, EWORKSPACE, and ESHAPE where the gate's requests make a
+ * launch of 2^32 threads (about B c / 32 = 2^24).
  */
 typedef struct {
   float *pre_weight, *pre_bias, *post_weight, *post_bias, *gate;

@@ -16,7 +16,6 @@
 // rows shares its weights whatever the order of the requests.
 #include <hip/hip_runtime.h>
 
-#include <climits>
 #include <type_traits>
 
 #include "../../include/dyra.h"
@@ -1279,9 +1278,12 @@ Pack<T> pack_job(const void* src, void* dst, int64_t rows, int64_t ks, bool acro
   return j;
 }
 
+// workgroups that sort
+int group_wgs(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(cdiv64(n, 2 * GROUP_NT), 64)); }
+
 template <typename T>
 void launch_group(const Requests& rq, const Grouped& g, const Pack<T>& a, const Pack<T>& b, hipStream_t st) {
-  const int wgs = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv64(rq.n, 2 * GROUP_NT), 64));
+  const int wgs = group_wgs(rq.n);
   const int64_t na = a.src ? (int64_t)rq.slots * a.wgs : 0, nb = b.src ? (int64_t)rq.slots * b.wgs : 0;
   hipLaunchKernelGGL((group_kernel<T>), dim3((unsigned)(wgs + na + nb)), dim3(GROUP_NT), 0, st, rq, g, wgs, a, b,
                      (int)na);
@@ -1312,6 +1314,11 @@ void launch_expand_rt(const ExpandArgs& a, const JoinArgs& j, int join_wgs, unsi
     hipLaunchKernelGGL((expand_kernel<T, RT, 8>), dim3(grid), nt, 0, st, a, j, join_wgs);
 }
 
+// workgroups of the expand but for those of a join: whole runs of every XCD
+int64_t expand_wgs(int64_t row_blocks, int64_t col_blocks) {
+  return cdiv64(row_blocks, 8 * XCD_RUN) * (8 * XCD_RUN) * col_blocks;
+}
+
 // join: the weight gradients' join of a backward pass, or null
 template <typename T>
 void launch_expand(const ExpandArgs& a, int ert, const JoinArgs* join, hipStream_t st) {
@@ -1321,7 +1328,7 @@ void launch_expand(const ExpandArgs& a, int ert, const JoinArgs* join, hipStream
     j = *join;
     wgs = (j.blocks[0] + j.blocks[1] + 7) & ~7;   // the XCDs of the others stay as they are
   }
-  const unsigned grid = (unsigned)(cdiv64((int64_t)a.tiles * a.sub, 8 * XCD_RUN) * (8 * XCD_RUN) * a.col_blocks + wgs);
+  const unsigned grid = (unsigned)(expand_wgs((int64_t)a.tiles * a.sub, a.col_blocks) + wgs);
   if (ert == 1) launch_expand_rt<T, 1>(a, j, wgs, grid, st);
   else launch_expand_rt<T, 2>(a, j, wgs, grid, st);
 }
@@ -1425,16 +1432,22 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
-// every grid of a call fits a launch
-bool grids_fit(const dyra_adapters& ad, const Plan& q, bool backward) {
-  const int64_t most = INT_MAX, c = std::max(ad.c1, ad.c2);
-  const int64_t packs = (cdiv64(ad.c1, 16) + cdiv64(ad.c2, 16)) * cdiv64(ad.r, 16) / PACK_BLOCKS + 2;
-  if (q.tile_cap * q.sub * q.ks > most || (q.tile_cap * 4 + 8 * XCD_RUN) * cdiv64(c, EXPAND_COLS) > most) return false;
-  if (q.packed && packs * ad.slots + 64 > most) return false;
+// Every launch of a call has fewer than 2^32 threads, as the runtime demands.
+// (Workgroup numbers are then below 2^24, and 32-bit in the kernels.)
+bool grids_fit(const dyra_adapters& ad, const Plan& q, int64_t n, int dtype, bool backward) {
+  const int64_t most = ((int64_t)1 << 32) - 1, kstep = dtype == DYRA_BF16 ? 32 : 16;
+  const int64_t cin = backward ? ad.c2 : ad.c1, cout = backward ? ad.c1 : ad.c2;
+  const int64_t packs = cdiv64(cdiv64(ad.r, 16) * cdiv64(cin, kstep), PACK_BLOCKS) +
+                        cdiv64(cdiv64(cout, 16) * cdiv64(ad.r, kstep), PACK_BLOCKS);
+  if (((q.packed ? packs * ad.slots : 0) + group_wgs(n)) * GROUP_NT > most) return false;
+  if (q.tile_cap * q.sub * q.ks * (SHRINK_WAVES * 64) > most) return false;
+  const int64_t joins =
+      backward ? (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots + 7 : 0;
+  if ((expand_wgs(q.tile_cap * (q.tile / (16 * q.ert)), cdiv64(cout, EXPAND_COLS)) + joins) * 256 > most) return false;
   if (!backward) return true;
-  return (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots +
-                 (q.tile_cap * 4 + 8 * XCD_RUN) * cdiv64(ad.c1, EXPAND_COLS) + 8 <= most &&
-         (cdiv64(ad.c1, 256) + cdiv64(ad.c2, 256)) * 2 * q.chunk_cap <= most;
+  const int64_t cols = 4 * (dtype == DYRA_BF16 ? grad_cols<bf16_t>() : grad_cols<float>());
+  const int64_t r_groups = cdiv64(ad.r, ad.r <= 16 ? 16 : ad.r <= 32 ? 32 : 64);
+  return (cdiv64(ad.c1, cols) + cdiv64(ad.c2, cols)) * r_groups * q.chunk_cap * 256 <= most;
 }
 
 }  // namespace
@@ -1467,7 +1480,7 @@ extern "C" int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int6
   const Plan q = make_plan(ad->slots, ad->r, ad->c1, ad->c2, n, B, dtype, false);
   if (q.total && !workspace) return DYRA_EINVAL;
   if (ws_bytes < q.total) return DYRA_EWORKSPACE;
-  if (!grids_fit(*ad, q, false)) return DYRA_ESHAPE;
+  if (!q.direct && !grids_fit(*ad, q, n, dtype, false)) return DYRA_ESHAPE;
   const Requests rq{offsets_dev, slots_dev, (int32_t)n, (int32_t)B, ad->slots};
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -1498,7 +1511,7 @@ extern "C" int dyra_adapter_backward(const dyra_adapters* ad, const void* X, int
   }
   const Plan q = make_plan(ad->slots, ad->r, ad->c1, ad->c2, n, B, dtype, true);
   if (ws_bytes < q.total) return DYRA_EWORKSPACE;
-  if (!grids_fit(*ad, q, true)) return DYRA_ESHAPE;
+  if (!grids_fit(*ad, q, n, dtype, true)) return DYRA_ESHAPE;
   const Requests rq{offsets_dev, slots_dev, (int32_t)n, (int32_t)B, ad->slots};
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);

@@ -16,7 +16,6 @@
 // first size runs at 5.2 TB/s, of 2 GiB at 4.85.
 #include <hip/hip_runtime.h>
 
-#include <climits>
 #include <type_traits>
 
 #include "../../include/dyra.h"
@@ -792,7 +791,7 @@ extern "C" int dyra_block_norm_backward(const dyra_block_norm* p, const void* x_
   const int F = flags_of(*p), V = vectors(F);
   const int blocks = (int)cdiv64(p->c, 32);
   const int requests = p->gate_kind == DYRA_GATE_REQUEST ? (int)B : 0;
-  if ((int64_t)blocks * (V + requests) > INT_MAX) return DYRA_ESHAPE;
+  if (((int64_t)blocks * (V + requests)) << 8 >= (int64_t)1 << 32) return DYRA_ESHAPE;   // threads of the join's launch
   NormArgs a = norm_args(*p, n, B, offsets_dev);
   a.x = x_new;
   a.y = y;

@@ -80,6 +80,17 @@ def test_backward_rejects_before_any_hip_call(kw, code):
     assert _backward(**kw) == code
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_launches_of_too_many_threads_are_rejected_before_any_hip_call(dtype):
+    """2^32 threads or more: the tiles of 2^28 rows, the packing of a pool,
+    the join of a pool's gradients."""
+    kw = dict(dtype=dtype, ws_bytes=1 << 62)
+    assert _forward(n=1 << 28, c1=8, c2=8, ldx=8, ldy=8, r=8, **kw) == -2
+    assert _backward(n=1 << 28, c1=8, c2=8, ldx=8, ldy=8, ldo=8, r=8, **kw) == -2
+    wide = 1 << 20
+    assert _backward(n=10, nb=2048, slots=2048, c1=wide, c2=wide, ldx=wide, ldy=wide, ldo=wide, r=128, **kw) == -2
+
+
 def _tensors(n=10, c1=64, c2=96, r=16, slots=3, nb=2):
     import torch
     bf = torch.bfloat16

@@ -66,6 +66,13 @@ def test_backward_of_no_rows_launches_no_row_kernel(kw):
     assert _backward(n=0, x_new=None, y=None, dz=None, dx=None, dy=None, grads=(None,) * 5, **kw) == 0
 
 
+def test_backward_of_too_many_requests_is_rejected_before_any_hip_call():
+    """2^32 threads or more in the join of a gate's gradients."""
+    for c, B in ((16384, 32768), (4096, 131072), (40, (1 << 23) + 1)):
+        kw = dict(c=c, gate_kind=2, gate=P, off=P, grads=(P, None, None, None, P), ws_bytes=1 << 62)
+        assert _backward(n=100, B=B, **kw) == -2
+
+
 def test_workspace_size():
     need = [ctypes.c_size_t() for _ in range(3)]
     L = D.lib()
