@@ -84,14 +84,29 @@ def _span(t):
     return lo, lo + (sum((s - 1) * d for s, d in zip(t.shape, t.stride())) + 1) * t.element_size() if t.numel() else lo
 
 
+def _overlap(a, b):
+    """Whether two tensors share a byte.  Column ranges of one wide matrix are
+    told apart row by row; tensors of other shapes by their spans."""
+    (lo, hi), (first, last) = _span(a), _span(b)
+    if not (lo < last and first < hi):
+        return False
+    if a.dim() != 2 or b.dim() != 2 or a.stride(1) != 1 or b.stride(1) != 1:
+        return True
+    # a single row may take the other's row stride
+    pitch = {t.stride(0) * t.element_size() for t in (a, b) if t.shape[0] > 1}
+    wide, other = (t.shape[1] * t.element_size() for t in (a, b))
+    if len(pitch) != 1 or max(wide, other) > (step := pitch.pop()):
+        return True
+    # row i of a begins `at` bytes into row `row` + i of b's grid
+    row, at = divmod(lo - first, step)
+    meets = lambda k: -a.shape[0] < k < b.shape[0]  # noqa: E731
+    return at < other and meets(row) or step - at < wide and meets(row + 1)
+
+
 def _apart(out, name, others):
     """An output overlaps no other operand (the kernels read those while others write)."""
-    lo, hi = _span(out)
     for other, t in others:
-        if t is None:
-            continue
-        a, z = _span(t)
-        if lo < z and a < hi:
+        if t is not None and _overlap(out, t):
             raise ValueError(f"{name} must not overlap {other}")
 
 

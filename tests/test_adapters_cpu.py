@@ -173,3 +173,22 @@ def test_results_and_workspace_are_allocated_on_the_given_stream(monkeypatch):
         assert AD._workspace(None, ad, 1000, 7, BF16, 1, "cuda:0", stream)[2] is made[-1]
         assert out.recorded == ([] if stream is None else [current]) and made[-1].recorded == []
     assert [b.stream for b in made] == [current, current, other, other]
+
+
+def test_column_ranges_of_one_matrix_do_not_overlap():
+    """Against the bytes themselves: every pair of column and row ranges."""
+    import itertools
+
+    import torch
+    from input_adaptive_rank_amd import adapters as AD
+    base = torch.zeros(6 * 5, dtype=torch.bfloat16)
+    wide = base.view(6, 5)
+    views = [wide[r0:r1, c0:c1] for r0, r1 in ((0, 6), (0, 2), (2, 6), (3, 4), (1, 1))
+             for c0, c1 in ((0, 5), (0, 2), (2, 5), (1, 4), (4, 5))]
+    views += [base[3:15].view(4, 3), base[7:9].view(1, 2), base[7:9].view(2, 1), base[4:22].view(3, 3, 2)]
+    where = torch.arange(30)
+    bytes_of = [set(where.as_strided(v.shape, v.stride(), v.storage_offset()).flatten().tolist()) for v in views]
+    for (a, x), (b, y) in itertools.product(zip(views, bytes_of), repeat=2):
+        one_grid = a.dim() == b.dim() == 2 and (a.shape[0] < 2 or b.shape[0] < 2 or a.stride(0) == b.stride(0))
+        if one_grid or x & y:
+            assert AD._overlap(a, b) == bool(x & y), (a.shape, a.storage_offset(), b.shape, b.storage_offset())

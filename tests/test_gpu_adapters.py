@@ -362,3 +362,26 @@ def test_another_stream_leaves_memory_that_is_still_in_use():
     assert all(bool((k == 4).all()) for k in kept)
     assert torch.equal(got, want) and torch.equal(h, H)
     assert all(torch.equal(p, q) for p, q in zip(other, grads))
+
+
+@pytest.mark.parametrize("n", [5, 700])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_operands_and_results_side_by_side_in_one_matrix(n, dtype):
+    """X, base (written in place) and dX as column ranges of one wide matrix."""
+    import torch
+    c1, c2 = 136, 72
+    case = make([n - 2, 2], [1, 0], c1, c2, 24, 2, dtype, seed=15)
+    d = put(case, dtype)
+    want, H = run_forward(d, base=d["base"], save_h=True)
+    grads = run_backward(d, H)
+    wide = torch.full((n, 2 * c1 + c2), float("nan"), dtype=d["X"].dtype, device="cuda")
+    X, Y, dX = wide[:, :c1], wide[:, c1:c1 + c2], wide[:, c1 + c2:]
+    X.copy_(d["X"])
+    Y.copy_(d["base"])
+    d["X"] = X
+    run_forward(d, base=Y, out=Y)
+    run_backward(d, H, dX=dX)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and torch.equal(dX, grads[0])
+    with pytest.raises(ValueError, match="overlap"):
+        run_forward(d, out=wide[:, c1 - 8:c1 + c2 - 8])
