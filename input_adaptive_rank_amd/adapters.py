@@ -111,7 +111,8 @@ def _apart(out, name, others):
 
 
 def _same(a, b):
-    return a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+    """Whether two row operands of one shape are the same memory (a single row has no stride)."""
+    return a.data_ptr() == b.data_ptr() and (a.shape[0] < 2 or a.stride() == b.stride())
 
 
 def _pool(X, A, B, offsets, slots, rank, scale):

@@ -192,3 +192,12 @@ def test_column_ranges_of_one_matrix_do_not_overlap():
         one_grid = a.dim() == b.dim() == 2 and (a.shape[0] < 2 or b.shape[0] < 2 or a.stride(0) == b.stride(0))
         if one_grid or x & y:
             assert AD._overlap(a, b) == bool(x & y), (a.shape, a.storage_offset(), b.shape, b.storage_offset())
+
+
+def test_a_single_row_is_the_same_memory_whatever_its_stride():
+    import torch
+    from input_adaptive_rank_amd import adapters as AD
+    wide = torch.zeros((3, 96), dtype=torch.bfloat16)
+    row = wide[0, 8:72]
+    assert AD._same(wide[:1, 8:72], row[None]) and not AD._same(wide[:1, 8:72], wide[:1, 16:80])
+    assert not AD._same(wide[:2, :32], wide.view(9, 32)[:2])

@@ -385,3 +385,14 @@ def test_operands_and_results_side_by_side_in_one_matrix(n, dtype):
     assert torch.equal(Y, want) and torch.equal(dX, grads[0])
     with pytest.raises(ValueError, match="overlap"):
         run_forward(d, out=wide[:, c1 - 8:c1 + c2 - 8])
+
+
+def test_one_row_in_place_by_another_view():
+    """base and out as two views of one row, which have different strides."""
+    import torch
+    d = put(make([1], [0], 64, 72, 8, 1, BF16, seed=16), BF16)
+    want = run_forward(d, base=d["base"])
+    wide = torch.zeros((2, 80), dtype=torch.bfloat16, device="cuda")
+    wide[:1, 8:].copy_(d["base"])
+    run_forward(d, base=wide[:1, 8:], out=wide[0, 8:][None])
+    assert torch.equal(wide[:1, 8:], want)
