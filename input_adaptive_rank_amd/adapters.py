@@ -205,17 +205,18 @@ def adapter_forward(X, A, B, offsets, slots, base=None, rank=None, scale=None, o
     handle = _on(dev, stream)
     xp, ldx = _rows(X, "X", n, c1, X.dtype, dev)
     bp, ldb = (None, 0) if base is None else _rows(base, "base", n, c2, X.dtype, dev)
+    Y = _output(out, (n, c2), X.dtype, dev, stream)
+    yp, ldy = _rows(Y, "out", n, c2, X.dtype, dev)
     if out is not None:
         _apart(out, "out", [("X", X), ("A", A), ("B", B)])
         if base is not None and not _same(out, base):
             _apart(out, "out", [("base (other than base itself)", base)])
-    Y = _output(out, (n, c2), X.dtype, dev, stream)
-    yp, ldy = _rows(Y, "out", n, c2, X.dtype, dev)
-    if save_h and H is None:
-        H = _output(None, (n, r), torch.float32, dev, stream)
-    elif H is not None:
-        _apart(H, "H", [("X", X), ("A", A), ("B", B), ("base", base), ("out", out)])
+    given = H is not None
+    if save_h:
+        H = _output(H, (n, r), torch.float32, dev, stream)
     hp = _flat(H, "H", (n, r), torch.float32, dev)
+    if given:
+        _apart(H, "H", [("X", X), ("A", A), ("B", B), ("base", base), ("out", out)])
     wp, wn, workspace = _workspace(workspace, ad, n, nb, dt, 0, dev, stream)
     D._check("dyra_adapter_forward",
              D.lib().dyra_adapter_forward(ad, xp, ldx, bp, ldb, yp, ldy, hp, n, nb, off, ids, dt, wp, wn, handle))
@@ -246,26 +247,27 @@ def adapter_backward(X, dY, H, A, B, offsets, slots, dX_base=None, rank=None, sc
     if need_dx:
         if dX_base is not None:
             bp, ldb = _rows(dX_base, "dX_base", n, c1, X.dtype, dev)
-        if dX is not None:
+        given = dX is not None
+        dX = _output(dX, (n, c1), X.dtype, dev, stream)
+        op, ldo = _rows(dX, "dX", n, c1, X.dtype, dev)
+        if given:
             _apart(dX, "dX", inputs)
             if dX_base is not None and not _same(dX, dX_base):
                 _apart(dX, "dX", [("dX_base (other than dX_base itself)", dX_base)])
-        dX = _output(dX, (n, c1), X.dtype, dev, stream)
-        op, ldo = _rows(dX, "dX", n, c1, X.dtype, dev)
     else:
         dX = None
     ap = wp2 = None
     if need_weights:
-        for t, name in ((dA, "dA"), (dB, "dB")):
-            if t is not None:
-                _apart(t, name, inputs + [("dX_base", dX_base), ("dX", dX)])
-        if dA is not None and dB is not None:
-            _apart(dA, "dA", [("dB", dB)])
         ns = A.shape[0]
+        given = [(t, name) for t, name in ((dA, "dA"), (dB, "dB")) if t is not None]
         dA = _output(dA, (ns, r, c1), torch.float32, dev, stream)
         dB = _output(dB, (ns, c2, r), torch.float32, dev, stream)
         ap = _flat(dA, "dA", (ns, r, c1), torch.float32, dev)
         wp2 = _flat(dB, "dB", (ns, c2, r), torch.float32, dev)
+        for t, name in given:
+            _apart(t, name, inputs + [("dX_base", dX_base), ("dX", dX)])
+        if len(given) == 2:
+            _apart(dA, "dA", [("dB", dB)])
     else:
         dA = dB = None
     wp, wn, workspace = _workspace(workspace, ad, n, nb, dt, 1, dev, stream)

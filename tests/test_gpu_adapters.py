@@ -396,3 +396,48 @@ def test_one_row_in_place_by_another_view():
     wide[:1, 8:].copy_(d["base"])
     run_forward(d, base=wide[:1, 8:], out=wide[0, 8:][None])
     assert torch.equal(wide[:1, 8:], want)
+
+
+FORWARD_REFUSALS = {
+    "out_not_a_tensor": dict(out="out"), "out_shape": dict(out=(10, 80)), "out_type": dict(out=(10, 72, "float32")),
+    "h_not_a_tensor": dict(H=3.0), "h_shape": dict(H=(10, 16, "float32")), "h_type": dict(H=(10, 8)),
+    "base_rows": dict(base=(9, 72)), "base_not_a_tensor": dict(base=[1]), "rank_type": dict(rank=(2, "float32")),
+    "scale_shape": dict(scale=(3, "float32")), "workspace_type": dict(workspace=(1 << 20, "float32")),
+    "offsets_short": dict(offsets=(2, "int32")),
+}
+
+
+def made(v):
+    """A tensor of the shape, and type if it ends in one, that a tuple names."""
+    import torch
+    if not isinstance(v, tuple):
+        return v
+    dtype = getattr(torch, v[-1]) if isinstance(v[-1], str) else torch.bfloat16
+    return torch.zeros(tuple(k for k in v if not isinstance(k, str)), dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("name", FORWARD_REFUSALS)
+def test_forward_refuses(name):
+    from input_adaptive_rank_amd import adapters as AD
+    d = put(make([4, 6], [0, 1], 64, 72, 8, 2, BF16, seed=17), BF16)
+    kw = dict(base=d["base"], rank=d["rank"], scale=d["scale"], offsets=d["offsets"], slots=d["slots"])
+    kw.update({k: made(v) for k, v in FORWARD_REFUSALS[name].items()})
+    with pytest.raises(ValueError, match=next(iter(FORWARD_REFUSALS[name]))):
+        AD.adapter_forward(d["X"], d["A"], d["B"], **kw)
+
+
+BACKWARD_REFUSALS = {
+    "dx_not_a_tensor": dict(dX="dX"), "dx_shape": dict(dX=(10, 72)), "da_not_a_tensor": dict(dA=0),
+    "da_type": dict(dA=(2, 8, 64)), "db_shape": dict(dB=(2, 8, 72, "float32")), "db_not_a_tensor": dict(dB="dB"),
+    "dx_base_shape": dict(dX_base=(10, 72)), "h_missing": dict(H=None),
+}
+
+
+@pytest.mark.parametrize("name", BACKWARD_REFUSALS)
+def test_backward_refuses(name):
+    from input_adaptive_rank_amd import adapters as AD
+    d = put(make([4, 6], [0, 1], 64, 72, 8, 2, BF16, seed=18), BF16)
+    kw = dict(H=made((10, 8, "float32")), offsets=d["offsets"], slots=d["slots"])
+    kw.update({k: made(v) for k, v in BACKWARD_REFUSALS[name].items()})
+    with pytest.raises(ValueError, match=next(iter(BACKWARD_REFUSALS[name]))):
+        AD.adapter_backward(d["X"], d["dY"], A=d["A"], B=d["B"], **kw)
