@@ -401,8 +401,9 @@ typedef struct {
 
 /*
  * Device workspace bytes of dyra_adapter_forward (backward = 0) or
- * dyra_adapter_backward (backward = 1) for n rows of B requests.  A forward
- * pass of a few rows needs none (0 bytes; the pointer may be NULL then).
+ * dyra_adapter_backward (backward = 1) for n rows of B requests.  It grows with
+ * min(slots, B), but for a word a slot.  A forward pass of a few rows needs none
+ * (0 bytes; the pointer may be NULL then).
  * Errors: EINVAL, ESHAPE.
  */
 int dyra_adapter_workspace_size(int32_t slots, int32_t r, int64_t c1, int64_t c2, int64_t n, int64_t B,

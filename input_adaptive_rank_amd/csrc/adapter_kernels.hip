@@ -16,6 +16,7 @@
 // rows shares its weights whatever the order of the requests.
 #include <hip/hip_runtime.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "../../include/dyra.h"
@@ -47,12 +48,19 @@ struct Requests {
     const int s = slot[b];
     return s < 0 || s >= slots ? slots : s;
   }
+  // Packed weights are kept by slot, or, of a pool with more slots than there
+  // are requests, by the slot's first request that has rows: time and memory
+  // follow the slots that can be in use (forward, 5003 rows of 8 requests,
+  // 4096 -> 4096, r = 64: 52 us and 10 MiB at 8, 512 and 2048 slots alike; by
+  // slot 52, 105 and 267 us, 10, 514 and 2050 MiB).
+  __host__ __device__ __forceinline__ bool by_slot() const { return B >= slots; }
 };
 
 // Rows in the order of their slots, in tiles of `tile` places that hold rows
 // of one slot: place i of tile t is row perm[t tile + i], -1 past its count.
 struct Tile {
-  int32_t slot, count;
+  uint16_t slot, pack;   // pack: where the slot's packed weights are
+  int32_t count;
 };
 struct Chunk {   // a run of tiles of one adapter slot
   int32_t slot, first, tiles, pad;
@@ -149,7 +157,7 @@ struct Pack {
   int32_t rows, ks;
   int32_t across;
   int32_t by_k;         // block order: kb rows / 16 + rb, else rb ks / KSTEP + kb
-  int32_t wgs;          // workgroups per slot
+  int32_t wgs;          // workgroups per slot (or request)
   __host__ __device__ int64_t blocks() const {
     return ((rows + 15) / 16) * (int64_t)((ks + Step<T>::K - 1) / Step<T>::K);
   }
@@ -160,14 +168,16 @@ constexpr int PACK_BLOCKS = 16;   // of a workgroup: one per wave, whose loads a
 template <typename T>
 __device__ void pack_blocks(const Pack<T>& j, const Requests& q, int id) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K;
-  const int slot = id / j.wgs, part = id % j.wgs;
-  int used = 0;
-  for (int b = threadIdx.x; b < q.B; b += GROUP_NT) used |= q.slot[b] == slot && q.len(b) > 0;
-  if (!__syncthreads_or(used)) return;
+  const int unit = id / j.wgs, part = id % j.wgs;
+  const int slot = q.by_slot() ? unit : q.id(unit), end_b = q.by_slot() ? q.B : unit;
+  if (!q.by_slot() && (slot >= q.slots || q.len(unit) == 0)) return;
+  int other = 0;   // a request with rows of the slot: it is used, or an earlier one's already
+  for (int b = threadIdx.x; b < end_b; b += GROUP_NT) other |= q.slot[b] == slot && q.len(b) > 0;
+  if ((__syncthreads_or(other) != 0) != q.by_slot()) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int RB = (j.rows + 15) / 16, KB = (j.ks + KSTEP - 1) / KSTEP, total = RB * KB;
   const T* src = j.src + (int64_t)slot * j.rows * j.ks;
-  T* dst = j.dst + (int64_t)slot * total * (64 * KPC) + lane * KPC;
+  T* dst = j.dst + (int64_t)unit * total * (64 * KPC) + lane * KPC;
   const int end = min((part + 1) * PACK_BLOCKS, total);
   for (int at = part * PACK_BLOCKS + wave; at < end; at += GROUP_NT / 64) {
     const int rb = j.by_k ? at % RB : at / KB, kb = j.by_k ? at / RB : at % KB;
@@ -200,6 +210,7 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, 
                                                          Pack<T> second, int first_wgs) {
   __shared__ __attribute__((aligned(16))) int32_t ids[GROUP_NT], lens[GROUP_NT], gpos[GROUP_NT], offs[GROUP_NT + 1];
   __shared__ int32_t run[MAX_SLOTS + 1], tile0[MAX_SLOTS + 1], chunk0[MAX_SLOTS + 1], rows_of[MAX_SLOTS + 1];
+  __shared__ int32_t first_of[MAX_SLOTS + 1];   // the first request with rows, where weights are packed by request
   __shared__ int wave_sums[3 * GROUP_NT / 64];
   const int tid = threadIdx.x, wg = blockIdx.x;
   if (wg >= group_wgs) {
@@ -210,7 +221,10 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, 
   }
   const int B = q.count(), S = q.slots, stride = group_wgs * GROUP_NT;
   // rows of each slot
-  for (int s = tid; s <= S; s += GROUP_NT) rows_of[s] = 0;
+  for (int s = tid; s <= S; s += GROUP_NT) {
+    rows_of[s] = 0;
+    first_of[s] = INT_MAX;
+  }
   // 1024 requests at a time; the first are loaded once
   int id, len;
   auto load = [&](int b0) {
@@ -224,10 +238,16 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, 
   };
   load(0);
   __syncthreads();
-  if (len) atomicAdd(&rows_of[id], len);
+  if (len) {
+    atomicAdd(&rows_of[id], len);
+    if (!q.by_slot()) atomicMin(&first_of[id], tid);
+  }
   for (int b = GROUP_NT + tid; b < B; b += GROUP_NT) {
     const int more = q.len(b);
-    if (more) atomicAdd(&rows_of[q.id(b)], more);
+    if (more) {
+      atomicAdd(&rows_of[q.id(b)], more);
+      if (!q.by_slot()) atomicMin(&first_of[q.id(b)], b);
+    }
   }
   __syncthreads();
   // first tile and first chunk of each slot; thread t sums slots [t E, (t + 1) E)
@@ -271,7 +291,9 @@ __global__ __launch_bounds__(GROUP_NT) void group_kernel(Requests q, Grouped g, 
   for (int i = wg * GROUP_NT + tid; i < g.tile_cap; i += stride) {
     const int s = slot_of(tile0, i, S), left = rows_of[s] - (i - tile0[s]) * g.tile;
     const int count = min(max(left, 0), g.tile);
-    g.tiles[i] = Tile{s, count};
+    // the comparison keeps it in range where inconsistent offsets give a tile to a slot without rows
+    const int pack = q.by_slot() ? s : first_of[s] < B ? first_of[s] : 0;
+    g.tiles[i] = Tile{(uint16_t)s, (uint16_t)pack, count};
     if (count)
       for (int u = count; u < g.tile; ++u) g.perm[(int64_t)i * g.tile + u] = -1;
   }
@@ -580,7 +602,7 @@ __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kern
       }
     const int steps = (int)cdiv64(p.K, KSTEP), lines = (steps + 1) >> 1, per = (lines + p.KS * W - 1) / (p.KS * W);
     const int u0 = (ks * W + wave) * per, u1 = min(u0 + per, lines);
-    const T* wbase = reinterpret_cast<const T*>(p.W) + (p.packed ? (int64_t)t.slot * steps * cts * 64 * KPC + lane * KPC
+    const T* wbase = reinterpret_cast<const T*>(p.W) + (p.packed ? (int64_t)t.pack * steps * cts * 64 * KPC + lane * KPC
                                                                  : (int64_t)t.slot * p.r * p.K + g * KPC);
     with_blocks<CT>(nct, [&](auto blocks) {
       constexpr int N = decltype(blocks)::value;
@@ -764,7 +786,7 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p, JoinArgs join
   for (int h = 0; h < 4; ++h) {
     const int64_t col = c0 + 16 * h + i;
     const T* wr = reinterpret_cast<const T*>(p.W) +
-                  (p.packed ? (((int64_t)t.slot * ((p.C + 15) >> 4) + ((c0 >> 4) + h)) * nks * 64 + lane) * KPC
+                  (p.packed ? (((int64_t)t.pack * ((p.C + 15) >> 4) + ((c0 >> 4) + h)) * nks * 64 + lane) * KPC
                             : ((int64_t)t.slot * p.C + col) * p.r + g * KPC);
     const int wstep = p.packed ? 64 * KPC : KSTEP;
 #pragma unroll
@@ -1223,8 +1245,9 @@ Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int6
   q.P = take(4 * n * r * q.ks);
   if (q.packed) {
     const int64_t kstep = dtype == DYRA_BF16 ? 32 : 16, kin = backward ? c2 : c1, kout = backward ? c1 : c2;
-    q.Ws = take(slots * cdiv64(r, 16) * cdiv64(kin, kstep) * 1024);
-    q.We = take(slots * cdiv64(kout, 16) * cdiv64(r, kstep) * 1024);
+    const int64_t units = std::min(slots, B);
+    q.Ws = take(units * cdiv64(r, 16) * cdiv64(kin, kstep) * 1024);
+    q.We = take(units * cdiv64(kout, 16) * cdiv64(r, kstep) * 1024);
   }
   if (backward) {
     const int cols = 4 * (dtype == DYRA_BF16 ? grad_cols<bf16_t>() : grad_cols<float>());
@@ -1284,7 +1307,7 @@ int group_wgs(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(cd
 template <typename T>
 void launch_group(const Requests& rq, const Grouped& g, const Pack<T>& a, const Pack<T>& b, hipStream_t st) {
   const int wgs = group_wgs(rq.n);
-  const int64_t na = a.src ? (int64_t)rq.slots * a.wgs : 0, nb = b.src ? (int64_t)rq.slots * b.wgs : 0;
+  const int64_t units = std::min(rq.slots, rq.B), na = a.src ? units * a.wgs : 0, nb = b.src ? units * b.wgs : 0;
   hipLaunchKernelGGL((group_kernel<T>), dim3((unsigned)(wgs + na + nb)), dim3(GROUP_NT), 0, st, rq, g, wgs, a, b,
                      (int)na);
 }
@@ -1434,12 +1457,12 @@ int backward_impl(const dyra_adapters& ad, const void* X, int64_t ldx, const voi
 
 // Every launch of a call has fewer than 2^32 threads, as the runtime demands.
 // (Workgroup numbers are then below 2^24, and 32-bit in the kernels.)
-bool grids_fit(const dyra_adapters& ad, const Plan& q, int64_t n, int dtype, bool backward) {
+bool grids_fit(const dyra_adapters& ad, const Plan& q, int64_t n, int64_t B, int dtype, bool backward) {
   const int64_t most = ((int64_t)1 << 32) - 1, kstep = dtype == DYRA_BF16 ? 32 : 16;
   const int64_t cin = backward ? ad.c2 : ad.c1, cout = backward ? ad.c1 : ad.c2;
   const int64_t packs = cdiv64(cdiv64(ad.r, 16) * cdiv64(cin, kstep), PACK_BLOCKS) +
                         cdiv64(cdiv64(cout, 16) * cdiv64(ad.r, kstep), PACK_BLOCKS);
-  if (((q.packed ? packs * ad.slots : 0) + group_wgs(n)) * GROUP_NT > most) return false;
+  if (((q.packed ? packs * std::min<int64_t>(ad.slots, B) : 0) + group_wgs(n)) * GROUP_NT > most) return false;
   if (q.tile_cap * q.sub * q.ks * (SHRINK_WAVES * 64) > most) return false;
   const int64_t joins =
       backward ? (cdiv64(ad.c1, 64) + cdiv64(ad.c2, 64)) * cdiv64(ad.r, 16) * ad.slots + 7 : 0;
@@ -1480,7 +1503,7 @@ extern "C" int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int6
   const Plan q = make_plan(ad->slots, ad->r, ad->c1, ad->c2, n, B, dtype, false);
   if (q.total && !workspace) return DYRA_EINVAL;
   if (ws_bytes < q.total) return DYRA_EWORKSPACE;
-  if (!q.direct && !grids_fit(*ad, q, n, dtype, false)) return DYRA_ESHAPE;
+  if (!q.direct && !grids_fit(*ad, q, n, B, dtype, false)) return DYRA_ESHAPE;
   const Requests rq{offsets_dev, slots_dev, (int32_t)n, (int32_t)B, ad->slots};
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -1511,7 +1534,7 @@ extern "C" int dyra_adapter_backward(const dyra_adapters* ad, const void* X, int
   }
   const Plan q = make_plan(ad->slots, ad->r, ad->c1, ad->c2, n, B, dtype, true);
   if (ws_bytes < q.total) return DYRA_EWORKSPACE;
-  if (!grids_fit(*ad, q, n, dtype, true)) return DYRA_ESHAPE;
+  if (!grids_fit(*ad, q, n, B, dtype, true)) return DYRA_ESHAPE;
   const Requests rq{offsets_dev, slots_dev, (int32_t)n, (int32_t)B, ad->slots};
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);

@@ -34,6 +34,15 @@ def test_workspace_grows_with_the_backward_pass():
     assert _size(n=1000)[1] < _size(n=2000)[1]
 
 
+@pytest.mark.parametrize("backward", [0, 1])
+def test_workspace_follows_the_slots_that_can_be_used(backward):
+    """Eight requests use at most eight slots of a pool of any size: but for
+    a word a slot, the same bytes."""
+    kw = dict(r=64, c1=4096, c2=4096, n=5003, B=8, backward=backward)
+    small, large, largest = (_size(slots=slots, **kw)[1] for slots in (8, 512, 2048))
+    assert small <= large <= largest <= small + 4 * 2048 + 256
+
+
 # fake, never dereferenced, aligned addresses: every call must be rejected on the host
 P = 1 << 12
 

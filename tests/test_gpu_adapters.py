@@ -441,3 +441,22 @@ def test_backward_refuses(name):
     kw.update({k: made(v) for k, v in BACKWARD_REFUSALS[name].items()})
     with pytest.raises(ValueError, match=next(iter(BACKWARD_REFUSALS[name]))):
         AD.adapter_backward(d["X"], d["dY"], A=d["A"], B=d["B"], **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("r", [16, 40])
+def test_a_large_pool_few_of_whose_slots_are_used(r, dtype):
+    """More slots than requests: repeated slots, an empty request before the
+    first one with rows of its slot, bare ones; slots far apart and the last."""
+    import torch
+    slots = 300
+    lens = [0, 700, 64, 0, 130, 1, 65, 300, 200]
+    ids = [299, 17, -1, 17, 299, 0, 17, 300, 299]
+    ranks = [r - s % 9 for s in range(slots)]
+    case = make(lens, ids, 264, 136, r, slots, dtype, seed=19, ranks=ranks)
+    d = put(case, dtype)
+    Y, H = run_forward(d, base=d["base"], save_h=True)
+    grads = run_backward(d, H, dX_base=d["dX_base"])
+    torch.cuda.synchronize()
+    check_forward(case, dtype, Y, H, case["base"])
+    check_backward(case, dtype, grads, case["dX_base"], host(H))
