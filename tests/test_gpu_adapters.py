@@ -460,3 +460,69 @@ def test_a_large_pool_few_of_whose_slots_are_used(r, dtype):
     torch.cuda.synchronize()
     check_forward(case, dtype, Y, H, case["base"])
     check_backward(case, dtype, grads, case["dX_base"], host(H))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("r", [40, 64, 72, 128])
+def test_a_few_rows_at_high_ranks(r, dtype):
+    """One launch, whose waves split 64 or 128 rank columns."""
+    import torch
+    from input_adaptive_rank_amd import adapters as AD
+    lens, ids, ranks = [1, 2, 0, 1, 1], [2, 0, 1, -1, 1], [r, r - 3, 17]
+    case = make(lens, ids, 520, 776, r, 3, dtype, seed=r, ranks=ranks)
+    d = put(case, dtype)
+    assert AD.adapter_workspace_size(3, r, 520, 776, 5, 5, dtype) == 0
+    Y, H = run_forward(d, base=d["base"], save_h=True)
+    torch.cuda.synchronize()
+    check_forward(case, dtype, Y, H, case["base"])
+
+
+def chunk_count(slots, r, c1, c2, n, requests, dtype):
+    """Chunks of rows that a backward pass has partial gradients for, from
+    what its workspace gains with c1 (their sums, and A's packed operands)."""
+    from input_adaptive_rank_amd import adapters as AD
+    wide, narrow = (AD.adapter_workspace_size(slots, r, c, c2, n, requests, dtype, True) for c in (240, 16))
+    packed = min(slots, requests) * 14 * -(-r // (32 if dtype == BF16 else 16)) * 1024
+    return round((wide - narrow - packed) / (4 * r * 224))
+
+
+def make_whole(lens, ids, c1, c2, r, slots, dtype, seed, ranks):
+    """Small whole numbers: every product and sum is exact in fp32, in whatever
+    order, so results equal the oracle's, rounded once."""
+    g = np.random.default_rng(seed)
+    n = int(sum(lens))
+    ints = lambda *shape: g.integers(-1, 2, shape).astype(np.float64)  # noqa: E731
+    return dict(X=ints(n, c1), base=ints(n, c2), dY=ints(n, c2), dX_base=ints(n, c1), A=ints(slots, r, c1),
+                B=ints(slots, c2, r), offsets=np.concatenate([[0], np.cumsum(lens)]).astype(np.int32),
+                slots=np.array(ids, np.int32), scale=g.choice([0.5, 1.0, 2.0], slots).astype(np.float32),
+                rank=np.array(ranks, np.int32))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("r,n", [(8, 33000), (32, 33000), (40, 33000), (72, 33000), (128, 33000), (40, 530000)])
+def test_many_rows_bit_by_bit(r, n, dtype):
+    """Chunks of several tiles (of the most there are at 530000 rows), several
+    chunks a slot, runs that end inside a tile and inside its halves, two row
+    blocks a workgroup in the product with c1 or c2; small odd widths."""
+    import torch
+    c1, c2, slots = 136, 72, 3
+    lens = [n // 3 + 17, 1, 4000, 40, n // 2 - 5000, 0]
+    lens.append(n - sum(lens))
+    ids = [0, 1, 2, 1, 0, 2, -1]
+    case = make_whole(lens, ids, c1, c2, r, slots, dtype, seed=r, ranks=[r, r - 1, r - 5])
+    tiles, chunks = n // 64, chunk_count(slots, r, c1, c2, n, len(lens), dtype)
+    log(f"  {tiles} tiles, {chunks} chunks")
+    assert chunks <= (tiles // 32 + slots + 1 if n == 530000 else tiles // 2)
+    d = put(case, dtype)
+    Y, H = run_forward(d, base=d["base"], save_h=True)
+    dX, dA, dB = run_backward(d, H, dX_base=d["dX_base"])
+    torch.cuda.synchronize()
+    y, h, _, _ = O.forward(case["X"], case["A"], case["B"], case["offsets"], ids, base=case["base"], rank=case["rank"],
+                           scale=case["scale"])
+    dx, da, db, _, size_a, size_b = O.backward(case["X"], case["dY"], h, case["A"], case["B"], case["offsets"], ids,
+                                               dX_base=case["dX_base"], rank=case["rank"], scale=case["scale"])
+    assert max(size_a.max(), size_b.max()) < 2.0 ** 23   # halves of whole numbers
+    for name, got, want in (("Y", Y, synth.round_storage(y, dtype)), ("H", H, h),
+                            ("dX", dX, synth.round_storage(dx, dtype)), ("dA", dA, da), ("dB", dB, db)):
+        wrong = int((host(got) != want).sum())
+        assert wrong == 0, (name, wrong)
