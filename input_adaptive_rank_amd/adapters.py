@@ -140,9 +140,12 @@ def _pool(X, A, B, offsets, slots, rank, scale):
 @functools.lru_cache(maxsize=1024)
 def adapter_workspace_size(slots: int, r: int, c1: int, c2: int, n: int, requests: int, dtype, backward=False) -> int:
     """Workspace bytes of a call with these sizes (0: it needs none); dtype: a torch or library type."""
+    dtype = _DTYPES.get(dtype, dtype)
+    if dtype not in (D.DT_BF16, D.DT_F32):
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     need = ctypes.c_size_t()
     D._check("dyra_adapter_workspace_size",
-             D.lib().dyra_adapter_workspace_size(slots, r, c1, c2, n, requests, _DTYPES.get(dtype, dtype),
+             D.lib().dyra_adapter_workspace_size(slots, r, c1, c2, n, requests, dtype,
                                                  int(bool(backward)), ctypes.byref(need)))
     return need.value
 

@@ -210,3 +210,13 @@ def test_a_single_row_is_the_same_memory_whatever_its_stride():
     row = wide[0, 8:72]
     assert AD._same(wide[:1, 8:72], row[None]) and not AD._same(wide[:1, 8:72], wide[:1, 16:80])
     assert not AD._same(wide[:2, :32], wide.view(9, 32)[:2])
+
+
+def test_workspace_size_refuses_other_types():
+    import torch
+    from input_adaptive_rank_amd import adapters as AD
+    sizes = (4, 16, 64, 96, 1000, 7)
+    assert AD.adapter_workspace_size(*sizes, torch.bfloat16) == AD.adapter_workspace_size(*sizes, BF16) == _size(n=1000)[1]
+    for dtype in (torch.float16, 7, "bf16"):
+        with pytest.raises(ValueError, match="dtype"):
+            AD.adapter_workspace_size(*sizes, dtype)
