@@ -1068,9 +1068,9 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs p) {
   const int which = id >= per0;
   id -= which ? per0 : 0;
   const GradSide& v = p.side[which];
-  // the shrink before this kernel read V of side 0 from the first row to the
-  // last: going back from the last finds the most of it in the Infinity Cache
-  const int cb = id % v.col_blocks, chunk = p.chunk_cap - 1 - id / v.col_blocks % p.chunk_cap;
+  // (chunks from the last to the first, against the order in which the shrink
+  // read the rows before, take the same time at 4099 and 32928 rows)
+  const int cb = id % v.col_blocks, chunk = id / v.col_blocks % p.chunk_cap;
   const int rg = id / v.col_blocks / p.chunk_cap;
   const Chunk t = p.g.chunks[chunk];
   if (t.tiles <= 0 || t.slot >= p.slots) return;
