@@ -425,9 +425,11 @@ int dyra_adapter_workspace_size(int32_t slots, int32_t r, int64_t c1, int64_t c2
  *   memory out of range whatever they hold; offsets that decrease give
  *   unspecified values in Y and H.  n and B may be 0 (no request: no adapter).
  * bf16: H is accumulated in fp32 and enters the second product as two bf16
- * terms, so Y is rounded once.  A request's result does not depend on the
- * other requests of the call other than through the order of the partial
- * sums.  Errors (before any HIP call): EINVAL, ESHAPE (sizes as above, or a
+ * terms (2^-18 of it is lost), in the form for a few rows, which needs no
+ * workspace, in fp32; Y is rounded once.  A request's result depends on the
+ * other requests of the call through that choice and the order of the partial
+ * sums alone.  An infinity in the pool may give NaN where the formula has an
+ * infinity (it meets both terms).  Errors (before any HIP call): EINVAL, ESHAPE (sizes as above, or a
  * launch would have 2^32 threads, from about 2^28 rows), EWORKSPACE; EHIP.
  */
 int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int64_t ldx, const void* base, int64_t ldb,
@@ -445,7 +447,9 @@ int dyra_adapter_forward(const dyra_adapters* ad, const void* X, int64_t ldx, co
  *   dA: device float [slots][r][c1], dB: device float [slots][c2][r], every
  *   element written (0 past a rank and for adapters without rows); both or
  *   neither may be NULL.  Sums are fp32 in a fixed order: the same call gives
- *   the same bits.  Other arguments and errors as for dyra_adapter_forward.
+ *   the same bits.  bf16: G enters dX as two bf16 terms, G and H enter dA and
+ *   dB as three (2^-27); an infinity in the pool, X or dY may give NaN where
+ *   the formula has an infinity.  Other arguments and errors as for dyra_adapter_forward.
  */
 int dyra_adapter_backward(const dyra_adapters* ad, const void* X, int64_t ldx, const void* dY, int64_t lddy,
                           const float* H, const void* dX_base, int64_t lddb, void* dX, int64_t lddx, float* dA,

@@ -10,9 +10,11 @@
 //             dA_a = sum_t G_t^T X_t,  dB_a = sum_t s_a dY_t^T H_t
 // A row of a request without an adapter (slot < 0 or >= slots) has H = G = 0.
 //
-// Every pass streams the n-row operands once and touches r-wide ones beside
-// them, so memory bounds all of it (r <= 128: at most 2 r flops per operand
-// byte).  Rows are grouped by adapter first (group_kernel), so that a tile of
+// A product streams an n-row operand and touches r-wide ones beside it: r flops
+// (bf16) or r / 2 (fp32) for a byte of it.  At what a large product and a large
+// copy reach on this card, 250 flops a byte in bf16 and 32 in fp32, memory
+// bounds all but fp32 above r = 64.  A backward pass reads X once and dY twice,
+// for G and for dB.  Rows are grouped by adapter first (group_kernel), so that a tile of
 // rows shares its weights whatever the order of the requests.
 #include <hip/hip_runtime.h>
 
@@ -566,7 +568,7 @@ __device__ __forceinline__ void shrink_slice(f32x4 (&acc)[RT][CT], const T* cons
 // written: 3.5 TB/s), where a tile's 512 KB of weights come from the L2 again
 // for every 32 rows and the last third of the workgroups is a second round.
 // Tiles of 64 rows with the weights in LDS were slower (125 us where this form
-// took 110), as was RT = 4.
+// took 110), as was RT = 4.  RT = 2 at r = 64 spills 3 registers.
 template <typename T, int RT, int CT>
 __global__ __launch_bounds__(SHRINK_WAVES * 64, CT > 4 ? 2 : 3) void shrink_kernel(ShrinkArgs p) {
   constexpr int KPC = Step<T>::KPC, KSTEP = Step<T>::K, W = SHRINK_WAVES;
@@ -952,7 +954,8 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&v)[Step<T>::KPC])
 // a microsecond at r = 16, c1 = 4096, where two more launches cost several.
 // The waves are JG groups of 16 rank columns (JG 16 >= r) times W / JG parts
 // of c1; weights are read a row of A at a time, 1 KB a wave.  Bound by latency:
-// 4 rows, 4096 -> 4096, r = 16 6.6 us.
+// 4 rows, 4096 -> 4096, r = 16 6.6 us.  Above r = 16 bf16 spills 5 or 6 of its
+// 128 registers; a call of 5 rows takes 14 us at r = 64, 24 at r = 128.
 template <typename T, int JG>
 __global__ __launch_bounds__(DIRECT_NT, 4) void direct_kernel(DirectArgs p) {
   constexpr int KPC = Step<T>::KPC, W = DIRECT_NT / 64, KG = W / JG, JB = 16;
@@ -1226,7 +1229,14 @@ Plan make_plan(int64_t slots, int64_t r, int64_t c1, int64_t c2, int64_t n, int6
   if (q.direct) return q;
   const bool small = n <= 512 && !backward;
   q.tile = small ? 16 : GRAD_TILE;
-  q.rt = r > 32 && n >= 8192 ? 2 : 1;   // a weight operand serves RT blocks of 16 rows; 256 workgroups first
+  // Row blocks of a shrink workgroup: two share a weight operand, one makes
+  // twice the workgroups.  One against two, forward / backward in us: r = 64,
+  // 1024 -> 4096, 4099 rows 38 / 63 and 41 / 59, 8192 49 / 82 and 52 / 78, 16500
+  // 84 / 141 and 83 / 135, 32928 148 / 238 and 145 / 219; r = 128, 4096 -> 4096,
+  // 4099 rows 63 / 140 and 67 / 130, 12000 131 / 249 and 122 / 241, 32928 337 /
+  // 578 and 292 / 535; fp32, r = 64, 1024 -> 1024, 16500 rows 85 / 138 and 88 /
+  // 143, 32928 144 / 233 and 145 / 232.
+  q.rt = r > 32 && n >= 8192 ? 2 : 1;
   q.sub = q.tile / (16 * q.rt);
   q.ert = small ? 1 : 2;   // 2 against 1 and 4: 109, 114 and 113 us at 32928 x 4096, 19, 18 and 21 at 4099 x 4096
   const int64_t used = std::min(slots + 1, B + 1);   // slots with rows, "no adapter" among them

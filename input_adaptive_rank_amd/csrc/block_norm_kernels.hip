@@ -8,12 +8,16 @@
 //   dg = sum over rows of d * u, and the weights' and biases' column sums.
 //
 // Forward moves 4 rows, backward 6, for some tens of operations an element:
-// memory bounds both.  A row stays in registers from its load to its store
-// (fp32, rounded once), so each operand crosses memory once.  Measured, bf16:
+// memory bounds both where a row and the column sums fit the registers.  A row
+// stays there from its load to its store (fp32, rounded once), so each operand
+// crosses memory once.  Measured, bf16:
 // forward 32928 x 1024 (layer norm, channel gate) 44 us, 6.1 TB/s; its
 // backward 74 + 5 us for the joined column sums, 5.1 TB/s; backward 4099 x
 // 4096 (both norms, a gate per request) 44 + 5 us, 4.1 TB/s.  A copy of the
 // first size runs at 5.2 TB/s, of 2 GiB at 4.85.
+// The widest rows spill, and then the spills bound them.  Forward: fp32 above
+// 8192 columns 115 registers (1000 x 16384 with all parameters 102 us, 2.6
+// TB/s), bf16 12 (1500 x 12288 41 us, 3.6 TB/s).  Backward: see its kernel.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -304,6 +308,13 @@ constexpr int vectors(int f) {
 // of both norms' statistics are taken together.  Column sums stay in
 // registers over the group's rows, meet in LDS over the workgroup's row
 // groups and go to one partial row a workgroup: no atomics, a fixed order.
+// With 16 waves a row (128 registers a lane) sums and row do not fit, and with
+// a post norm, gate and biases together (256) nearly; the spills go through the
+// caches and bound these.  Spilled registers and times with a post norm, gate
+// and biases | without: bf16 512 to 8192 columns 28 - 44 | 0, 4099 x 4096 105 us
+// (49 without the biases); bf16 above 8192 267 | 29, 1500 x 12288 414 | 77 us;
+// fp32 above 4096 137 | 0, 2000 x 8192 195 | 75 us; above 8192 404 | 54, 1000 x
+// 16384 379 | 106 us.
 // As forward, the next row is in flight while the present one is worked on
 // (but for the widest rows, whose registers do not hold both).
 template <typename T, int WPR, int NCH, int RPB, int F>
