@@ -156,7 +156,7 @@ def _workspace(workspace, ad, n, requests, dt, backward, device, stream):
     if workspace is None:
         if not need:
             return None, 0, None
-        workspace = _new((need,), torch.uint8, device, stream)
+        workspace = D._new((need,), torch.uint8, device, stream)
     else:
         D._expect_bytes(workspace, "workspace", need)
         D._expect_device([("workspace", workspace)], device)
@@ -176,23 +176,9 @@ def _on(device, stream):
     return stream.cuda_stream
 
 
-def _new(shape, dtype, device, stream):
-    """Memory of the stream that writes it.  A block of the current stream's
-    may have been freed with work still to come there, which `stream` would
-    not wait for; one of its own comes back to it in its own order."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
 def _output(t, shape, dtype, device, stream):
     """t, or a new tensor for a result, which the caller may use on the current stream."""
-    if t is None:
-        t = _new(shape, dtype, device, stream)
-        if stream is not None:
-            t.record_stream(torch.cuda.current_stream(device))
-    return t
+    return D._result(shape, dtype, device, stream) if t is None else t
 
 
 def adapter_forward(X, A, B, offsets, slots, base=None, rank=None, scale=None, out=None, save_h=False, H=None,

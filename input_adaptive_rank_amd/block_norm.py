@@ -27,7 +27,7 @@ import ctypes
 import torch
 
 from . import dyra as D
-from .adapters import _DTYPES, _apart, _flat, _new, _on, _output
+from .adapters import _DTYPES, _apart, _flat, _on, _output
 
 MAX_C = 16384   # DYRA_BLOCK_NORM_MAX_C
 _KINDS = {"none": 0, "rms": 1, "layer": 2}
@@ -148,7 +148,7 @@ def block_norm_backward(x_new, y, dz, dx_new=None, pre="rms", post="none", pre_w
     L = D.lib()
     D._check("dyra_block_norm_workspace_size", L.dyra_block_norm_workspace_size(p, n, nb, dt, need))
     if workspace is None:
-        workspace = _new((need.value,), torch.uint8, dev, stream)
+        workspace = D._new((need.value,), torch.uint8, dev, stream)
     else:
         D._expect_bytes(workspace, "workspace", need.value)
         D._expect_device([("workspace", workspace)], dev)

@@ -343,6 +343,26 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream):
+    """Memory of the stream that writes it.  A block of the current stream's
+    may have been freed with work still to come there, which `stream` would
+    not wait for, and would be reused there once freed; one of its own comes
+    back to it in its own order."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream):
+    """A new tensor that the caller may use on the current stream."""
+    t = _new(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(_torch().cuda.current_stream(device))
+    return t
+
+
 def forward(spec: Spec, plan, X, bias, Y, B: int, s: int, dtype: int, eps: float = 1e-6,
             solver: int = SOLVER_AUTO, workspace=None, stream=None):
     """Launches the DyRA forward (asynchronous on `stream`)."""
@@ -404,7 +424,9 @@ def forward_varlen(spec: Spec, plan, X, bias, Y, offsets, dtype: int, eps: float
     _check_forward_tensors(spec, plan, X, bias, Y, 1, n, dtype, workspace,
                            lambda: workspace_size_varlen(spec, off, dtype, half_steps))
     if offsets_dev is None:
-        offsets_dev = torch.from_numpy(off.astype(np.int32)).to(X.device)
+        offsets_dev = _new((B + 1,), torch.int32, X.device, stream)
+        with torch.cuda.stream(stream):   # None: the current one
+            offsets_dev.copy_(torch.from_numpy(off.astype(np.int32)))
     _expect_shape(offsets_dev, "offsets_dev", (B + 1,), torch.int32)
     _expect_device([("offsets_dev", offsets_dev)], X.device)
     if status is not None:
@@ -501,7 +523,9 @@ class DyraLayer:
         self._ws = None
         self._ws_key = None
 
-    def workspace(self, B: int, s: int):
+    def workspace(self, B: int, s: int, stream=None):
+        """The layer's workspace, kept for the calls to come (calls that
+        overlap in time race on it)."""
         torch = _torch()
         key = (B, s)
         if self._ws_key != key:
@@ -509,7 +533,11 @@ class DyraLayer:
                  workspace_size_als(self.spec, B, s, self.dtype, self.half_steps))
             if self._ws is None or self._ws.numel() < n:
                 self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+                if stream is not None:   # the block may have work to come on the current stream
+                    stream.wait_stream(torch.cuda.current_stream(self.device))
             self._ws_key = key
+        if stream is not None:
+            self._ws.record_stream(stream)
         return self._ws
 
     def forward(self, X, B: int, s: int, out=None, stream=None):
@@ -518,8 +546,8 @@ class DyraLayer:
             raise ValueError("X dtype does not match the plan dtype")
         if X.device != self.device:
             raise ValueError(f"X is on {X.device}, the layer on {self.device}")
-        Y = out if out is not None else torch.empty((B * s, self.spec.c2), dtype=X.dtype, device=X.device)
-        ws = self.workspace(B, s)
+        Y = out if out is not None else _result((B * s, self.spec.c2), X.dtype, X.device, stream)
+        ws = self.workspace(B, s, stream)
         if self.half_steps == 2:
             forward(self.spec, self.plan, X, self.bias, Y, B, s, self.dtype, self.eps, self.solver, ws, stream)
         else:
@@ -535,19 +563,19 @@ class DyraLayer:
         off = _offsets(offsets)
         if X.dtype != torch_dtype(self.dtype) or X.device != self.device:
             raise ValueError("X dtype / device does not match the layer")
-        Y = out if out is not None else torch.empty((int(off[-1]), self.spec.c2), dtype=X.dtype, device=X.device)
+        Y = out if out is not None else _result((int(off[-1]), self.spec.c2), X.dtype, X.device, stream)
         n = workspace_size_varlen(self.spec, off, self.dtype, self.half_steps)
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        st = torch.empty(off.size - 1, dtype=torch.int32, device=self.device)
+        ws = _new((n,), torch.uint8, self.device, stream)
+        st = _result((off.size - 1,), torch.int32, self.device, stream)
         forward_varlen(self.spec, self.plan, X, self.bias, Y, off, self.dtype, self.eps, self.solver, ws,
                        status=st, stream=stream, half_steps=self.half_steps)
         return Y, st
 
     def forward_events(self, X, B: int, s: int, out, events, stream=None):
-        ws = self.workspace(B, s)
+        ws = self.workspace(B, s, stream)
         forward_events(self.spec, self.plan, X, self.bias, out, B, s, self.dtype, self.eps, self.solver, ws,
                        events, stream)
         return out
 
     def status(self, B: int, s: int, stream=None) -> np.ndarray:
-        return solver_status(self.spec, self.workspace(B, s), B, s, self.dtype, stream)
+        return solver_status(self.spec, self.workspace(B, s, stream), B, s, self.dtype, stream)
