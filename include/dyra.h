@@ -522,6 +522,48 @@ int dyra_block_norm_backward(const dyra_block_norm* p, const void* x_new, const 
                              int64_t B, const int32_t* offsets_dev, int32_t dtype, void* workspace, size_t ws_bytes,
                              void* stream);
 
+/*
+ * Softmax cross entropy over a vocabulary, without its logits in memory.  For
+ * hidden rows H [n][C], a head W [V][C] and targets[n]
+ *   a_tv = scale H_t . W_v,  lse_t = log sum_v exp a_tv,
+ *   loss_t = lse_t - a_t,target.
+ * A row whose target is outside 0 .. V - 1 (by convention -1) is ignored:
+ * loss 0 (its lse is computed).
+ *   H: device [n][C], rows ldh elements apart (a multiple of 8 in bf16, 4 in
+ *   fp32, at most 2^20).  W: device [V][C].  targets: device int32[n].
+ *   loss, lse: device float[n].  scale: positive and finite.
+ *   n: 0 .. 2^20;  C: a multiple of 8, <= 2^17;  V: 1 .. 2^24;  n C < 2^33 and
+ *   n V < 2^37.
+ * Asynchronous on `stream`; no output overlaps another operand.  bf16: exact
+ * products summed in fp32.  fp32: operands as three bf16 terms, products to
+ * 2^-24; an infinity in H or W then gives NaN.
+ * Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
+ */
+int dyra_vocab_loss_workspace_size(int64_t n, int64_t C, int64_t V, int32_t dtype, int32_t backward, int32_t need_dh,
+                                   int32_t need_dw, size_t* bytes);
+int dyra_vocab_loss_forward(const void* H, int64_t ldh, const void* W, const int32_t* targets, float scale,
+                            float* loss, float* lse, int64_t n, int64_t C, int64_t V, int32_t dtype, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * Its gradients, from dloss[n] (that of loss) and the lse that the forward
+ * pass returned:
+ *   d_tv = scale dloss_t (exp(a_tv - lse_t) - [v = target_t]),
+ *   dH = d W,  dW = d^T H.
+ * Ignored rows add nothing to dW and have a zero row of dH (with a finite W),
+ * whatever H, lse and dloss hold there.
+ *   dH: device [n][C], rows lddh apart, or NULL: not wanted.  dW: device
+ *   [V][C], or NULL.  One of them must be given; every element is written (n
+ *   may be 0).  need_dh, need_dw above: whether they are.
+ * The logits are multiplied again for one piece of the vocabulary after the
+ * other; a piece's d lies in the workspace, in bf16 (fp32: three bf16 terms).
+ * Sums are fp32 in a fixed order: the same call gives the same bits.
+ * Errors as for dyra_vocab_loss_forward.
+ */
+int dyra_vocab_loss_backward(const void* H, int64_t ldh, const void* W, const int32_t* targets, const float* lse,
+                             const float* dloss, float scale, void* dH, int64_t lddh, void* dW, int64_t n, int64_t C,
+                             int64_t V, int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
+
 /* Static string naming a status code. */
 const char* dyra_status_string(int code);
 

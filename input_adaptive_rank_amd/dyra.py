@@ -131,6 +131,9 @@ def lib():
                                      P],
             "dyra_adapter_backward": [ctypes.POINTER(Adapters), P, I64, P, I64, P, P, I64, P, I64, P, P, I64, I64, P,
                                       P, I32, P, SZ, P],
+            "dyra_vocab_loss_workspace_size": [I64, I64, I64, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+            "dyra_vocab_loss_forward": [P, I64, P, P, ctypes.c_float, P, P, I64, I64, I64, I32, P, SZ, P],
+            "dyra_vocab_loss_backward": [P, I64, P, P, P, P, ctypes.c_float, P, I64, P, I64, I64, I64, I32, P, SZ, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
