@@ -523,6 +523,72 @@ int dyra_block_norm_backward(const dyra_block_norm* p, const void* x_new, const 
                              void* stream);
 
 /*
+ * Projections with 4-bit weights.  A weight W [c2][c1] is held as codes 0 ..
+ * 15 with a bf16 scale and a zero point for each group of `group` (32, 64 or
+ * 128) columns of a row (the last group may be short):
+ *   w[o][k] = scale[o][k / group] (code[o][k] - zero[o][k / group]).
+ *   c1, c2: multiples of 8, <= 2^20;  c1 c2 <= 2^34.
+ * packed: device, 16-byte aligned, dyra_q4_packed_size bytes, as dyra_q4_pack
+ * writes it.
+ */
+typedef struct {
+  int64_t c1, c2;
+  int32_t group;
+  const void* packed;
+} dyra_q4;
+int dyra_q4_packed_size(int64_t c1, int64_t c2, int32_t group, size_t* bytes);
+
+/*
+ * Lays a weight out for the products, once (asynchronous on `stream`).
+ *   codes: device uint8 [c2][c1 / 2], 4-byte aligned, two codes a byte, the even
+ *   column in the low half.  scale: device bf16 [c2][groups], groups =
+ *   ceil(c1 / group).  zero: device uint8 [c2][groups] (its low four bits
+ *   count), or NULL: 8.
+ * Errors: EINVAL (a NULL or misaligned pointer, another group), ESHAPE; EHIP.
+ */
+int dyra_q4_pack(int64_t c1, int64_t c2, int32_t group, const void* codes, const void* scale, const void* zero,
+                 void* packed, void* stream);
+
+/*
+ * Codes, scales and zero points of a matrix W, device [c2][c1] (asynchronous).
+ * zero NULL: code 8 stands for 0 and a group's largest magnitude for 7 scales.
+ * Else the lowest and highest value of a group (0 among them) are 15 scales
+ * apart.  A scale is rounded to bf16 before the codes, which are rounded to the
+ * nearest (ties to even) and clamped to 0 .. 15; a group of zeros has scale 0.  W must be finite.
+ */
+int dyra_q4_quantise(const void* W, int64_t c1, int64_t c2, int32_t group, int32_t dtype, void* codes, void* scale,
+                     void* zero, void* stream);
+
+/* The weight in dtype, device [c2][c1] (asynchronous): exact in fp32, rounded
+ * once in bf16. */
+int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* stream);
+
+/*
+ * Y = X W^T + bias (asynchronous on `stream`).
+ *   X: device [n][c1], rows ldx elements apart.  bias: device [c2] or NULL.
+ *   Y: device [n][c2], rows ldy apart; overlaps no operand.  Strides are
+ *   multiples of 8 (bf16) or 4 (fp32), at most 2^20.  n: 0 .. 2^24, n c1 and n
+ *   c2 < 2^33.
+ * Up to 64 rows need no workspace (0 bytes; the pointer may be NULL) and
+ * multiply the codes exactly; more rows read W rounded to bf16 (bf16) or
+ * exactly (fp32) from the workspace.  Sums are fp32; fp32 operands enter as
+ * three bf16 terms (2^-24).  An infinity in X may give NaN where the formula
+ * has an infinity.  Sums have a fixed order: the same call gives the same bits.
+ * Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
+ */
+int dyra_q4_workspace_size(int64_t c1, int64_t c2, int64_t n, int32_t dtype, int32_t backward, size_t* bytes);
+int dyra_q4_forward(const dyra_q4* w, const void* X, int64_t ldx, const void* bias, void* Y, int64_t ldy, int64_t n,
+                    int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The input gradient dX = dY W (the weight is frozen), dY: device [n][c2], dX:
+ * device [n][c1].  Other arguments, roundings and errors as for many rows of
+ * dyra_q4_forward; the workspace is dyra_q4_workspace_size(..., backward = 1).
+ */
+int dyra_q4_backward(const dyra_q4* w, const void* dY, int64_t lddy, void* dX, int64_t lddx, int64_t n, int32_t dtype,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Softmax cross entropy over a vocabulary, without its logits in memory.  For
  * hidden rows H [n][C], a head W [V][C] and targets[n]
  *   a_tv = scale H_t . W_v,  lse_t = log sum_v exp a_tv,

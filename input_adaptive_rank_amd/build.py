@@ -18,8 +18,9 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = shutil.which("hipcc") or os.path.join(ROCM, "bin", "hipcc")
 
 HOST_SOURCES = ["host_linalg.cpp", "prepare.cpp"]
-HIP_SOURCES = ["dyra_kernels.hip", "adapter_kernels.hip", "block_norm_kernels.hip", "vocab_loss_kernels.hip"]
-HEADERS = ["host_linalg.h", "spec.h", "device_common.h", "gemm_engine.h"]
+HIP_SOURCES = ["dyra_kernels.hip", "adapter_kernels.hip", "block_norm_kernels.hip", "q4_kernels.hip",
+               "vocab_loss_kernels.hip"]
+HEADERS = ["host_linalg.h", "spec.h", "device_common.h", "gemm_engine.h", "lds_dma.h", "mfma_product.h"]
 
 HOST_FLAGS = ["-O3", "-fPIC", "-std=c++17", "-mavx2", "-mfma", "-Wall", "-Wno-unused-function"]
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -1,0 +1,559 @@
+// Projections with 4-bit weights: w = scale (code - zero), one scale and zero
+// point for each row's group of 32, 64 or 128 columns.
+//   forward   Y = X W^T + bias        W [c2][c1]
+//   backward  dX = dY W               (the weight is frozen)
+//
+// Packed weight.  Codes lie in blocks of 16 rows x 128 columns, 1 KB in the
+// order in which the lanes of a wave read them as 16-column operands of
+// v_mfma_f32_16x16x32_bf16: lane (j, g) holds columns 32 s + 8 g + 0 .. 7 of
+// row j in its word s = 0 .. 3, the even columns in the low half.  A pair of
+// codes then becomes a pair of bf16 numbers 128 + code with one shift and one
+// and-or: 0x4300 is 128, whose last mantissa bit is worth 1.  Parameters lie as
+// [block of 16 rows][group][16] words, the bf16 scale above the bf16 number
+// 128 + zero.
+//
+// Few rows: each wave multiplies whole blocks of codes, in exact products,
+//   sum_k x (128 + code) - (128 + zero) sum_k x,
+// the last sum from one more product with ones, and scales each group's sum.
+// Many rows: W is written out once as bf16 (rounded: 2^-9 of a weight, below
+// the rounding of the result) and multiplied tile by tile; for fp32 operands
+// as two bf16 planes, which hold it exactly (8 bits of scale times 5).
+#include "mfma_product.h"
+
+namespace {
+
+using namespace product;
+
+constexpr int ROW_WAVES = 8;      // waves of a few-row workgroup
+constexpr int64_t FEW = 64;       // rows it takes
+
+struct Weight {
+  const uint4* codes;     // [row blocks][column blocks][64]
+  const uint32_t* params; // [row blocks][column blocks * groups a block][16]
+  int32_t c1, c2, kt;     // kt: column blocks
+};
+
+__device__ __forceinline__ float scale_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+__device__ __forceinline__ float zero_of(uint32_t p) { return __uint_as_float(p << 16); }   // 128 + zero
+
+// 128 + code of a word's eight columns, as bf16.
+__device__ __forceinline__ uint4 widen(uint32_t w) {
+  return make_uint4((w & 0x000f000fu) | 0x43004300u, (w >> 4 & 0x000f000fu) | 0x43004300u,
+                    (w >> 8 & 0x000f000fu) | 0x43004300u, (w >> 12 & 0x000f000fu) | 0x43004300u);
+}
+
+// code - zero of a word's eight columns, as bf16 (whole numbers below 16: exact).
+__device__ __forceinline__ uint4 centre(uint32_t w, float zero) {
+  const uint4 v = widen(w);
+  auto two = [&](uint32_t p) {
+    return pack_bf16x2(__uint_as_float(p << 16) - zero, __uint_as_float(p & 0xffff0000u) - zero);
+  };
+  return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+
+struct RowsArgs {
+  Weight w;
+  const void* X;
+  const void* bias;
+  void* Y;
+  int64_t ldx, ldy;
+  int32_t n;
+};
+
+// One block of 16 rows of W (columns of Y) a workgroup, its column blocks dealt
+// to the waves in turn; RT row blocks of X; GPB groups a column block.
+template <typename T, int RT, int GPB>
+__global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
+  __shared__ float red[ROW_WAVES][RT * 256];
+  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;   // column blocks under way
+  constexpr int NP = planes_of<T>();
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cb = blockIdx.x, t0 = blockIdx.y * RT * 16, kt = a.w.kt, c1 = a.w.c1;
+  const uint4* codes = a.w.codes + (int64_t)cb * kt * 64 + lane;
+  const uint32_t* params = a.w.params + (int64_t)cb * kt * GPB * 16 + j;
+  const T* X = reinterpret_cast<const T*>(a.X);
+  f32x4 sum[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) sum[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int b0 = w; b0 < kt; b0 += ROW_WAVES * U) {
+    uint4 q[U], x[U][RT][4][sizeof(T) / 2];
+    uint32_t p[U][GPB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * ROW_WAVES;
+      if (b >= kt) {   // nothing: a scale of zero
+        q[u] = zero4();
+#pragma unroll
+        for (int i = 0; i < GPB; ++i) p[u][i] = 0;
+      } else {
+        q[u] = codes[(int64_t)b * 64];
+#pragma unroll
+        for (int i = 0; i < GPB; ++i) p[u][i] = params[(b * GPB + i) * 16];
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int row = t0 + 16 * r + j, k = b * 128 + 32 * s + 8 * g;
+          const bool in = row < a.n && k < c1;
+          const uint4* at = reinterpret_cast<const uint4*>(X + row * a.ldx + k);
+#pragma unroll
+          for (int h = 0; h < (int)sizeof(T) / 2; ++h) x[u][r][s][h] = in ? at[h] : zero4();
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t words[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+      for (int i = 0; i < GPB; ++i) {
+        const float sc = scale_of(p[u][i]), zo = zero_of(p[u][i]);
+        f32x4 acc[RT], all[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = all[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = i * 4 / GPB; s < (i + 1) * 4 / GPB; ++s) {
+          if constexpr (NP == 1) {
+            const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+            const uint4 wq = widen(words[s]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              mma16(acc[r], x[u][r][s][0], wq);
+              mma16(all[r], x[u][r][s][0], ones);
+            }
+          } else {
+            const uint4 wq = centre(words[s], zo);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              float v[8] = {__uint_as_float(x[u][r][s][0].x), __uint_as_float(x[u][r][s][0].y),
+                            __uint_as_float(x[u][r][s][0].z), __uint_as_float(x[u][r][s][0].w),
+                            __uint_as_float(x[u][r][s][1].x), __uint_as_float(x[u][r][s][1].y),
+                            __uint_as_float(x[u][r][s][1].z), __uint_as_float(x[u][r][s][1].w)};
+#pragma unroll
+              for (int t = 0; t < 3; ++t) {
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                  v[2 * e] -= __uint_as_float(h[e] << 16);
+                  v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+                }
+                mma16(acc[r], make_uint4(h[0], h[1], h[2], h[3]), wq);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sum[r][e] = fmaf(sc, NP == 1 ? fmaf(-zo, all[r][e], acc[r][e]) : acc[r][e], sum[r][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(&red[w][r * 256 + lane * 4]) = sum[r];
+  __syncthreads();
+  const T* bias = reinterpret_cast<const T*>(a.bias);
+  for (int u = threadIdx.x; u < RT * 256; u += ROW_WAVES * 64) {
+    const int i = u >> 4, col = u & 15, row = t0 + i, o = cb * 16 + col;
+    if (row >= a.n || o >= a.w.c2) continue;
+    // D[i][col] of row block i / 16: lane col + 16 (i % 16 / 4), register i % 4
+    const int at = (i >> 4) * 256 + (col + 16 * (i >> 2 & 3)) * 4 + (i & 3);
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < ROW_WAVES; ++k) v += red[k][at];
+    if (bias) v += TT<T>::to_f(bias[o]);
+    reinterpret_cast<T*>(a.Y)[row * a.ldy + o] = TT<T>::from_f(v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the weight written out
+// ---------------------------------------------------------------------------
+
+// W as NP bf16 planes, row by row [c2][c1] or (TURN) transposed [c1][c2]; 128 x
+// 128 a workgroup.  One plane rounds W, two hold it exactly.
+template <int NP, bool TURN, int GPB>
+__global__ __launch_bounds__(256) void dense_kernel(Weight w, bf16_t* out, int64_t plane) {
+  __shared__ __attribute__((aligned(1024))) char lds[128 * 256];
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4, wv = threadIdx.x >> 6;
+  const int b = blockIdx.x % w.kt, o0 = blockIdx.x / w.kt * 128;
+  float v[2][4][8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int cb = o0 / 16 + wv * 2 + i;
+    const bool in = cb * 16 < w.c2;
+    const uint4 q = in ? w.codes[((int64_t)cb * w.kt + b) * 64 + lane] : zero4();
+    const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const uint32_t p = in ? w.params[((int64_t)cb * w.kt * GPB + b * GPB + s * GPB / 4) * 16 + j] : 0;
+      const float sc = scale_of(p), zo = zero_of(p);
+      const uint4 x = widen(words[s]);
+      const uint32_t h[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[i][s][2 * e] = sc * (__uint_as_float(h[e] << 16) - zo);
+        v[i][s][2 * e + 1] = sc * (__uint_as_float(h[e] & 0xffff0000u) - zo);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NP; ++t) {
+    if (t) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[e] = pack_bf16x2(v[i][s][2 * e], v[i][s][2 * e + 1]);
+          v[i][s][2 * e] -= __uint_as_float(h[e] << 16);
+          v[i][s][2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+        }
+        *reinterpret_cast<uint4*>(lds + tile_at((wv * 2 + i) * 16 + j, 4 * s + g, 16)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    __syncthreads();
+    const int rows = min(128, w.c2 - o0), cols = min(128, w.c1 - b * 128);
+    if constexpr (TURN)
+      tile_transposed<128, 128, 256>(lds, out + t * plane + (int64_t)b * 128 * w.c2 + o0, w.c2, rows, cols);
+    else tile_rows<128, 128, 256>(lds, out + t * plane + (int64_t)o0 * w.c1 + b * 128, w.c1, rows, cols);
+  }
+}
+
+// W in fp32, exact; eight columns a thread.
+__global__ __launch_bounds__(256) void dense_f32_kernel(Weight w, float* out, int gpb) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, words = w.c1 / 8;
+  const int64_t row = i / words;
+  const int k = (int)(i - row * words) * 8;
+  if (row >= w.c2) return;
+  const int64_t cb = row / 16, b = k / 128;
+  const int lane = (int)(row % 16) + 16 * (k % 32 / 8), s = k % 128 / 32;
+  const uint32_t q = reinterpret_cast<const uint32_t*>(w.codes)[((cb * w.kt + b) * 64 + lane) * 4 + s];
+  const uint32_t p = w.params[((cb * w.kt + b) * gpb + s * gpb / 4) * 16 + row % 16];
+  const float sc = scale_of(p), zo = zero_of(p);
+  const uint4 x = widen(q);
+  const uint32_t h[4] = {x.x, x.y, x.z, x.w};
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = sc * (__uint_as_float(h[e] << 16) - zo);
+    v[2 * e + 1] = sc * (__uint_as_float(h[e] & 0xffff0000u) - zo);
+  }
+  float4* o = reinterpret_cast<float4*>(out + row * w.c1 + k);
+  o[0] = make_float4(v[0], v[1], v[2], v[3]);
+  o[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// ---------------------------------------------------------------------------
+// making a weight
+// ---------------------------------------------------------------------------
+
+// The packed form of codes [c2][c1 / 2] (the even column in a byte's low
+// half), scales and zero points [c2][groups]; a lane of a block a thread.
+__global__ __launch_bounds__(256) void pack_kernel(const uint32_t* __restrict__ codes,
+                                                   const bf16_t* __restrict__ scale, const uint8_t* __restrict__ zero,
+                                                   uint4* __restrict__ out, uint32_t* __restrict__ params, int c1,
+                                                   int c2, int kt, int gpb, int64_t lanes) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= lanes) return;
+  const int lane = (int)(i & 63), j = lane & 15, g = lane >> 4;
+  const int64_t blk = i >> 6, cb = blk / kt, row = cb * 16 + j;
+  const int b = (int)(blk - cb * kt);
+  auto half = [](uint32_t v) {   // nibbles 0, 2, 4, 6 side by side
+    v &= 0x0f0f0f0fu;
+    v = (v | v >> 4) & 0x00ff00ffu;
+    return (v | v >> 8) & 0xffffu;
+  };
+  uint32_t w[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int k = b * 128 + 32 * s + 8 * g;
+    const uint32_t q = row < c2 && k < c1 ? codes[row * (c1 / 8) + k / 8] : 0;
+    w[s] = half(q) | half(q >> 4) << 16;
+  }
+  out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  const int group = 128 / gpb, groups = (c1 + group - 1) / group;
+  if (g < gpb) {   // lane group g writes group g of the block
+    const int q = b * gpb + g;
+    const bool in = row < c2 && q < groups;
+    const uint32_t z = in && zero ? zero[row * groups + q] & 15 : 8;
+    params[(cb * kt * gpb + q) * 16 + j] = (in ? (uint32_t)scale[row * groups + q] << 16 : 0u) | 0x4300u | z;
+  }
+}
+
+// Codes of a matrix to the nearest, ties to even.  Without zero points the
+// largest magnitude of a group is 7 scales; with them lowest and highest (0
+// among them) are 15 scales apart.  A scale is rounded to bf16 first.
+template <typename T>
+__global__ __launch_bounds__(256) void quantise_kernel(const T* __restrict__ W, int c1, int64_t c2, int group,
+                                                       uint8_t* __restrict__ codes, bf16_t* __restrict__ scale,
+                                                       uint8_t* __restrict__ zero) {
+  const int groups = (c1 + group - 1) / group;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 4;   // four lanes a group
+  const int part = threadIdx.x & 3;
+  const int64_t row = i / groups;
+  const int q = (int)(i - row * groups), k0 = q * group, k1 = min(k0 + group, c1);
+  const bool in = row < c2;
+  float lo = 0.f, hi = 0.f;
+  if (in)
+    for (int k = k0 + part * 8; k < k1; k += 32)
+      for (int e = 0; e < 8; ++e) {
+        const float v = TT<T>::to_f(W[row * c1 + k + e]);
+        lo = fminf(lo, v);
+        hi = fmaxf(hi, v);
+      }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    lo = fminf(lo, __shfl_xor(lo, d));
+    hi = fmaxf(hi, __shfl_xor(hi, d));
+  }
+  if (!in) return;
+  const float span = zero ? hi / 15.f - lo / 15.f : fmaxf(hi, -lo) / 7.f;
+  const bf16_t sc = f2bf(span);
+  const float s = bf2f(sc);
+  const float z = !zero ? 8.f : s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
+  for (int k = k0 + part * 8; k < k1; k += 32)
+    for (int e = 0; e < 8; e += 2) {
+      uint32_t c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float v = s > 0.f ? rintf(TT<T>::to_f(W[row * c1 + k + e + h]) / s) + z : z;
+        c[h] = (uint32_t)fminf(fmaxf(v, 0.f), 15.f);
+      }
+      codes[(row * c1 + k + e) / 2] = (uint8_t)(c[0] | c[1] << 4);
+    }
+  if (part == 0) {
+    scale[row * groups + q] = sc;
+    if (zero) zero[row * groups + q] = (uint8_t)z;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+int validate(int64_t c1, int64_t c2, int group) {
+  if (group != 32 && group != 64 && group != 128) return DYRA_EINVAL;
+  if (c1 <= 0 || c2 <= 0 || c1 % 8 || c2 % 8 || c1 > (int64_t)1 << 20 || c2 > (int64_t)1 << 20) return DYRA_ESHAPE;
+  if (c1 * c2 > (int64_t)1 << 34) return DYRA_ESHAPE;   // launches below 2^32 threads
+  return DYRA_OK;
+}
+
+int validate_call(const dyra_q4* w, int64_t n, int dtype) {
+  if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_EINVAL;
+  const int rc = validate(w->c1, w->c2, w->group);
+  if (rc) return rc;
+  if (n < 0 || n > (int64_t)1 << 24) return DYRA_ESHAPE;
+  if (n * std::max(w->c1, w->c2) >= (int64_t)1 << 33) return DYRA_ESHAPE;
+  return DYRA_OK;
+}
+
+int64_t code_bytes(int64_t c1, int64_t c2) { return cdiv(c2, 16) * cdiv(c1, 128) * 1024; }
+int64_t param_bytes(int64_t c1, int64_t c2, int group) { return cdiv(c2, 16) * cdiv(c1, 128) * (128 / group) * 64; }
+
+Weight weight_of(const dyra_q4& w) {
+  const char* p = reinterpret_cast<const char*>(w.packed);
+  return {reinterpret_cast<const uint4*>(p), reinterpret_cast<const uint32_t*>(p + code_bytes(w.c1, w.c2)),
+          (int32_t)w.c1, (int32_t)w.c2, (int32_t)cdiv(w.c1, 128)};
+}
+
+// Sizes of a call of many rows; few rows need no workspace.
+struct Plan {
+  bool few;
+  Pick tile;
+  size_t dense, planes, part, total;
+};
+
+// in, out: the reduced and the resulting width
+Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
+  Plan q{};
+  q.few = !backward && n <= FEW;
+  if (q.few) return q;
+  const bool wide = dtype == DYRA_F32;
+  q.tile = pick(n, out, (wide ? 5 : 1) * cdiv(in, 64), true);
+  size_t at = 0;
+  auto take = [&at](int64_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  q.dense = take((wide ? 4 : 2) * in * out);
+  if (wide) q.planes = take(6 * n * in);
+  if (q.tile.split > 1) q.part = take(4 * q.tile.split * n * out);
+  q.total = at;
+  return q;
+}
+
+template <typename T, int RT>
+void launch_rows(const RowsArgs& a, int group, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.w.c2, 16), (unsigned)cdiv(a.n, 16 * RT)), nt(ROW_WAVES * 64);
+  if (group == 128) hipLaunchKernelGGL((rows_kernel<T, RT, 1>), grid, nt, 0, st, a);
+  else if (group == 64) hipLaunchKernelGGL((rows_kernel<T, RT, 2>), grid, nt, 0, st, a);
+  else hipLaunchKernelGGL((rows_kernel<T, RT, 4>), grid, nt, 0, st, a);
+}
+
+template <int NP, bool TURN>
+void launch_dense(const Weight& w, int group, bf16_t* out, hipStream_t st) {
+  const dim3 grid((unsigned)(cdiv(w.c2, 128) * w.kt)), nt(256);
+  const int64_t plane = (int64_t)w.c1 * w.c2;
+  if (group == 128) hipLaunchKernelGGL((dense_kernel<NP, TURN, 1>), grid, nt, 0, st, w, out, plane);
+  else if (group == 64) hipLaunchKernelGGL((dense_kernel<NP, TURN, 2>), grid, nt, 0, st, w, out, plane);
+  else hipLaunchKernelGGL((dense_kernel<NP, TURN, 4>), grid, nt, 0, st, w, out, plane);
+}
+
+// out [n][cout] = in [n][cin] times the weight (TURN: its transpose was the forward's)
+template <typename T, bool TURN>
+int many(const dyra_q4& w, const T* in, int64_t ldi, const T* bias, T* out, int64_t ldo, int64_t n, const Plan& q,
+         char* ws, hipStream_t st) {
+  constexpr bool wide = sizeof(T) == 4;
+  const int64_t cin = TURN ? w.c2 : w.c1, cout = TURN ? w.c1 : w.c2;
+  bf16_t* dense = reinterpret_cast<bf16_t*>(ws + q.dense);
+  launch_dense<wide ? 2 : 1, TURN>(weight_of(w), w.group, dense, st);
+  Operand a{in, 2 * ldi, 0, (int32_t)n};
+  if constexpr (wide) {
+    bf16_t* planes = reinterpret_cast<bf16_t*>(ws + q.planes);
+    launch_planes<T>(in, ldi, n, cin, planes, nullptr, 0, n * cin, 0, nullptr, 0, st);
+    a = {planes, 2 * cin, 2 * n * cin, (int32_t)n};
+  }
+  const Job j = job(a, {dense, 2 * cin, 2 * cin * cout, (int32_t)cout}, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
+  if (q.tile.split == 1) {
+    launch_as(q.tile, j, Store<T>{out, ldo, 0, (int32_t)n, (int32_t)cout, bias, 0}, st);
+  } else {
+    float* part = reinterpret_cast<float*>(ws + q.part);
+    launch_as(q.tile, j, Store<float>{part, cout, n * cout, (int32_t)n, (int32_t)cout, nullptr, 0}, st);
+    hipLaunchKernelGGL((parts_kernel<T>), dim3((unsigned)cdiv(n * (cout / 4), 256)), dim3(256), 0, st, part, n * cout,
+                       q.tile.split, out, ldo, n, (int)cout, bias);
+  }
+  return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
+}
+
+template <typename T>
+int forward_impl(const dyra_q4& w, const T* X, int64_t ldx, const T* bias, T* Y, int64_t ldy, int64_t n,
+                 const Plan& q, char* ws, hipStream_t st) {
+  if (!q.few) return many<T, false>(w, X, ldx, bias, Y, ldy, n, q, ws, st);
+  const RowsArgs a{weight_of(w), X, bias, Y, ldx, ldy, (int32_t)n};
+  if (n <= 16) launch_rows<T, 1>(a, w.group, st);
+  else if (n <= 32) launch_rows<T, 2>(a, w.group, st);
+  else launch_rows<T, 4>(a, w.group, st);
+  return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
+}
+
+}  // namespace
+
+extern "C" int dyra_q4_packed_size(int64_t c1, int64_t c2, int32_t group, size_t* bytes) {
+  if (!bytes) return DYRA_EINVAL;
+  const int rc = validate(c1, c2, group);
+  if (rc) return rc;
+  *bytes = (size_t)(code_bytes(c1, c2) + param_bytes(c1, c2, group));
+  return DYRA_OK;
+}
+
+extern "C" int dyra_q4_pack(int64_t c1, int64_t c2, int32_t group, const void* codes, const void* scale,
+                            const void* zero, void* packed, void* stream) {
+  if (!codes || !scale || !packed) return DYRA_EINVAL;
+  const int rc = validate(c1, c2, group);
+  if (rc) return rc;
+  if (misaligned(codes, 3) || misaligned(scale, 1) || misaligned(packed, 15)) return DYRA_EINVAL;
+  const int64_t kt = cdiv(c1, 128), lanes = cdiv(c2, 16) * kt * 64;
+  char* p = reinterpret_cast<char*>(packed);
+  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)cdiv(lanes, 256)), dim3(256), 0,
+                     reinterpret_cast<hipStream_t>(stream), reinterpret_cast<const uint32_t*>(codes),
+                     reinterpret_cast<const bf16_t*>(scale), reinterpret_cast<const uint8_t*>(zero),
+                     reinterpret_cast<uint4*>(p), reinterpret_cast<uint32_t*>(p + code_bytes(c1, c2)), (int)c1, (int)c2,
+                     (int)kt, 128 / group, lanes);
+  return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
+}
+
+extern "C" int dyra_q4_quantise(const void* W, int64_t c1, int64_t c2, int32_t group, int32_t dtype, void* codes,
+                                void* scale, void* zero, void* stream) {
+  if (!W || !codes || !scale) return DYRA_EINVAL;
+  if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_EINVAL;
+  const int rc = validate(c1, c2, group);
+  if (rc) return rc;
+  if (misaligned(W, 15) || misaligned(codes, 3) || misaligned(scale, 1)) return DYRA_EINVAL;
+  const dim3 grid((unsigned)cdiv(c2 * cdiv(c1, group) * 4, 256)), nt(256);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  uint8_t *q = reinterpret_cast<uint8_t*>(codes), *z = reinterpret_cast<uint8_t*>(zero);
+  bf16_t* s = reinterpret_cast<bf16_t*>(scale);
+  if (dtype == DYRA_BF16)
+    hipLaunchKernelGGL((quantise_kernel<bf16_t>), grid, nt, 0, st, reinterpret_cast<const bf16_t*>(W), (int)c1, c2,
+                       group, q, s, z);
+  else
+    hipLaunchKernelGGL((quantise_kernel<float>), grid, nt, 0, st, reinterpret_cast<const float*>(W), (int)c1, c2,
+                       group, q, s, z);
+  return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
+}
+
+extern "C" int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* stream) {
+  if (!w || !w->packed || !out) return DYRA_EINVAL;
+  const int rc = validate_call(w, 0, dtype);
+  if (rc) return rc;
+  if (misaligned(w->packed, 15) || misaligned(out, 15)) return DYRA_EINVAL;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == DYRA_BF16) launch_dense<1, false>(weight_of(*w), w->group, reinterpret_cast<bf16_t*>(out), st);
+  else
+    hipLaunchKernelGGL(dense_f32_kernel, dim3((unsigned)cdiv(w->c2 * (w->c1 / 8), 256)), dim3(256), 0, st,
+                       weight_of(*w), reinterpret_cast<float*>(out), 128 / w->group);
+  return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
+}
+
+extern "C" int dyra_q4_workspace_size(int64_t c1, int64_t c2, int64_t n, int32_t dtype, int32_t backward,
+                                      size_t* bytes) {
+  if (!bytes || (backward != 0 && backward != 1)) return DYRA_EINVAL;
+  const dyra_q4 w{c1, c2, 128, nullptr};
+  const int rc = validate_call(&w, n, dtype);
+  if (rc) return rc;
+  *bytes = n ? (backward ? make_plan(c2, c1, n, dtype, true) : make_plan(c1, c2, n, dtype, false)).total : 0;
+  return DYRA_OK;
+}
+
+extern "C" int dyra_q4_forward(const dyra_q4* w, const void* X, int64_t ldx, const void* bias, void* Y, int64_t ldy,
+                               int64_t n, int32_t dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!w || !w->packed) return DYRA_EINVAL;
+  const int rc = validate_call(w, n, dtype);
+  if (rc) return rc;
+  if (misaligned(w->packed, 15)) return DYRA_EINVAL;
+  if (n == 0) return DYRA_OK;
+  if (!X || !Y || misaligned(X, 15) || misaligned(bias, 15) || misaligned(Y, 15) || misaligned(workspace, 15))
+    return DYRA_EINVAL;
+  if (bad_stride(ldx, w->c1, dtype) || bad_stride(ldy, w->c2, dtype)) return DYRA_ESHAPE;
+  const Plan q = make_plan(w->c1, w->c2, n, dtype, false);
+  if (q.total && !workspace) return DYRA_EINVAL;
+  if (ws_bytes < q.total) return DYRA_EWORKSPACE;
+  char* ws = reinterpret_cast<char*>(workspace);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == DYRA_BF16)
+    return forward_impl(*w, reinterpret_cast<const bf16_t*>(X), ldx, reinterpret_cast<const bf16_t*>(bias),
+                        reinterpret_cast<bf16_t*>(Y), ldy, n, q, ws, st);
+  return forward_impl(*w, reinterpret_cast<const float*>(X), ldx, reinterpret_cast<const float*>(bias),
+                      reinterpret_cast<float*>(Y), ldy, n, q, ws, st);
+}
+
+extern "C" int dyra_q4_backward(const dyra_q4* w, const void* dY, int64_t lddy, void* dX, int64_t lddx, int64_t n,
+                                int32_t dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!w || !w->packed) return DYRA_EINVAL;
+  const int rc = validate_call(w, n, dtype);
+  if (rc) return rc;
+  if (misaligned(w->packed, 15)) return DYRA_EINVAL;
+  if (n == 0) return DYRA_OK;
+  if (!dY || !dX || !workspace || misaligned(dY, 15) || misaligned(dX, 15) || misaligned(workspace, 15))
+    return DYRA_EINVAL;
+  if (bad_stride(lddy, w->c2, dtype) || bad_stride(lddx, w->c1, dtype)) return DYRA_ESHAPE;
+  const Plan q = make_plan(w->c2, w->c1, n, dtype, true);
+  if (ws_bytes < q.total) return DYRA_EWORKSPACE;
+  char* ws = reinterpret_cast<char*>(workspace);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == DYRA_BF16)
+    return many<bf16_t, true>(*w, reinterpret_cast<const bf16_t*>(dY), lddy, nullptr, reinterpret_cast<bf16_t*>(dX),
+                              lddx, n, q, ws, st);
+  return many<float, true>(*w, reinterpret_cast<const float*>(dY), lddy, nullptr, reinterpret_cast<float*>(dX), lddx, n,
+                           q, ws, st);
+}

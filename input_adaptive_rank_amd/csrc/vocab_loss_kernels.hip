@@ -16,10 +16,8 @@
 // the two products of the backward pass (2^-9 of each term, below the
 // rounding of the gradients, which are bf16).  fp32: every operand is three
 // bf16 planes (24 bits), a product the six pairs of planes that reach 2^-24.
-#include <algorithm>
 #include <cmath>
 
-#include "../../include/dyra.h"
 #include "mfma_product.h"
 
 namespace {
@@ -27,8 +25,6 @@ namespace {
 using namespace product;
 
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
-
-template <typename T> constexpr int planes_of() { return sizeof(T) == 2 ? 1 : 3; }
 
 // ---------------------------------------------------------------------------
 // forward
@@ -187,92 +183,6 @@ struct Gradient {
   }
 };
 
-// A matrix [rows][cols] as bf16 planes, row by row and transposed (rows padded
-// with zeros to ldt there); rows whose target is none of the vocabulary's are
-// zero in the transposed form, whatever they hold.
-template <typename T>
-struct Planes {
-  const T* in;
-  int64_t ld;
-  bf16_t *out, *outt;   // null: not wanted
-  int64_t ldo, ldt, plane, plane_t;
-  const int32_t* targets;   // or null
-  int32_t rows, cols, vocab;
-};
-
-template <typename T>
-__global__ __launch_bounds__(256) void planes_kernel(Planes<T> a, int blocks_c) {
-  constexpr int NP = planes_of<T>(), E = 8, PER = 128 * 16 / 256;   // 8-element chunks a thread
-  __shared__ __attribute__((aligned(1024))) char lds[128 * 256];
-  const int r0 = blockIdx.x / blocks_c * 128, c0 = blockIdx.x % blocks_c * 128;
-  float v[PER][E];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = threadIdx.x + i * 256, row = r0 + c / 16, col = c0 + c % 16 * 8;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-    if (row < a.rows && col < a.cols) {
-      const T* p = a.in + row * a.ld + col;
-      if constexpr (sizeof(T) == 2) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[i][2 * e] = __uint_as_float(q[e] << 16);
-          v[i][2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
-        }
-      } else {
-        const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-        v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NP; ++t) {
-    if (t) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = threadIdx.x + i * 256, rr = c / 16, row = r0 + rr, col = c0 + c % 16 * 8;
-      uint32_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = pack_bf16x2(v[i][2 * e], v[i][2 * e + 1]);
-        v[i][2 * e] -= __uint_as_float(h[e] << 16);
-        v[i][2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-      }
-      uint4 x = make_uint4(h[0], h[1], h[2], h[3]);
-      if (a.out && row < a.rows && col < a.cols)
-        *reinterpret_cast<uint4*>(a.out + t * a.plane + row * a.ldo + col) = x;
-      if (a.targets && row < a.rows && (a.targets[row] < 0 || a.targets[row] >= a.vocab)) x = zero4();
-      if (a.outt) *reinterpret_cast<uint4*>(lds + tile_at(rr, c % 16, 16)) = x;
-    }
-    if (!a.outt) continue;
-    __syncthreads();
-    tile_transposed<128, 128, 256>(lds, a.outt + t * a.plane_t + (int64_t)c0 * a.ldt + r0, a.ldt,
-                                   min(128, (int)a.ldt - r0), min(128, a.cols - c0));
-  }
-}
-
-// out = the sum of the parts, rounded once.
-template <typename T>
-__global__ __launch_bounds__(256) void parts_kernel(const float* __restrict__ part, int64_t slice, int parts,
-                                                    T* __restrict__ out, int64_t ld, int64_t rows, int cols) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = cols / 4;
-  const int64_t row = i / quads;
-  const int col = (int)(i - row * quads) * 4;
-  if (row >= rows) return;
-  float4 s = *reinterpret_cast<const float4*>(part + row * cols + col);
-  for (int p = 1; p < parts; ++p) {
-    const float4 v = *reinterpret_cast<const float4*>(part + p * slice + row * cols + col);
-    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-  }
-  T* o = out + row * ld + col;
-  if constexpr (sizeof(T) == 2)
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-  else *reinterpret_cast<float4*>(o) = s;
-}
-
 template <typename T>
 __global__ __launch_bounds__(256) void zero_kernel(T* __restrict__ out, int64_t elems) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < elems / 8; i += (int64_t)gridDim.x * 256)
@@ -282,39 +192,6 @@ __global__ __launch_bounds__(256) void zero_kernel(T* __restrict__ out, int64_t 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-
-size_t align256(int64_t b) { return ((size_t)b + 255) & ~(size_t)255; }
-int64_t up(int64_t a, int64_t m) { return cdiv(a, m) * m; }
-
-enum Shape { BIG, SMALL, THIN };
-
-// The tile of a product of m x n results over `steps` k-steps, and into how
-// many parts its steps are split (1 where only whole sums will do).
-struct Pick {
-  Shape shape;
-  int split;
-};
-
-Pick pick(int64_t m, int64_t n, int64_t steps, bool may_split) {
-  if (m <= 64) {
-    const int64_t tiles = cdiv(n, 128);
-    const int64_t s = may_split ? std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(1, tiles), steps / 8)) : 1;
-    return {THIN, (int)std::min<int64_t>(s, 16)};
-  }
-  const int64_t big = cdiv(m, 256) * cdiv(n, 256), small = cdiv(m, 128) * cdiv(n, 128);
-  if (big >= 200) return {BIG, 1};
-  const int64_t s = may_split ? std::max<int64_t>(1, std::min<int64_t>(cdiv(384, small), steps / 8)) : 1;
-  return {SMALL, (int)std::min<int64_t>(s, 16)};
-}
-
-template <class E>
-void launch_as(const Pick& p, const Job& j, const E& e, hipStream_t st) {
-  if (p.shape == BIG) launch<Big>(j, p.split, e, st);
-  else if (p.shape == SMALL) launch<Small>(j, p.split, e, st);
-  else launch<Thin>(j, p.split, e, st);
-}
-
-int64_t tile_cols(Shape s) { return s == BIG ? Big::BN : Small::BN; }
 
 // Sizes of a call.
 struct Plan {
@@ -383,21 +260,6 @@ int validate(int64_t n, int64_t C, int64_t V, int dtype) {
   // every launch has fewer than 2^32 threads
   if (n * C >= (int64_t)1 << 33 || n * V >= (int64_t)1 << 37) return DYRA_ESHAPE;
   return DYRA_OK;
-}
-
-bool misaligned(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
-
-bool bad_stride(int64_t ld, int64_t c, int dtype) {
-  return ld < c || ld > (int64_t)1 << 20 || ld % (dtype == DYRA_BF16 ? 8 : 4) != 0;
-}
-
-template <typename T>
-void launch_planes(const T* in, int64_t ld, int64_t rows, int64_t cols, bf16_t* out, bf16_t* outt, int64_t ldt,
-                   int64_t plane, int64_t plane_t, const int32_t* targets, int64_t vocab, hipStream_t st) {
-  const int64_t padded = outt ? ldt : rows;
-  const Planes<T> a{in, ld, out, outt, cols, ldt, plane, plane_t, targets, (int32_t)rows, (int32_t)cols, (int32_t)vocab};
-  const int64_t bc = cdiv(cols, 128), grid = cdiv(padded, 128) * bc;
-  hipLaunchKernelGGL((planes_kernel<T>), dim3((unsigned)grid), dim3(256), 0, st, a, (int)bc);
 }
 
 // The operands of the logits of a piece: H and W rows from v0.
@@ -474,7 +336,8 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
   }
   if (dH && !q.direct)
     hipLaunchKernelGGL((parts_kernel<T>), dim3((unsigned)cdiv(n * (C / 4), 256)), dim3(256), 0, st,
-                       reinterpret_cast<const float*>(ws + q.acc), n * C, q.dh.split, dH, lddh, n, (int)C);
+                       reinterpret_cast<const float*>(ws + q.acc), n * C, q.dh.split, dH, lddh, n, (int)C,
+                       (const T*)nullptr);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 

@@ -78,6 +78,10 @@ class BlockNormGrads(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in ("pre_weight", "pre_bias", "post_weight", "post_bias", "gate")]
 
 
+class Q4(ctypes.Structure):
+    _fields_ = [("c1", ctypes.c_int64), ("c2", ctypes.c_int64), ("group", ctypes.c_int32), ("packed", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -131,6 +135,13 @@ def lib():
                                      P],
             "dyra_adapter_backward": [ctypes.POINTER(Adapters), P, I64, P, I64, P, P, I64, P, I64, P, P, I64, I64, P,
                                       P, I32, P, SZ, P],
+            "dyra_q4_packed_size": [I64, I64, I32, ctypes.POINTER(SZ)],
+            "dyra_q4_pack": [I64, I64, I32, P, P, P, P, P],
+            "dyra_q4_quantise": [P, I64, I64, I32, I32, P, P, P, P],
+            "dyra_q4_dense": [ctypes.POINTER(Q4), P, I32, P],
+            "dyra_q4_workspace_size": [I64, I64, I64, I32, I32, ctypes.POINTER(SZ)],
+            "dyra_q4_forward": [ctypes.POINTER(Q4), P, I64, P, P, I64, I64, I32, P, SZ, P],
+            "dyra_q4_backward": [ctypes.POINTER(Q4), P, I64, P, I64, I64, I32, P, SZ, P],
             "dyra_vocab_loss_workspace_size": [I64, I64, I64, I32, I32, I32, I32, ctypes.POINTER(SZ)],
             "dyra_vocab_loss_forward": [P, I64, P, P, ctypes.c_float, P, P, I64, I64, I64, I32, P, SZ, P],
             "dyra_vocab_loss_backward": [P, I64, P, P, P, P, ctypes.c_float, P, I64, P, I64, I64, I64, I32, P, SZ, P],
