@@ -368,7 +368,7 @@ Weight weight_of(const dyra_q4& w) {
 // Sizes of a call of many rows; few rows need no workspace.
 struct Plan {
   bool few;
-  Pick tile;
+  Shape tile;
   size_t dense, planes, part, total;
 };
 
@@ -378,7 +378,8 @@ Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
   q.few = !backward && n <= FEW;
   if (q.few) return q;
   const bool wide = dtype == DYRA_F32;
-  q.tile = pick(n, out, (wide ? 5 : 1) * cdiv(in, 64), true);
+  const Job j = job({nullptr, 0, 0, (int32_t)n}, {nullptr, 0, 0, (int32_t)out}, in, wide ? 5 : 1, 0);
+  q.tile = shape_of(j);
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
     const size_t here = at;
@@ -387,7 +388,7 @@ Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
   };
   q.dense = take((wide ? 4 : 2) * in * out);
   if (wide) q.planes = take(6 * n * in);
-  if (q.tile.split > 1) q.part = take(4 * q.tile.split * n * out);
+  q.part = take(part_bytes(q.tile, j));
   q.total = at;
   return q;
 }
@@ -420,18 +421,12 @@ int many(const dyra_q4& w, const T* in, int64_t ldi, const T* bias, T* out, int6
   Operand a{in, 2 * ldi, 0, (int32_t)n};
   if constexpr (wide) {
     bf16_t* planes = reinterpret_cast<bf16_t*>(ws + q.planes);
-    launch_planes<T>(in, ldi, n, cin, planes, nullptr, 0, n * cin, 0, nullptr, 0, st);
+    launch_planes<T>(in, ldi, n, cin, planes, nullptr, 0, n * cin, 0, nullptr, nullptr, st);
     a = {planes, 2 * cin, 2 * n * cin, (int32_t)n};
   }
-  const Job j = job(a, {dense, 2 * cin, 2 * cin * cout, (int32_t)cout}, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
-  if (q.tile.split == 1) {
-    launch_as(q.tile, j, Store<T>{out, ldo, 0, (int32_t)n, (int32_t)cout, bias, 0}, st);
-  } else {
-    float* part = reinterpret_cast<float*>(ws + q.part);
-    launch_as(q.tile, j, Store<float>{part, cout, n * cout, (int32_t)n, (int32_t)cout, nullptr, 0}, st);
-    hipLaunchKernelGGL((parts_kernel<T>), dim3((unsigned)cdiv(n * (cout / 4), 256)), dim3(256), 0, st, part, n * cout,
-                       q.tile.split, out, ldo, n, (int)cout, bias);
-  }
+  Job j = job(a, {dense, 2 * cin, 2 * cin * cout, (int32_t)cout}, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
+  j.part = reinterpret_cast<float4*>(ws + q.part);
+  launch_as(q.tile, j, Store<T>{out, ldo, (int32_t)cout, bias, nullptr, nullptr}, st);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 

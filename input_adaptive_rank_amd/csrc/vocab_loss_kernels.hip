@@ -30,70 +30,62 @@ constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // forward
 // ---------------------------------------------------------------------------
 
-// The tile's part of each row's softmax, in powers of two: maximum m and
-// sum of 2^(a - m) over its columns; the target's logit where it lies here.
+// Each row's softmax over 64 columns, in powers of two: the maximum m and the
+// sum of 2^(a - m); and the target's logit where it lies among them.
 struct RowStats {
-  float2* part;             // [tiles of columns][rows]
+  float2* part;             // [blocks of 64 columns][rows]
   float* mine;              // [rows] logit of the target
   const int32_t* targets;
   float scale;
-  int32_t rows, cols;       // of H, of this piece of W
-  int32_t v0, t0;           // first column and tile of the piece
+  int32_t cols, v0;         // of this piece of W; its first, a multiple of 64
 
   template <class C>
-  __device__ __forceinline__ void operator()(Acc<C>& acc, char* lds, int m0, int n0, int, int wm, int wn) const {
-    const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5;
+  __device__ __forceinline__ void block(const f32x16 (&v)[C::FN], char*, int row0, int col0, int rows) const {
+    const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5, row = row0 + l;
+    if (col0 >= cols) return;
     const float k2 = scale * LOG2E;
-    float2* st = reinterpret_cast<float2*>(lds);
-    const int c0 = n0 + wn * C::WN;
-    const bool edge = c0 + C::WN > cols;
+    const int at = (int)((unsigned)(row < rows ? targets[row] : -1) - (unsigned)(v0 + col0));
+    const bool has = (unsigned)at < (unsigned)min(C::WN, cols - col0) && (at >> 2 & 1) == g;
+    if (__any(has)) {
+#pragma unroll
+      for (int i = 0; i < 16 * C::FN; ++i)
+        if (has && i == ((at >> 5) * 16 + (at >> 3 & 3) * 4 + (at & 3))) mine[row] = v[i / 16][i % 16] * scale;
+    }
+    const int edge = cols - col0 - 4 * g;   // columns from here on are none
+    float a[16 * C::FN];
+#pragma unroll
+    for (int i = 0; i < 16 * C::FN; ++i) {
+      a[i] = v[i / 16][i % 16];
+      if (edge < C::WN) a[i] = i / 16 * 32 + (i % 16 / 4) * 8 + i % 4 < edge ? a[i] : -INFINITY;
+    }
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16 * C::FN; ++i) top = fmaxf(top, a[i]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // nothing above -inf: exponents are taken from 0, so that a NaN stays
+    const float m2 = top == -INFINITY ? 0.f : top * k2;
+#pragma unroll
+    for (int i = 0; i < 16 * C::FN; ++i) sum += __builtin_amdgcn_exp2f(fmaf(a[i], k2, -m2));
+    sum += __shfl_xor(sum, 32);
+    if (g == 0 && row < rows)
+      part[(int64_t)((v0 + col0) / 64) * rows + row] = make_float2(top == -INFINITY ? -INFINITY : m2, sum);
+  }
+
+  template <class C>
+  __device__ __forceinline__ void tile(Acc<C>& acc, char* lds, int m0, int n0, int rows, int wm, int wn) const {
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
-      const int rr = wm * C::WM + fm * 32 + l, row = m0 + rr;
-      const int at = (int)((unsigned)(row < rows ? targets[row] : -1) - (unsigned)(v0 + c0));
-      const bool has = c0 < cols && (unsigned)at < (unsigned)min(C::WN, cols - c0) && (at >> 2 & 1) == g;
-      if (__any(has)) {
-#pragma unroll
-        for (int i = 0; i < 16 * C::FN; ++i)
-          if (has && i == ((at >> 5) * 16 + (at >> 3 & 3) * 4 + (at & 3))) mine[row] = acc[fm][i / 16][i % 16] * scale;
-      }
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < 16 * C::FN; ++i)
-          if (c0 + i / 16 * 32 + (i % 16 / 4) * 8 + 4 * g + i % 4 >= cols) acc[fm][i / 16][i % 16] = -INFINITY;
-      }
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16 * C::FN; ++i) top = fmaxf(top, acc[fm][i / 16][i % 16]);
-      top = fmaxf(top, __shfl_xor(top, 32));
-      // nothing above -inf: exponents are taken from 0, so that a NaN stays
-      const float m2 = top == -INFINITY ? 0.f : top * k2;
-#pragma unroll
-      for (int i = 0; i < 16 * C::FN; ++i) sum += __builtin_amdgcn_exp2f(fmaf(acc[fm][i / 16][i % 16], k2, -m2));
-      sum += __shfl_xor(sum, 32);
-      if (g == 0) st[rr * C::NWN + wn] = make_float2(top == -INFINITY ? -INFINITY : m2, sum);
-    }
-    __syncthreads();
-    for (int rr = threadIdx.x; rr < C::BM; rr += C::NT) {
-      if (m0 + rr >= rows) break;
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < C::NWN; ++i) top = fmaxf(top, st[rr * C::NWN + i].x);
-#pragma unroll
-      for (int i = 0; i < C::NWN; ++i) {
-        const float2 s = st[rr * C::NWN + i];
-        sum += s.x == -INFINITY ? s.y : s.y * __builtin_amdgcn_exp2f(s.x - top);   // an empty sum is 0, or NaN
-      }
-      part[(int64_t)(t0 + n0 / C::BN) * rows + m0 + rr] = make_float2(top, sum);
+      block<C>(acc[fm], lds, m0 + wm * C::WM + fm * 32, n0 + wn * C::WN, rows);
+      __builtin_amdgcn_sched_barrier(0);   // one block after the other: registers
     }
   }
 };
 
-// Joins a row's parts: 32 rows a workgroup, eight lanes a row.
-__global__ __launch_bounds__(256) void row_loss_kernel(const float2* __restrict__ part, const float* __restrict__ mine,
-                                                       const int32_t* __restrict__ targets, float* __restrict__ loss,
-                                                       float* __restrict__ lse, int rows, int vocab, int tiles) {
-  __shared__ float2 st[8][32];
+// Joins a row's parts: 32 rows a workgroup, 32 lanes a row.
+__global__ __launch_bounds__(1024) void row_loss_kernel(const float2* __restrict__ part, const float* __restrict__ mine,
+                                                        const int32_t* __restrict__ targets, float* __restrict__ loss,
+                                                        float* __restrict__ lse, int rows, int vocab, int blocks) {
+  __shared__ float2 st[32][32];
   const int rr = threadIdx.x & 31, k = threadIdx.x >> 5, row = blockIdx.x * 32 + rr;
   float top = -INFINITY, sum = 0.f;
   auto join = [&](float2 s) {
@@ -104,13 +96,19 @@ __global__ __launch_bounds__(256) void row_loss_kernel(const float2* __restrict_
   };
   if (row < rows) {
 #pragma unroll 8
-    for (int t = k; t < tiles; t += 8) join(part[(int64_t)t * rows + row]);
+    for (int t = k; t < blocks; t += 32) join(part[(int64_t)t * rows + row]);
   }
   st[k][rr] = make_float2(top, sum);
   __syncthreads();
+  if (k < 4) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) join(st[k + 4 * i][rr]);
+    st[k][rr] = make_float2(top, sum);
+  }
+  __syncthreads();
   if (k || row >= rows) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) join(st[i][rr]);
+  for (int i = 1; i < 4; ++i) join(st[i][rr]);
   const float all = top == -INFINITY ? logf(sum) : fmaf(top, LN2, logf(sum));
   lse[row] = all;
   const int t = targets[row];
@@ -121,39 +119,112 @@ __global__ __launch_bounds__(256) void row_loss_kernel(const float2* __restrict_
 // backward
 // ---------------------------------------------------------------------------
 
-// d of the tile, in NP bf16 planes, row by row and transposed.  Columns past
-// the piece's and rows past n are zero up to the padded sizes.
+// The rows that count: map[0 .. *live - 1], ascending, by the first workgroup;
+// the others set the rest's gradients to zero.
+template <typename T>
+__global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ targets, int n, int vocab,
+                                                    int32_t* __restrict__ live, int32_t* __restrict__ map,
+                                                    T* __restrict__ dH, int64_t ld, int C) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  if (blockIdx.x) {
+    const int row = (blockIdx.x - 1) * 16 + w;
+    if (row >= n) return;
+    const int t = targets[row];
+    if (t >= 0 && t < vocab) return;
+    constexpr int E = 16 / sizeof(T);
+    for (int c = lane * E; c < C; c += 64 * E) *reinterpret_cast<uint4*>(dH + row * ld + c) = zero4();
+    return;
+  }
+  constexpr int PER = 8;
+  __shared__ int sums[2][16];
+  int base = 0, flip = 0;
+  for (int r0 = 0; r0 < n; r0 += 1024 * PER, flip ^= 1) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int row = r0 + tid * PER + i, t = row < n ? targets[row] : -1;
+      bits |= (uint32_t)(t >= 0 && t < vocab) << i;
+    }
+    const int mine = __popc(bits);
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 63) sums[flip][w] = upto;
+    __syncthreads();
+    int at = base + upto - mine;
+    for (int i = 0; i < 16; ++i) {
+      const int o = sums[flip][i];
+      base += o;
+      if (i < w) at += o;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (bits >> i & 1) map[at++] = r0 + tid * PER + i;
+  }
+  if (tid == 0) *live = base;
+}
+
+// d of a tile, in NP bf16 planes, row by row and transposed.  Columns past the
+// piece's and rows past the last are zero up to the padded sizes.
 template <int NP>
 struct Gradient {
   bf16_t *d, *dt;               // [NP][rows][ldd], [NP][cols][ldt]; null: not wanted
   int64_t ldd, ldt, plane, plane_t;
   const float *lse, *dloss;
-  const int32_t* targets;
+  const int32_t *targets, *map;
   float scale;
-  int32_t rows, cols, vocab;    // of H, of this piece, in all
-  int32_t v0;
+  int32_t cols, v0;             // of this piece
+
+  // a row's logits to its d, in 32 x WN results
+  template <class C>
+  __device__ __forceinline__ void values(f32x16 (&v)[C::FN], int row, int col0, int rows) const {
+    const int g = (threadIdx.x & 63) >> 5;
+    const float k2 = scale * LOG2E;
+    const bool in = row < rows;
+    const int r = in ? map[row] : 0;
+    const float w = in ? dloss[r] * scale : 0.f, l2 = in ? -lse[r] * LOG2E : 0.f;
+    const int at = in ? targets[r] - v0 - col0 : -1;
+    const bool has = (unsigned)at < (unsigned)C::WN && (at >> 2 & 1) == g;
+#pragma unroll
+    for (int i = 0; i < 16 * C::FN; ++i) v[i / 16][i % 16] = __builtin_amdgcn_exp2f(fmaf(v[i / 16][i % 16], k2, l2));
+    if (__any(has)) {
+#pragma unroll
+      for (int i = 0; i < 16 * C::FN; ++i)
+        v[i / 16][i % 16] -= has && i == ((at >> 5) * 16 + (at >> 3 & 3) * 4 + (at & 3)) ? 1.f : 0.f;
+    }
+    const int edge = in ? cols - col0 - 4 * g : 0;   // columns from here on are none
+#pragma unroll
+    for (int i = 0; i < 16 * C::FN; ++i) {
+      const int c = i / 16 * 32 + (i % 16 / 4) * 8 + i % 4;
+      v[i / 16][i % 16] = edge >= C::WN || c < edge ? v[i / 16][i % 16] * w : 0.f;
+    }
+  }
+
+  // two neighbouring results as bf16; what is left of them for the next plane
+  __device__ static __forceinline__ uint32_t peel(f32x16& v, int i) {
+    const uint32_t h = pack_bf16x2(v[i], v[i + 1]);
+    if constexpr (NP > 1) {
+      v[i] -= __uint_as_float(h << 16);
+      v[i + 1] -= __uint_as_float(h & 0xffff0000u);
+    }
+    return h;
+  }
 
   template <class C>
-  __device__ __forceinline__ void operator()(Acc<C>& acc, char* lds, int m0, int n0, int, int wm, int wn) const {
+  __device__ __forceinline__ void tile(Acc<C>& acc, char* lds, int m0, int n0, int rows, int wm, int wn) const {
     static_assert(C::BM * C::BN * 2 <= C::LDS && C::BN % 128 == 0, "the tile fits the ring");
     constexpr int CPR = C::BN / 8;
     const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5;
-    const float k2 = scale * LOG2E;
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
-      const int row = m0 + wm * C::WM + fm * 32 + l;
-      const int target = row < rows ? targets[row] : -1;
-      const bool live = target >= 0 && target < vocab;
-      const float w = live ? dloss[row] * scale : 0.f, l2 = live ? -lse[row] * LOG2E : 0.f;
-      const int at = target - v0 - n0 - wn * C::WN - 4 * g;
-#pragma unroll
-      for (int i = 0; i < 16 * C::FN; ++i) {
-        const int c = i / 16 * 32 + (i % 16 / 4) * 8 + i % 4;
-        const float p = __builtin_amdgcn_exp2f(fmaf(acc[fm][i / 16][i % 16], k2, l2)) - (c == at ? 1.f : 0.f);
-        acc[fm][i / 16][i % 16] = live && n0 + wn * C::WN + 4 * g + c < cols ? w * p : 0.f;
-      }
+      values<C>(acc[fm], m0 + wm * C::WM + fm * 32 + l, n0 + wn * C::WN, rows);
+      __builtin_amdgcn_sched_barrier(0);   // one block after the other: registers
     }
-    const int valid = min(C::BM, rows - m0), padded = min(C::BM, (int)ldt - m0), wide = min(C::BN, (int)ldd - n0);
+    const int valid = min(C::BM, rows - m0), padded = min(C::BM, ((rows + 63) & ~63) - m0);
+    const int wide = min(C::BN, (int)ldd - n0);
 #pragma unroll
     for (int t = 0; t < NP; ++t) {
       if (t) __syncthreads();   // the plane before has been copied out
@@ -163,22 +234,53 @@ struct Gradient {
         for (int fn = 0; fn < C::FN; ++fn)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t h[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = 4 * q + 2 * e;
-              h[e] = pack_bf16x2(acc[fm][fn][i], acc[fm][fn][i + 1]);
-              if constexpr (NP > 1) {   // the rest is the next plane's
-                acc[fm][fn][i] -= __uint_as_float(h[e] << 16);
-                acc[fm][fn][i + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-              }
-            }
             const int row = wm * C::WM + fm * 32 + l, col = wn * C::WN + fn * 32 + 8 * q + 4 * g;
-            *reinterpret_cast<uint2*>(lds + tile_at(row, col / 8, CPR) + 8 * g) = make_uint2(h[0], h[1]);
+            const uint32_t x = peel(acc[fm][fn], 4 * q), y = peel(acc[fm][fn], 4 * q + 2);
+            *reinterpret_cast<uint2*>(lds + tile_at(row, col / 8, CPR) + 8 * g) = make_uint2(x, y);
           }
       __syncthreads();
       if (d) tile_rows<C::BM, C::BN, C::NT>(lds, d + t * plane + (int64_t)m0 * ldd + n0, ldd, valid, wide);
       if (dt) tile_transposed<C::BM, C::BN, C::NT>(lds, dt + t * plane_t + (int64_t)n0 * ldt + m0, ldt, padded, wide);
+    }
+  }
+
+  // one wave's 32 x 64 results
+  template <class C>
+  __device__ __forceinline__ void block(f32x16 (&v)[C::FN], char* lds, int row0, int col0, int rows) const {
+    const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5;
+    values<C>(v, row0 + l, col0, rows);
+    auto at = [](int row, int chunk) { return row * 128 + (((chunk ^ row ^ row >> 3) & 7) << 4); };
+    const int padded = (rows + 63) & ~63, wide = (int)ldd;
+#pragma unroll
+    for (int t = 0; t < NP; ++t) {
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int fn = 0; fn < C::FN; ++fn)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x = peel(v[fn], 4 * q), y = peel(v[fn], 4 * q + 2);
+          *reinterpret_cast<uint2*>(lds + at(l, fn * 4 + q) + 8 * g) = make_uint2(x, y);
+        }
+      __builtin_amdgcn_wave_barrier();
+      if (d) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 3), k = lane & 7, col = col0 + k * 8;
+          if (row0 + rr < rows && col < wide)
+            *reinterpret_cast<uint4*>(d + t * plane + (row0 + rr) * ldd + col) =
+                *reinterpret_cast<const uint4*>(lds + at(rr, k));
+        }
+      }
+      const int r0 = (lane & 3) * 8, k = lane >> 2;   // 8 x 8 elements a lane of the first half
+      if (dt && k < 8 && row0 + r0 < padded && col0 + k * 8 < wide) {
+        uint4 in[8], out[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) in[e] = *reinterpret_cast<const uint4*>(lds + at(r0 + e, k));
+        transpose8x8_b16(in, out);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(dt + t * plane_t + (col0 + k * 8 + e) * ldt + row0 + r0) = out[e];
+      }
     }
   }
 };
@@ -193,62 +295,68 @@ __global__ __launch_bounds__(256) void zero_kernel(T* __restrict__ out, int64_t 
 // host side
 // ---------------------------------------------------------------------------
 
+// The three products of a call, without operands: their sizes and shapes.
+Operand rows_of(int64_t rows) { return {nullptr, 0, 0, (int32_t)rows}; }
+
 // Sizes of a call.
 struct Plan {
-  int64_t np, nrow;                     // n padded
-  int64_t piece, pieces;                // columns of the vocabulary at a time
-  Pick logits, dh, dw;
-  int64_t tiles;                        // forward: tiles of columns in all
-  bool direct;                          // dH needs no fp32 parts
-  size_t part, mine, hp, ht, wp, wt, d, dt, acc, total;
+  int64_t np, nrow;                     // planes; rows padded for the transposed forms
+  int64_t piece;                        // columns of the vocabulary at a time
+  Shape logits, dh, dw;
+  size_t part, mine, live, map, hp, ht, wp, wt, d, dt, acc, parts, total;
 };
+
+const int32_t* const SOME = reinterpret_cast<const int32_t*>(4);   // "found on the device", for sizes alone
 
 Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool need_dh, bool need_dw) {
   Plan q{};
   const bool wide = dtype == DYRA_F32;
   q.np = wide ? 3 : 1;
   const int terms = wide ? 6 : 1;
-  q.nrow = up(std::max<int64_t>(n, 1), 64);
+  q.nrow = up(n, 64);
   // d of a piece, both ways, is at most 2^26 elements a plane pair (256 MB in
   // bf16, the last-level cache); planes of fp32 weights at most 2^28
-  int64_t most = V;
+  int64_t most = (int64_t)1 << 24;
   if (backward) most = std::min<int64_t>(most, ((int64_t)1 << 26) / q.nrow);
   if (wide) most = std::min<int64_t>(most, ((int64_t)1 << 28) / (3 * C));
   most = std::max<int64_t>(256, most & ~(int64_t)255);
-  q.pieces = cdiv(V, most);
-  q.piece = std::min(up(V, 64), up(cdiv(V, q.pieces), 256));
-  q.pieces = cdiv(V, q.piece);
-  const int64_t step = cdiv(C, 64);
-  q.logits = pick(n, q.piece, terms * step, false);
+  q.piece = std::min(up(V, 64), up(cdiv(V, cdiv(V, most)), 256));
+  const int32_t* live = backward ? SOME : nullptr;
+  const Job logits = job(rows_of(n), rows_of(q.piece), C, terms, 0, live);
+  // a 256 x 256 tile's d in three planes leaves the registers
+  q.logits = shape_of(logits, !(wide && backward));
+  int64_t parts = part_bytes(q.logits, logits);
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
     const size_t here = at;
     at += align256(bytes);
     return here;
   };
-  if (wide) {
-    q.hp = take(2 * q.np * n * C);
-    q.wp = take(2 * q.np * q.piece * C);
-  }
+  if (wide) q.wp = take(2 * q.np * q.piece * C);
+  if (wide || backward) q.hp = take(2 * q.np * n * C);
   if (!backward) {
-    q.tiles = (q.pieces - 1) * cdiv(q.piece, tile_cols(q.logits.shape)) +
-              cdiv(V - (q.pieces - 1) * q.piece, tile_cols(q.logits.shape));
-    q.part = take(8 * q.tiles * n);
+    q.part = take(8 * cdiv(V, 64) * n);
     q.mine = take(4 * n);
   } else {
+    q.live = take(4);
+    q.map = take(4 * n);
     if (need_dh) {
-      q.dh = pick(n, C, terms * cdiv(q.piece, 64), true);
-      q.direct = q.pieces == 1 && q.dh.split == 1;
+      const Job j = job(rows_of(n), rows_of(C), q.piece, terms, 0, live);
+      q.dh = shape_of(j);
+      parts = std::max(parts, part_bytes(q.dh, j));
       q.wt = take(2 * q.np * C * q.piece);
       q.d = take(2 * q.np * n * q.piece);
-      if (!q.direct) q.acc = take(4 * q.dh.split * n * C);
+      if (q.piece < V) q.acc = take(4 * n * C);
     }
     if (need_dw) {
-      q.dw = pick(q.piece, C, terms * cdiv(q.nrow, 64), false);
+      const Job j = job(rows_of(q.piece), rows_of(C), q.nrow, terms, 0, live, true);
+      q.dw = shape_of(j);
+      parts = std::max(parts, part_bytes(q.dw, j));
       q.ht = take(2 * q.np * C * q.nrow);
       q.dt = take(2 * q.np * q.piece * q.nrow);
     }
   }
+  q.parts = take(parts);
   q.total = at;
   return q;
 }
@@ -262,15 +370,15 @@ int validate(int64_t n, int64_t C, int64_t V, int dtype) {
   return DYRA_OK;
 }
 
-// The operands of the logits of a piece: H and W rows from v0.
+// The logits of a piece: rows of H (or of its planes) by rows of W from v0.
 template <typename T>
-Job logits_job(const T* H, int64_t ldh, const T* W, int64_t v0, int64_t cols, int64_t n, int64_t C, const Plan& q,
-               char* ws) {
-  if constexpr (sizeof(T) == 2)
-    return job({H, 2 * ldh, 0, (int32_t)n}, {W + v0 * C, 2 * C, 0, (int32_t)cols}, C, 1, TERMS_1);
-  else
-    return job({ws + q.hp, 2 * C, 2 * n * C, (int32_t)n}, {ws + q.wp, 2 * C, 2 * q.piece * C, (int32_t)cols}, C, 6,
-               TERMS_33);
+Job logits_job(Operand h, const T* W, int64_t v0, int64_t cols, int64_t C, const Plan& q, char* ws,
+               const int32_t* live) {
+  Job j;
+  if constexpr (sizeof(T) == 2) j = job(h, {W + v0 * C, 2 * C, 0, (int32_t)cols}, C, 1, TERMS_1, live);
+  else j = job(h, {ws + q.wp, 2 * C, 2 * q.piece * C, (int32_t)cols}, C, 6, TERMS_33, live);
+  j.part = reinterpret_cast<float4*>(ws + q.parts);
+  return j;
 }
 
 template <typename T>
@@ -279,20 +387,21 @@ int forward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, fl
   constexpr bool wide = sizeof(T) == 4;
   float2* part = reinterpret_cast<float2*>(ws + q.part);
   float* mine = reinterpret_cast<float*>(ws + q.mine);
-  if constexpr (wide)
-    launch_planes<T>(H, ldh, n, C, reinterpret_cast<bf16_t*>(ws + q.hp), nullptr, 0, n * C, 0, nullptr, 0, st);
-  int64_t t0 = 0;
+  Operand h{H, 2 * ldh, 0, (int32_t)n};
+  if constexpr (wide) {
+    h = {ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
+    launch_planes<T>(H, ldh, n, C, reinterpret_cast<bf16_t*>(ws + q.hp), nullptr, 0, n * C, 0, nullptr, nullptr, st);
+  }
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
     const int64_t cols = std::min(q.piece, V - v0);
     if constexpr (wide)
       launch_planes<T>(W + v0 * C, C, cols, C, reinterpret_cast<bf16_t*>(ws + q.wp), nullptr, 0, q.piece * C, 0,
-                       nullptr, 0, st);
-    const RowStats e{part, mine, targets, scale, (int32_t)n, (int32_t)cols, (int32_t)v0, (int32_t)t0};
-    launch_as(q.logits, logits_job<T>(H, ldh, W, v0, cols, n, C, q, ws), e, st);
-    t0 += cdiv(cols, tile_cols(q.logits.shape));
+                       nullptr, nullptr, st);
+    launch_as(q.logits, logits_job<T>(h, W, v0, cols, C, q, ws, nullptr),
+              RowStats{part, mine, targets, scale, (int32_t)cols, (int32_t)v0}, st);
   }
-  hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)cdiv(n, 32)), dim3(256), 0, st, part, mine, targets, loss, lse,
-                     (int)n, (int)V, (int)q.tiles);
+  hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)cdiv(n, 32)), dim3(1024), 0, st, part, mine, targets, loss, lse,
+                     (int)n, (int)V, (int)cdiv(V, 64));
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
@@ -303,41 +412,37 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
   constexpr int NP = planes_of<T>(), terms = NP == 3 ? 6 : 1;
   constexpr uint32_t pairs = NP == 3 ? TERMS_33 : TERMS_1;
   auto at = [&](size_t o) { return reinterpret_cast<bf16_t*>(ws + o); };
-  bf16_t* hp = NP == 3 ? at(q.hp) : nullptr;
-  bf16_t* ht = dW ? at(q.ht) : nullptr;
-  if (hp || ht)
-    launch_planes<T>(H, ldh, n, C, hp, ht, q.nrow, n * C, C * q.nrow, targets, V, st);
+  int32_t *live = reinterpret_cast<int32_t*>(ws + q.live), *map = reinterpret_cast<int32_t*>(ws + q.map);
+  float* acc = reinterpret_cast<float*>(ws + q.acc);
+  bf16_t *wp = NP == 3 ? at(q.wp) : nullptr, *wt = dH ? at(q.wt) : nullptr, *ht = dW ? at(q.ht) : nullptr;
+  hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets, (int)n,
+                     (int)V, live, map, dH, lddh, (int)C);
+  launch_planes<T>(H, ldh, n, C, at(q.hp), ht, ht ? q.nrow : 0, n * C, C * q.nrow, map, live, st);
+  const Operand h{at(q.hp), 2 * C, 2 * n * C, (int32_t)n};
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
-    const int64_t cols = std::min(q.piece, V - v0);
-    bf16_t* wp = NP == 3 ? at(q.wp) : nullptr;
-    bf16_t* wt = dH ? at(q.wt) : nullptr;
+    const int64_t cols = std::min(q.piece, V - v0), ldd = up(cols, 64);
     if (wp || wt)
-      launch_planes<T>(W + v0 * C, C, cols, C, wp, wt, up(cols, 64), q.piece * C, C * q.piece, nullptr, 0, st);
-    const int64_t ldd = up(cols, 64);
-    const Gradient<NP> e{dH ? at(q.d) : nullptr, dW ? at(q.dt) : nullptr, ldd, q.nrow, n * q.piece,
-                         q.piece * q.nrow, lse, dloss, targets, scale, (int32_t)n, (int32_t)cols, (int32_t)V,
-                         (int32_t)v0};
-    launch_as(q.logits, logits_job<T>(H, ldh, W, v0, cols, n, C, q, ws), e, st);
+      launch_planes<T>(W + v0 * C, C, cols, C, wp, wt, wt ? ldd : 0, q.piece * C, C * q.piece, nullptr, nullptr, st);
+    const Gradient<NP> e{dH ? at(q.d) : nullptr, dW ? at(q.dt) : nullptr, ldd,     q.nrow, n * q.piece,
+                         q.piece * q.nrow,       lse,                     dloss,   targets, map,
+                         scale,                  (int32_t)cols,           (int32_t)v0};
+    launch_as<NP == 1>(q.logits, logits_job<T>(h, W, v0, cols, C, q, ws, live), e, st);
     if (dH) {
-      const Job j = job({at(q.d), 2 * ldd, 2 * n * q.piece, (int32_t)n}, {wt, 2 * ldd, 2 * C * q.piece, (int32_t)C}, ldd,
-                        terms, pairs);
-      if (q.direct) {
-        launch_as(q.dh, j, Store<T>{dH, lddh, 0, (int32_t)n, (int32_t)C, nullptr, 0}, st);
-      } else {
-        launch_as(q.dh, j, Store<float>{reinterpret_cast<float*>(ws + q.acc), C, n * C, (int32_t)n, (int32_t)C, nullptr,
-                                        v0 > 0}, st);
-      }
+      Job j = job({at(q.d), 2 * ldd, 2 * n * q.piece, (int32_t)n}, {wt, 2 * ldd, 2 * C * q.piece, (int32_t)C}, ldd, terms,
+                  pairs, live);
+      j.part = reinterpret_cast<float4*>(ws + q.parts);
+      // pieces add up in fp32; the last rounds and puts the rows in their places
+      const float* prior = v0 ? acc : nullptr;
+      if (v0 + cols < V) launch_as(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr}, st);
+      else launch_as(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map}, st);
     }
     if (dW) {
-      const Job j = job({at(q.dt), 2 * q.nrow, 2 * q.piece * q.nrow, (int32_t)cols},
-                        {ht, 2 * q.nrow, 2 * C * q.nrow, (int32_t)C}, q.nrow, terms, pairs);
-      launch_as(q.dw, j, Store<T>{dW + v0 * C, C, 0, (int32_t)cols, (int32_t)C, nullptr, 0}, st);
+      Job j = job({at(q.dt), 2 * q.nrow, 2 * q.piece * q.nrow, (int32_t)cols},
+                  {ht, 2 * q.nrow, 2 * C * q.nrow, (int32_t)C}, q.nrow, terms, pairs, live, true);
+      j.part = reinterpret_cast<float4*>(ws + q.parts);
+      launch_as(q.dw, j, Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr}, st);
     }
   }
-  if (dH && !q.direct)
-    hipLaunchKernelGGL((parts_kernel<T>), dim3((unsigned)cdiv(n * (C / 4), 256)), dim3(256), 0, st,
-                       reinterpret_cast<const float*>(ws + q.acc), n * C, q.dh.split, dH, lddh, n, (int)C,
-                       (const T*)nullptr);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
