@@ -538,6 +538,11 @@ inline Shape shape_of(const Job& j, bool may_be_big = true) {
   return may_be_big && layout<Big>(j, -1).cost <= layout<Small>(j, -1).cost ? BIG : SMALL;
 }
 
+// Estimated microseconds of a product.
+inline double cost(Shape s, const Job& j) {
+  return 0.1 * (s == BIG ? layout<Big>(j, -1).cost : s == SMALL ? layout<Small>(j, -1).cost : layout<Thin>(j, -1).cost);
+}
+
 // Bytes of partial tiles that a product may leave.
 template <class C>
 inline int64_t part_bytes_as(const Job& j) {

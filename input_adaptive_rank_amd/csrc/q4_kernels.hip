@@ -25,7 +25,6 @@ namespace {
 using namespace product;
 
 constexpr int ROW_WAVES = 8;      // waves of a few-row workgroup
-constexpr int64_t FEW = 64;       // rows it takes
 
 struct Weight {
   const uint4* codes;     // [row blocks][column blocks][64]
@@ -64,112 +63,249 @@ struct RowsArgs {
   int32_t n;
 };
 
-// One block of 16 rows of W (columns of Y) a workgroup, its column blocks dealt
-// to the waves in turn; RT row blocks of X; GPB groups a column block.
-template <typename T, int RT, int GPB>
-__global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
-  __shared__ float red[ROW_WAVES][RT * 256];
-  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;   // column blocks under way
-  constexpr int NP = planes_of<T>();
-  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cb = blockIdx.x, t0 = blockIdx.y * RT * 16, kt = a.w.kt, c1 = a.w.c1;
-  const uint4* codes = a.w.codes + (int64_t)cb * kt * 64 + lane;
-  const uint32_t* params = a.w.params + (int64_t)cb * kt * GPB * 16 + j;
-  const T* X = reinterpret_cast<const T*>(a.X);
-  f32x4 sum[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) sum[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int b0 = w; b0 < kt; b0 += ROW_WAVES * U) {
-    uint4 q[U], x[U][RT][4][sizeof(T) / 2];
-    uint32_t p[U][GPB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = b0 + u * ROW_WAVES;
-      if (b >= kt) {   // nothing: a scale of zero
-        q[u] = zero4();
-#pragma unroll
-        for (int i = 0; i < GPB; ++i) p[u][i] = 0;
-      } else {
-        q[u] = codes[(int64_t)b * 64];
-#pragma unroll
-        for (int i = 0; i < GPB; ++i) p[u][i] = params[(b * GPB + i) * 16];
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int row = t0 + 16 * r + j, k = b * 128 + 32 * s + 8 * g;
-          const bool in = row < a.n && k < c1;
-          const uint4* at = reinterpret_cast<const uint4*>(X + row * a.ldx + k);
-#pragma unroll
-          for (int h = 0; h < (int)sizeof(T) / 2; ++h) x[u][r][s][h] = in ? at[h] : zero4();
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t words[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-#pragma unroll
-      for (int i = 0; i < GPB; ++i) {
-        const float sc = scale_of(p[u][i]), zo = zero_of(p[u][i]);
-        f32x4 acc[RT], all[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = all[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = i * 4 / GPB; s < (i + 1) * 4 / GPB; ++s) {
-          if constexpr (NP == 1) {
-            const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-            const uint4 wq = widen(words[s]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              mma16(acc[r], x[u][r][s][0], wq);
-              mma16(all[r], x[u][r][s][0], ones);
-            }
-          } else {
-            const uint4 wq = centre(words[s], zo);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              float v[8] = {__uint_as_float(x[u][r][s][0].x), __uint_as_float(x[u][r][s][0].y),
-                            __uint_as_float(x[u][r][s][0].z), __uint_as_float(x[u][r][s][0].w),
-                            __uint_as_float(x[u][r][s][1].x), __uint_as_float(x[u][r][s][1].y),
-                            __uint_as_float(x[u][r][s][1].z), __uint_as_float(x[u][r][s][1].w)};
-#pragma unroll
-              for (int t = 0; t < 3; ++t) {
-                uint32_t h[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-                  v[2 * e] -= __uint_as_float(h[e] << 16);
-                  v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-                }
-                mma16(acc[r], make_uint4(h[0], h[1], h[2], h[3]), wq);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sum[r][e] = fmaf(sc, NP == 1 ? fmaf(-zo, all[r][e], acc[r][e]) : acc[r][e], sum[r][e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(&red[w][r * 256 + lane * 4]) = sum[r];
-  __syncthreads();
+// The waves' sums of RT x OB blocks, added in their order, to Y.  Row i, column
+// col of a block lie in lane col + 16 (i / 4), register i % 4.
+template <typename T, int RT, int OB>
+__device__ __forceinline__ void store_sums(const RowsArgs& a, const float* red, int cb0, int t0) {
   const T* bias = reinterpret_cast<const T*>(a.bias);
-  for (int u = threadIdx.x; u < RT * 256; u += ROW_WAVES * 64) {
-    const int i = u >> 4, col = u & 15, row = t0 + i, o = cb * 16 + col;
+  for (int u = threadIdx.x; u < RT * OB * 256; u += ROW_WAVES * 64) {
+    const int i = u / (16 * OB), col = u % (16 * OB), row = t0 + i, o = cb0 * 16 + col;
     if (row >= a.n || o >= a.w.c2) continue;
-    // D[i][col] of row block i / 16: lane col + 16 (i % 16 / 4), register i % 4
-    const int at = (i >> 4) * 256 + (col + 16 * (i >> 2 & 3)) * 4 + (i & 3);
+    const int at = ((i >> 4) * OB + (col >> 4)) * 256 + ((col & 15) + 16 * (i >> 2 & 3)) * 4 + (i & 3);
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < ROW_WAVES; ++k) v += red[k][at];
+    for (int k = 0; k < ROW_WAVES; ++k) v += red[k * RT * OB * 256 + at];
     if (bias) v += TT<T>::to_f(bias[o]);
     reinterpret_cast<T*>(a.Y)[row * a.ldy + o] = TT<T>::from_f(v);
   }
+}
+
+// fp32: OB blocks of 16 rows of W (columns of Y) by RT blocks of 16 rows of X a
+// workgroup, the column blocks of both dealt to its waves in turn; GPB groups a
+// column block.  X enters as three bf16 terms, which the whole numbers code -
+// zero multiply exactly; splitting it is what costs (4096 -> 4096, 32 rows: 18
+// us), so that two blocks of W share it where there are workgroups enough.
+template <int RT, int OB, int GPB>
+__global__ __launch_bounds__(ROW_WAVES * 64) void rows_f32_kernel(RowsArgs a) {
+  __shared__ float red[ROW_WAVES][RT * OB * 256];
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cb0 = blockIdx.x * OB, t0 = blockIdx.y * RT * 16, kt = a.w.kt, c1 = a.w.c1;
+  const int blocks = (a.w.c2 + 15) / 16;
+  const float* X = reinterpret_cast<const float*>(a.X);
+  f32x4 sum[OB][RT];
+#pragma unroll
+  for (int o = 0; o < OB; ++o)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) sum[o][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int b = w; b < kt; b += ROW_WAVES) {
+    uint4 q[OB];
+    uint32_t p[OB][GPB];
+#pragma unroll
+    for (int o = 0; o < OB; ++o) {
+      const int64_t at = (int64_t)min(cb0 + o, blocks - 1) * kt + b;   // past the last: not stored
+      q[o] = a.w.codes[at * 64 + lane];
+#pragma unroll
+      for (int i = 0; i < GPB; ++i) p[o][i] = a.w.params[(at * GPB + i) * 16 + j];
+    }
+    float4 x[RT][4][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int row = t0 + 16 * r + j, k = b * 128 + 32 * s + 8 * g;
+        const bool in = row < a.n && k < c1;
+        const float4* at = reinterpret_cast<const float4*>(X + row * a.ldx + k);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[r][s][h] = in ? at[h] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+    for (int i = 0; i < GPB; ++i) {
+      f32x4 acc[OB][RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int o = 0; o < OB; ++o) acc[o][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = i * 4 / GPB; s < (i + 1) * 4 / GPB; ++s) {
+        uint4 wq[OB];
+#pragma unroll
+        for (int o = 0; o < OB; ++o)
+          wq[o] = centre(s == 0 ? q[o].x : s == 1 ? q[o].y : s == 2 ? q[o].z : q[o].w, zero_of(p[o][i]));
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          float v[8] = {x[r][s][0].x, x[r][s][0].y, x[r][s][0].z, x[r][s][0].w,
+                        x[r][s][1].x, x[r][s][1].y, x[r][s][1].z, x[r][s][1].w};
+#pragma unroll
+          for (int t = 0; t < 3; ++t) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+              v[2 * e] -= __uint_as_float(h[e] << 16);
+              v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int o = 0; o < OB; ++o) mma16(acc[o][r], make_uint4(h[0], h[1], h[2], h[3]), wq[o]);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 0; o < OB; ++o)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[o][r][e] = fmaf(scale_of(p[o][i]), acc[o][r][e], sum[o][r][e]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int o = 0; o < OB; ++o) *reinterpret_cast<f32x4*>(&red[w][(r * OB + o) * 256 + lane * 4]) = sum[o][r];
+  __syncthreads();
+  store_sums<float, RT, OB>(a, &red[0][0], cb0, t0);
+}
+
+// bf16: RT blocks of 16 rows of X by OB blocks of 16 rows of W a workgroup, the
+// column blocks of both dealt to its waves in turn.  Read as operands, X would
+// cost most: 16 rows of 64 bytes touch 16 lines, and a line is what a load
+// costs.  So each wave brings its column block of X in whole lines (eight rows
+// of 128 bytes a load) into its own part of LDS, half a block at a time, the next
+// one while this one is multiplied, and its codes and parameters beside it.
+// Nothing is shared between the waves before their sums.  48 rows, 4096 ->
+// 12288: 13.5 us (operands straight from memory 28, one block of W a workgroup 41).
+template <int RT, int OB, int GPB>
+__global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
+  constexpr int XH = RT * 2048, CODES = 2 * XH, PARAMS = CODES + OB * 1024, WAVE = PARAMS + GPB * 256;
+  constexpr int RED = RT * OB * 1024;   // a wave's sums
+  __shared__ __attribute__((aligned(1024))) char lds[ROW_WAVES * (WAVE > RED ? WAVE : RED)];
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cb0 = blockIdx.x * OB, t0 = blockIdx.y * RT * 16, kt = a.w.kt;
+  const int blocks = min(OB, (a.w.c2 + 15) / 16 - cb0);
+  const char* mine = lds + w * WAVE;
+  const uint32_t base = lds_addr(mine);
+  constexpr int OUT = (int)0x80000000u;   // reads as zero
+  const int ldx = (int)a.ldx * 2, row8 = lane >> 3, end = a.w.c1 * 2;
+  int vx[2 * RT];
+#pragma unroll
+  for (int d = 0; d < 2 * RT; ++d) {
+    const int row = 8 * d + row8;
+    vx[d] = t0 + row < a.n ? row * ldx + (((lane & 7) ^ (row >> 1 & 7)) << 4) : OUT;
+  }
+  const int vp = g < blocks ? (g * kt * GPB * 16 + j) * 4 : OUT;
+  const i32x4v rx = rsrc_words(reinterpret_cast<const char*>(a.X) + (int64_t)t0 * ldx, 0x7fffffffu);
+  const i32x4v rc = rsrc_words(a.w.codes + (int64_t)cb0 * kt * 64, 0x7fffffffu);
+  const i32x4v rp = rsrc_words(a.w.params + (int64_t)cb0 * kt * GPB * 16, 0x7fffffffu);
+  // half h of X's column block b; past the last block all of it is out of range,
+  // so that every turn has the same number of loads
+  auto load_x = [&](int b, auto half) __attribute__((always_inline)) {
+    constexpr int H = decltype(half)::value;
+    const int at = b * 256 + H * 128;
+    const bool all = b + 1 < kt;
+    static_for<0, 2 * RT>([&](auto d) __attribute__((always_inline)) {
+      constexpr int D = decltype(d)::value;
+      const int ch = ((lane & 7) ^ ((8 * D + row8) >> 1 & 7)) << 4;
+      dma16k<H * XH + D * 1024>(rx, all || at + ch < end ? vx[D] : OUT, at, base);
+    });
+  };
+  auto load_w = [&](int b) __attribute__((always_inline)) {
+    const bool in = b < kt;
+    static_for<0, OB>([&](auto o) __attribute__((always_inline)) {
+      constexpr int O = decltype(o)::value;
+      dma16k<CODES + O * 1024>(rc, in && O < blocks ? lane * 16 : OUT, (O * kt + b) * 1024, base);
+    });
+    static_for<0, GPB>([&](auto i) __attribute__((always_inline)) {
+      constexpr int I = decltype(i)::value;
+      dma4(rp, in ? vp : OUT, (b * GPB + I) * 64, base + PARAMS + I * 256);
+    });
+  };
+  f32x4 sum[OB][RT], acc[OB][RT], all[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int o = 0; o < OB; ++o) sum[o][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  std::integral_constant<int, 0> first;
+  std::integral_constant<int, 1> second;
+  load_x(w, first);
+  load_w(w);
+  load_x(w, second);
+  for (int b = w; b < kt; b += ROW_WAVES) {
+    uint4 q[OB];
+    uint32_t p[OB][GPB];
+    auto multiply_half = [&](auto half) __attribute__((always_inline)) {
+      constexpr int H = decltype(half)::value;
+      uint4 x[2][RT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const int row = 16 * r + j;
+          x[s][r] = *reinterpret_cast<const uint4*>(mine + H * XH + row * 128 + (((4 * s + g) ^ (row >> 1 & 7)) << 4));
+        }
+      if constexpr (H == 0) {
+#pragma unroll
+        for (int o = 0; o < OB; ++o) {
+          q[o] = *reinterpret_cast<const uint4*>(mine + CODES + o * 1024 + lane * 16);
+#pragma unroll
+          for (int i = 0; i < GPB; ++i)
+            p[o][i] = *reinterpret_cast<const uint32_t*>(mine + PARAMS + i * 256 + (o * 16 + j) * 4);
+        }
+      }
+      wait_lgkm0();   // read: the next turn's may land here
+      asm volatile("" ::: "memory");
+      load_x(b + ROW_WAVES, half);
+      if constexpr (H == 0) load_w(b + ROW_WAVES);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        constexpr int STEPS = 4 / GPB;   // of a group
+        const int step = 2 * H + s;
+        if (step % STEPS == 0) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            all[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int o = 0; o < OB; ++o) acc[o][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+          }
+        }
+        const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mma16(all[r], x[s][r], ones);
+#pragma unroll
+        for (int o = 0; o < OB; ++o) {
+          const uint4 wq = widen(step == 0 ? q[o].x : step == 1 ? q[o].y : step == 2 ? q[o].z : q[o].w);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) mma16(acc[o][r], x[s][r], wq);
+        }
+        if (step % STEPS == STEPS - 1) {
+#pragma unroll
+          for (int o = 0; o < OB; ++o) {
+            const float sc = scale_of(p[o][step / STEPS]), zo = zero_of(p[o][step / STEPS]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sum[o][r][e] = fmaf(sc, fmaf(-zo, all[r][e], acc[o][r][e]), sum[o][r][e]);
+          }
+        }
+      }
+    };
+    wait_vm_lgkm0<2 * RT>();   // this block's first half, codes and parameters have landed
+    asm volatile("" ::: "memory");
+    multiply_half(first);
+    wait_vm_lgkm0<2 * RT + OB + GPB>();   // its second half
+    asm volatile("" ::: "memory");
+    multiply_half(second);
+  }
+  wait_vm_lgkm0<0>();
+  __syncthreads();   // no load is under way: the waves' sums
+  float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int o = 0; o < OB; ++o) *reinterpret_cast<f32x4*>(red + ((w * RT + r) * OB + o) * 256 + lane * 4) = sum[o][r];
+  __syncthreads();
+  store_sums<bf16_t, RT, OB>(a, red, cb0, t0);
 }
 
 // ---------------------------------------------------------------------------
@@ -365,9 +501,40 @@ Weight weight_of(const dyra_q4& w) {
           (int32_t)w.c1, (int32_t)w.c2, (int32_t)cdiv(w.c1, 128)};
 }
 
-// Sizes of a call of many rows; few rows need no workspace.
+// How few rows run: RT x OB blocks a workgroup, and the estimated microseconds.
+struct FewRows {
+  int rt, ob;
+  double us;
+};
+
+// In bf16 a workgroup fills a CU's LDS, so that workgroups run in rounds of 256;
+// a round's time is made of its turns of eight column blocks, of its sums' way
+// through LDS and, but for the first, of its start.  Measured at 4096 -> 4096 (us): 1 row, RT OB = 1 1 4.7, 1 2
+// 5.2, 1 4 6.7; 64 rows, 2 1 9.7, 2 2 7.0, 2 4 9.4, 3 2 8.4; 384 rows, 2 4 28.7, 3 4 26.3.  fp32
+// splits X anew for each pair of blocks of W.
+FewRows few_rows(int64_t c1, int64_t c2, int64_t n, int dtype) {
+  const int64_t blocks = cdiv(c2, 16), turns_k = cdiv(cdiv(c1, 128), ROW_WAVES);
+  FewRows best{0, 0, 1e30};
+  if (dtype == DYRA_F32) {
+    const int rt = n <= 16 ? 1 : n <= 32 ? 2 : 4;
+    const int64_t groups = cdiv(n, 16 * rt);
+    const int ob = cdiv(blocks, 2) * groups >= 192 ? 2 : 1;
+    return {rt, ob, 2.5 + (double)cdiv(cdiv(blocks, ob) * groups, 256) * turns_k * rt * (2.0 + 0.25 * ob)};
+  }
+  for (int rt = 1; rt <= 3; ++rt)
+    for (int ob = 1; ob <= 4; ++ob) {
+      const double rounds = (double)cdiv(cdiv(blocks, ob) * cdiv(n, 16 * rt), 256);
+      const double turn = 0.4 + 0.16 * rt + 0.025 * ob + 0.12 * rt * ob;
+      const double us = 0.7 + rounds * (1.5 + turns_k * turn + 0.17 * rt * ob);
+      if (us < best.us) best = {rt, ob, us};
+    }
+  return best;
+}
+
+// Sizes of a call; few rows need no workspace.
 struct Plan {
   bool few;
+  FewRows rows;
   Shape tile;
   size_t dense, planes, part, total;
 };
@@ -375,11 +542,18 @@ struct Plan {
 // in, out: the reduced and the resulting width
 Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
   Plan q{};
-  q.few = !backward && n <= FEW;
-  if (q.few) return q;
   const bool wide = dtype == DYRA_F32;
   const Job j = job({nullptr, 0, 0, (int32_t)n}, {nullptr, 0, 0, (int32_t)out}, in, wide ? 5 : 1, 0);
   q.tile = shape_of(j);
+  if (!backward) {
+    // many rows: the weight is written out and read again, two or three launches.
+    // Few and many, measured, us: 4096 -> 4096, 384 rows 23 and 38, 768 45 and 49, 1024 64
+    // and 54; 4096 -> 12288, 384 rows 68 and 73, 512 95 and 78; fp32, 4096 -> 4096, 128 rows 42
+    // and 61, 256 81 and 75.
+    q.rows = few_rows(in, out, n, dtype);
+    q.few = q.rows.us <= 8 + (wide ? 4 + in * out / 2e6 : in * out / 3e6) + cost(q.tile, j);
+    if (q.few) return q;
+  }
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
     const size_t here = at;
@@ -393,12 +567,28 @@ Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
   return q;
 }
 
+template <typename T, int RT, int OB>
+void launch_rows_as(const RowsArgs& a, int group, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.w.c2, 16 * OB), (unsigned)cdiv(a.n, 16 * RT)), nt(ROW_WAVES * 64);
+  if constexpr (sizeof(T) == 2) {
+    if (group == 128) hipLaunchKernelGGL((rows_kernel<RT, OB, 1>), grid, nt, 0, st, a);
+    else if (group == 64) hipLaunchKernelGGL((rows_kernel<RT, OB, 2>), grid, nt, 0, st, a);
+    else hipLaunchKernelGGL((rows_kernel<RT, OB, 4>), grid, nt, 0, st, a);
+  } else {
+    if (group == 128) hipLaunchKernelGGL((rows_f32_kernel<RT, OB, 1>), grid, nt, 0, st, a);
+    else if (group == 64) hipLaunchKernelGGL((rows_f32_kernel<RT, OB, 2>), grid, nt, 0, st, a);
+    else hipLaunchKernelGGL((rows_f32_kernel<RT, OB, 4>), grid, nt, 0, st, a);
+  }
+}
+
 template <typename T, int RT>
-void launch_rows(const RowsArgs& a, int group, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(a.w.c2, 16), (unsigned)cdiv(a.n, 16 * RT)), nt(ROW_WAVES * 64);
-  if (group == 128) hipLaunchKernelGGL((rows_kernel<T, RT, 1>), grid, nt, 0, st, a);
-  else if (group == 64) hipLaunchKernelGGL((rows_kernel<T, RT, 2>), grid, nt, 0, st, a);
-  else hipLaunchKernelGGL((rows_kernel<T, RT, 4>), grid, nt, 0, st, a);
+void launch_rows(const RowsArgs& a, int ob, int group, hipStream_t st) {
+  if (ob == 1) launch_rows_as<T, RT, 1>(a, group, st);
+  else if (ob == 2) launch_rows_as<T, RT, 2>(a, group, st);
+  else if constexpr (sizeof(T) == 2) {
+    if (ob == 3) launch_rows_as<T, RT, 3>(a, group, st);
+    else launch_rows_as<T, RT, 4>(a, group, st);
+  }
 }
 
 template <int NP, bool TURN>
@@ -435,9 +625,9 @@ int forward_impl(const dyra_q4& w, const T* X, int64_t ldx, const T* bias, T* Y,
                  const Plan& q, char* ws, hipStream_t st) {
   if (!q.few) return many<T, false>(w, X, ldx, bias, Y, ldy, n, q, ws, st);
   const RowsArgs a{weight_of(w), X, bias, Y, ldx, ldy, (int32_t)n};
-  if (n <= 16) launch_rows<T, 1>(a, w.group, st);
-  else if (n <= 32) launch_rows<T, 2>(a, w.group, st);
-  else launch_rows<T, 4>(a, w.group, st);
+  if (q.rows.rt == 1) launch_rows<T, 1>(a, q.rows.ob, w.group, st);
+  else if (q.rows.rt == 2) launch_rows<T, 2>(a, q.rows.ob, w.group, st);
+  else launch_rows<T, sizeof(T) == 2 ? 3 : 4>(a, q.rows.ob, w.group, st);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
