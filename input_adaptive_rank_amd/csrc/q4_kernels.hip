@@ -15,7 +15,7 @@
 // Few rows: each wave multiplies whole blocks of codes, in exact products,
 //   sum_k x (128 + code) - (128 + zero) sum_k x,
 // the last sum from one more product with ones, and scales each group's sum.
-// Many rows: W is written out once as bf16 (rounded: 2^-9 of a weight, below
+// Many rows: W is written out once as bf16 (rounded: at most 2^-8 of a weight, like
 // the rounding of the result) and multiplied tile by tile; for fp32 operands
 // as two bf16 planes, which hold it exactly (8 bits of scale times 5).
 #include "mfma_product.h"

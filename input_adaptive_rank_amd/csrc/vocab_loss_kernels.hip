@@ -13,7 +13,7 @@
 // keep d within what the last-level cache holds.
 //
 // bf16: logits are sums of exact products in fp32; d is rounded to bf16 for
-// the two products of the backward pass (2^-9 of each term, below the
+// the two products of the backward pass (at most 2^-8 of a term, like the
 // rounding of the gradients, which are bf16).  fp32: every operand is three
 // bf16 planes (24 bits), a product the six pairs of planes that reach 2^-24.
 #include <cmath>
