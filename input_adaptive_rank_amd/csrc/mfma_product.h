@@ -1,15 +1,17 @@
 // Matrix products C = sum_t A_t B_t^T on bf16 MFMAs, with the caller's own
 // epilogue, for the 4-bit projection and the vocabulary loss.
 //
-// Both operands lie with the reduction axis contiguous ("rows" of K elements)
-// and come in one or more planes: an fp32 operand is held as bf16 planes
+// An operand lies with the reduction axis contiguous (rows of K elements), or
+// turned (K rows, as a weight lies for its input gradient and both operands of a
+// weight's gradient do): then the LDS turns it, four rows of 16 columns a read.
+// It comes in one or more planes: an fp32 operand is held as bf16 planes
 // hi + mid + lo (24 bits), and the product as the sum of the plane pairs
 // ("terms") whose size reaches the result's precision.  All terms of a tile
 // run through one accumulator.
 //
 // A workgroup computes a BM x BN tile.  Every wave loads its part of each
 // 64-element k-step straight into an NS-slot LDS ring (1 KB a wave
-// instruction, rows of 128 bytes swizzled as lds_off does) NS - 1 steps ahead,
+// instruction, whole lines, swizzled) NS - 1 steps ahead,
 // and multiplies its WM x WN part of the tile; one barrier a step hands a
 // landed slot over and a used one back.
 #pragma once
@@ -22,7 +24,10 @@
 namespace product {
 namespace {   // kernels made in one source file are not another's
 
-// Rows of K elements; row r of plane t at p + t * plane + r * ld (bytes).
+constexpr int OUT = (int)0x80000000u;   // an offset out of range: reads as zero
+
+// `rows` rows of K elements, or (turned) K rows of `rows` elements; row r of
+// plane t at p + t * plane + r * ld (bytes).
 struct Operand {
   const void* p;
   int64_t ld, plane;
@@ -46,6 +51,7 @@ constexpr uint32_t TERMS_32 = pair_of(2, 0) | pair_of(1, 1) << 4 | pair_of(1, 0)
 struct Job {
   Operand a, b;
   int32_t kbytes;      // bytes of a row that count, a multiple of 16
+  int32_t krows;       // rows of a turned operand that count
   int32_t nk, terms;
   uint32_t pairs;
   int32_t may_split, live_k;
@@ -86,7 +92,7 @@ typedef Tile<64, 128, 2, 2, 3, 2, 6> Thin;
 // 434 us instead of 568).  Product and join work it out from the sizes that
 // they find.
 struct Layout {
-  int rows, tiles_m, tiles_n, kbytes, nk;
+  int rows, tiles_m, tiles_n, kbytes, krows, nk;
   int whole, tail, split, per;   // tiles computed whole, tiles split, parts of one, steps of a part
   int count;                     // workgroups
   double cost;                   // tenths of a microsecond, estimated
@@ -97,12 +103,13 @@ __host__ __device__ inline Layout layout(const Job& j, int live) {
   Layout y;
   y.rows = j.a.rows;
   y.kbytes = j.kbytes;
+  y.krows = j.krows;
   y.nk = j.nk;
   if (live >= 0) {
     if (j.live_k) {
-      y.nk = (live + 63) / 64;
-      y.nk = y.nk < j.nk ? y.nk : j.nk;
-      y.kbytes = y.nk * 128;
+      y.krows = live < j.krows ? live : j.krows;
+      y.kbytes = 2 * y.krows;
+      y.nk = (y.krows + 63) / 64;
     } else {
       y.rows = live < y.rows ? live : y.rows;
     }
@@ -122,11 +129,11 @@ __host__ __device__ inline Layout layout(const Job& j, int live) {
       }
     }
   }
-  y.split = split;
+  y.per = (steps + split - 1) / split;
+  y.split = split > 1 ? (steps + y.per - 1) / y.per : 1;   // no part without a step
   y.tail = split > 1 ? rest : 0;
   y.whole = tiles - y.tail;
-  y.per = (steps + split - 1) / split;
-  y.count = y.whole + y.tail * split;
+  y.count = y.whole + y.tail * y.split;
   y.cost = (double)(tiles / C::SLOTS) * steps * C::STEP + least;
   return y;
 }
@@ -146,22 +153,64 @@ __device__ __forceinline__ void corner(const Layout& y, int t, int& m0, int& n0)
 template <class C>
 using Acc = f32x16[C::FM][C::FN];
 
-// acc += one k-step of a slot.  Lane (l, g) reads chunk 2 s + g of rows l + 32 f
-// of its part; sub-step s + 1 is read while s multiplies.  The operands are
-// swapped, so that lane (l, g) ends with row l of A and, in element 4 q + e,
-// column 8 q + 4 g + e of B.
-template <class C>
-__device__ __forceinline__ void multiply(const char* slot, Acc<C>& acc, int wm, int wn, int l, int g) {
-  const char* as = slot + (wm * C::WM + l) * 128;
-  const char* bs = slot + C::BM * 128 + (wn * C::WN + l) * 128;
-  const int h = (l >> 1) & 7;
+// A turned operand in a slot: 64 rows of W = BM or BN elements.  A 16-byte chunk
+// lies at chunk ^ turn(row): the four rows that 32 lanes read together lie in four
+// different quarters of the 256-byte bank window.
+template <int W>
+__device__ __forceinline__ int turn(int row) {
+  return W >= 128 ? (row & 3) << 2 : (row & 2) << 1;
+}
+
+// Four elements of one column: of 16 lanes, lane i gives the place of row i / 4,
+// columns 4 (i % 4) .. + 3, and receives column i of the four rows.
+__device__ __forceinline__ uint2 read_turned(const char* at) {
+  typedef short four __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) four*)(uintptr_t)(const __attribute__((address_space(3))) char*)at));
+}
+
+// F operands of 32 rows or columns of a wave, for one sub-step of 16 after the other.
+template <int W, int F, bool TURNED>
+struct Feed {
+  const char* at;       // of the slot's operand
+  int off[TURNED ? F : 1];
+
+  __device__ __forceinline__ Feed(const char* slot, int first, int lane) : at(slot) {
+    if constexpr (TURNED) {
+      const int i = lane & 15;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int chunk = first / 8 + 4 * f + 2 * (lane >> 4 & 1) + (i >> 1 & 1);
+        off[f] = (8 * (lane >> 5) + (i >> 2)) * (2 * W) + ((chunk ^ turn<W>(i >> 2)) << 4) + (i & 1) * 8;
+      }
+    } else {
+      at += (first + (lane & 31)) * 128;
+      off[0] = (lane >> 5) ^ (lane >> 1 & 7);   // chunk 2 s + lane / 32 at chunk ^ (row / 2 % 8)
+    }
+  }
+  __device__ __forceinline__ uint4 read(int s, int f) const {
+    if constexpr (TURNED) {
+      const uint2 a = read_turned(at + off[f] + 16 * s * (2 * W)), b = read_turned(at + off[f] + (16 * s + 4) * (2 * W));
+      return make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      return *reinterpret_cast<const uint4*>(at + f * 4096 + (((2 * s) ^ off[0]) << 4));
+    }
+  }
+};
+
+// acc += one k-step of a slot; sub-step s + 1 is read while s multiplies.  The
+// operands are swapped, so that lane (l, g) ends with row l of A and, in
+// element 4 q + e, column 8 q + 4 g + e of B.
+template <class C, bool TA, bool TB>
+__device__ __forceinline__ void multiply(const char* slot, Acc<C>& acc, int wm, int wn, int lane) {
+  const Feed<C::BM, C::FM, TA> a(slot, wm * C::WM, lane);
+  const Feed<C::BN, C::FN, TB> b(slot + C::BM * 128, wn * C::WN, lane);
   uint4 af[2][C::FM], bf[2][C::FN];
   auto load = [&](int s) __attribute__((always_inline)) {
-    const int at = (((2 * s + g) ^ h) & 7) << 4;
 #pragma unroll
-    for (int f = 0; f < C::FM; ++f) af[s & 1][f] = *reinterpret_cast<const uint4*>(as + f * 4096 + at);
+    for (int f = 0; f < C::FM; ++f) af[s & 1][f] = a.read(s, f);
 #pragma unroll
-    for (int f = 0; f < C::FN; ++f) bf[s & 1][f] = *reinterpret_cast<const uint4*>(bs + f * 4096 + at);
+    for (int f = 0; f < C::FN; ++f) bf[s & 1][f] = b.read(s, f);
   };
   load(0);
 #pragma unroll
@@ -176,17 +225,87 @@ __device__ __forceinline__ void multiply(const char* slot, Acc<C>& acc, int wm, 
   }
 }
 
+// The L loads with which a wave brings its part of an operand's k-step: 1 KB each,
+// eight rows of 128 bytes, or whole rows of a turned operand.
+template <int W, int L, int NW, bool TURNED>
+struct Bring {
+  int v[L], edge;   // offsets from the operand's corner; row or byte of the first within a step
+  const char* p;
+  int64_t ld;
+
+  // corner: of the tile's first row, or (turned) column; count: rows or columns from there on
+  __device__ __forceinline__ void aim(const Operand& o, int at, int plane) {
+    p = reinterpret_cast<const char*>(o.p) + plane * o.plane + (TURNED ? 2 * (int64_t)at : at * o.ld);
+    ld = o.ld;
+  }
+  __device__ __forceinline__ void open(const Operand& o, int count, int w, int lane) {
+    if constexpr (TURNED) {
+      constexpr int CPR = W / 8, RPB = 64 / CPR;   // chunks a row, rows a load
+      edge = w * RPB + lane / CPR;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int row = edge + i * NW * RPB, ch = (lane % CPR) ^ turn<W>(row);
+        v[i] = ch * 8 < count ? row * (int)o.ld + ch * 16 : OUT;
+      }
+    } else {
+      // row 8 w + lane / 8, 16-byte chunk (lane % 8) ^ (row / 2 % 8); NW is even
+      const int row0 = 8 * w + (lane >> 3);
+      edge = ((lane & 7) ^ ((row0 >> 1) & 7)) << 4;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int row = row0 + 8 * NW * i;
+        v[i] = row < count ? row * (int)o.ld + edge : OUT;
+      }
+    }
+  }
+  // step kt to LDS at `to`; live: whether it is one at all
+  template <int OFF>
+  __device__ __forceinline__ void step(int kt, int kbytes, int krows, bool live, uint32_t to) const {
+    if constexpr (TURNED) {
+      const i32x4v rs = rsrc_words(p + (int64_t)kt * 64 * ld, 0x7fffffffu);
+      constexpr int RPB = 512 / W;
+      if (live && kt * 64 + 64 <= krows) {
+        static_for<0, L>([&](auto i) __attribute__((always_inline)) {
+          constexpr int I = decltype(i)::value;
+          dma16k<OFF + I * NW * 1024>(rs, v[I], 0, to);
+        });
+      } else {
+        const int rows = live ? krows - kt * 64 : 0;
+        static_for<0, L>([&](auto i) __attribute__((always_inline)) {
+          constexpr int I = decltype(i)::value;
+          dma16k<OFF + I * NW * 1024>(rs, edge + I * NW * RPB < rows ? v[I] : OUT, 0, to);
+        });
+      }
+    } else {
+      const i32x4v rs = rsrc_words(p, 0x7fffffffu);
+      const int kb = kt * 128;
+      if (live && kb + 128 <= kbytes) {
+        static_for<0, L>([&](auto i) __attribute__((always_inline)) {
+          constexpr int I = decltype(i)::value;
+          dma16k<OFF + I * NW * 1024>(rs, v[I], kb, to);
+        });
+      } else {
+        const bool in = live && edge < kbytes - kb;
+        static_for<0, L>([&](auto i) __attribute__((always_inline)) {
+          constexpr int I = decltype(i)::value;
+          dma16k<OFF + I * NW * 1024>(rs, in ? v[I] : OUT, kb, to);
+        });
+      }
+    }
+  }
+};
+
 // Epilogues: e.tile<C>(acc, lds, m0, n0, rows, wm, wn) takes a whole tile (the
 // ring is its to use), e.block<C>(v, lds, row0, col0, rows) 32 x WN results of
 // one wave, which has 32 * WN floats of LDS.
-template <class C, class E>
+template <class C, bool TA, bool TB, class E>
 __global__ __launch_bounds__(C::NT, C::WPE) void product_kernel(Job j, E e) {
   __shared__ __attribute__((aligned(1024))) char ring[C::LDS];
   const Layout y = layout<C>(j, j.live ? *j.live : -1);
   if ((int)blockIdx.x >= y.count) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = w / C::NWN, wn = w % C::NWN, l = lane & 31, g = lane >> 5;
+  const int wm = w / C::NWN, wn = w % C::NWN;
   // whole tiles and parts are each dealt over the XCDs; a part if not negative
   const int over = (int)blockIdx.x - y.whole, part = over < 0 ? over : xcd_tile_id(over, y.count - y.whole);
   int m0, n0, first = 0, steps = j.terms * y.nk;
@@ -198,52 +317,23 @@ __global__ __launch_bounds__(C::NT, C::WPE) void product_kernel(Job j, E e) {
     first = z * y.per;
     steps = max(0, min(y.per, steps - first));
   }
-  // row 8 w + lane / 8 of the wave's row block 0, 16-byte chunk (lane % 8) ^ (row / 2 % 8)
-  const int row0 = 8 * w + (lane >> 3), ch = ((lane & 7) ^ ((row0 >> 1) & 7)) << 4;
-  const int lda = (int)j.a.ld, ldb = (int)j.b.ld;
-  constexpr int OUT = (int)0x80000000u;   // reads as zero
-  int va[C::LA], vb[C::LB];
-#pragma unroll
-  for (int i = 0; i < C::LA; ++i) {
-    const int r = row0 + 8 * C::NW * i;
-    va[i] = m0 + r < y.rows ? r * lda + ch : OUT;
-  }
-#pragma unroll
-  for (int i = 0; i < C::LB; ++i) {
-    const int r = row0 + 8 * C::NW * i;
-    vb[i] = n0 + r < j.b.rows ? r * ldb + ch : OUT;
-  }
+  Bring<C::BM, C::LA, C::NW, TA> a;
+  Bring<C::BN, C::LB, C::NW, TB> b;
+  a.open(j.a, y.rows - m0, w, lane);
+  b.open(j.b, j.b.rows - n0, w, lane);
   const uint32_t base = lds_addr(ring) + w * 1024;
   int term = y.nk ? first / y.nk : 0, kt = first - term * y.nk, left = steps;
-  i32x4v ra, rb;
   auto aim = [&]() __attribute__((always_inline)) {
     const uint32_t pr = j.pairs >> (4 * term);
-    ra = rsrc_words(reinterpret_cast<const char*>(j.a.p) + (int64_t)m0 * j.a.ld + (pr & 3) * j.a.plane, 0x7fffffffu);
-    rb = rsrc_words(reinterpret_cast<const char*>(j.b.p) + (int64_t)n0 * j.b.ld + (pr >> 2 & 3) * j.b.plane,
-                    0x7fffffffu);
+    a.aim(j.a, m0, pr & 3);
+    b.aim(j.b, n0, pr >> 2 & 3);
   };
   aim();
   // one k-step into a slot; past the last every lane reads out of range, so
   // that each step issues the same number of loads
   auto issue = [&](uint32_t slot) __attribute__((always_inline)) {
-    const int kb = kt * 128;
-    const uint32_t to = base + slot;
-    if (left > 0 && kb + 128 <= y.kbytes) {
-      static_for<0, C::LA>([&](auto i) __attribute__((always_inline)) {
-        dma16k<decltype(i)::value * C::NW * 1024>(ra, va[decltype(i)::value], kb, to);
-      });
-      static_for<0, C::LB>([&](auto i) __attribute__((always_inline)) {
-        dma16k<C::BM * 128 + decltype(i)::value * C::NW * 1024>(rb, vb[decltype(i)::value], kb, to);
-      });
-    } else {
-      const bool in = left > 0 && ch < y.kbytes - kb;
-      static_for<0, C::LA>([&](auto i) __attribute__((always_inline)) {
-        dma16k<decltype(i)::value * C::NW * 1024>(ra, in ? va[decltype(i)::value] : OUT, kb, to);
-      });
-      static_for<0, C::LB>([&](auto i) __attribute__((always_inline)) {
-        dma16k<C::BM * 128 + decltype(i)::value * C::NW * 1024>(rb, in ? vb[decltype(i)::value] : OUT, kb, to);
-      });
-    }
+    a.template step<0>(kt, y.kbytes, y.krows, left > 0, base + slot);
+    b.template step<C::BM * 128>(kt, y.kbytes, y.krows, left > 0, base + slot);
     if (--left > 0 && ++kt == y.nk) {
       kt = 0;
       ++term;
@@ -270,7 +360,7 @@ __global__ __launch_bounds__(C::NT, C::WPE) void product_kernel(Job j, E e) {
       bare_barrier();                                    // everyone's; the slot of step t - 1 is free
       issue(in);
       in = in + C::SLOT == C::LDS ? 0 : in + C::SLOT;
-      if constexpr (decltype(multiplies)::value) multiply<C>(ring + out, acc, wm, wn, l, g);
+      if constexpr (decltype(multiplies)::value) multiply<C, TA, TB>(ring + out, acc, wm, wn, lane);
       out = out + C::SLOT == C::LDS ? 0 : out + C::SLOT;
     }
   };
@@ -391,119 +481,56 @@ struct Store {
 };
 
 // ---------------------------------------------------------------------------
-// a bf16 tile in LDS, row by row or transposed to memory
+// planes
 // ---------------------------------------------------------------------------
 
-// 16-byte chunk of a tile whose rows hold a multiple of 16 chunks.  Sixteen
-// neighbouring rows, and sixteen rows eight apart (a transposing read), lie in
-// sixteen different places of the 256-byte bank window.
-__device__ __forceinline__ int tile_at(int row, int chunk, int chunks) {
-  return (row * chunks + (chunk ^ ((row ^ (row >> 3)) & 15))) * 16;
-}
-
-// rows x cols of the tile (each a multiple of 8 at most ROWS, COLS) to out[row][col]
-template <int ROWS, int COLS, int NT>
-__device__ __forceinline__ void tile_rows(const char* lds, bf16_t* out, int64_t ld, int rows, int cols) {
-  constexpr int CPR = COLS / 8;
-  for (int c = threadIdx.x; c < ROWS * CPR; c += NT) {
-    const int row = c / CPR, k = c % CPR;
-    if (row < rows && k * 8 < cols)
-      *reinterpret_cast<uint4*>(out + row * ld + k * 8) = *reinterpret_cast<const uint4*>(lds + tile_at(row, k, CPR));
-  }
-}
-
-// ... to out[col][row]: a thread turns 8 x 8 elements, neighbouring lanes the
-// next eight rows
-template <int ROWS, int COLS, int NT>
-__device__ __forceinline__ void tile_transposed(const char* lds, bf16_t* out, int64_t ld, int rows, int cols) {
-  constexpr int CPR = COLS / 8, RB = ROWS / 8;
-  for (int c = threadIdx.x; c < RB * CPR; c += NT) {
-    const int r0 = c % RB * 8, k = c / RB;
-    if (r0 < rows && k * 8 < cols) {
-      uint4 in[8], t[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) in[e] = *reinterpret_cast<const uint4*>(lds + tile_at(r0 + e, k, CPR));
-      transpose8x8_b16(in, t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + (int64_t)(k * 8 + e) * ld + r0) = t[e];
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// operands and results beside a product
-// ---------------------------------------------------------------------------
-
-// planes of an operand of type T
-template <typename T> constexpr int planes_of() { return sizeof(T) == 2 ? 1 : 3; }
-
-// A matrix [rows][cols] as bf16 planes, row by row and transposed (there padded
-// with zeros to ldt rows).  map: only its rows map[0 .. *live - 1].
+// A matrix [rows][cols] as bf16 planes, eight elements a thread.  map: only
+// its rows map[0 .. *live - 1].
 template <typename T>
 struct Planes {
   const T* in;
-  int64_t ld;
-  bf16_t *out, *outt;   // null: not wanted
-  int64_t ldo, ldt, plane, plane_t;
+  int64_t ld, plane;
+  bf16_t* out;                 // [planes][rows][cols]
   const int32_t *map, *live;   // or null
   int32_t rows, cols;
 };
 
 template <typename T>
-__global__ __launch_bounds__(256) void planes_kernel(Planes<T> a, int blocks_c) {
-  constexpr int NP = planes_of<T>(), E = 8, PER = 128 * 16 / 256;   // 8-element chunks a thread
-  __shared__ __attribute__((aligned(1024))) char lds[128 * 256];
-  const int r0 = blockIdx.x / blocks_c * 128, c0 = blockIdx.x % blocks_c * 128;
-  const int rows = a.live ? min(*a.live, a.rows) : a.rows;
-  const int padded = min((rows + 63) & ~63, (int)a.ldt);   // transposed rows that are read
-  if (r0 >= max(rows, a.outt ? padded : 0)) return;
-  float v[PER][E];
+__device__ __forceinline__ void make_planes(const Planes<T>& a, int64_t i) {
+  const int per = a.cols / 8;
+  const int64_t row = i / per;
+  const int col = (int)(i - row * per) * 8;
+  if (row >= (a.live ? min(*a.live, a.rows) : a.rows)) return;
+  const T* p = a.in + (a.map ? a.map[row] : row) * a.ld + col;
+  bf16_t* o = a.out + row * a.cols + col;
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(p);
+  } else {
+    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+    float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = threadIdx.x + i * 256, row = r0 + c / 16, col = c0 + c % 16 * 8;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-    if (row < rows && col < a.cols) {
-      const T* p = a.in + (a.map ? a.map[row] : row) * a.ld + col;
-      if constexpr (sizeof(T) == 2) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[i][2 * e] = __uint_as_float(q[e] << 16);
-          v[i][2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
-        }
-      } else {
-        const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-        v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NP; ++t) {
-    if (t) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = threadIdx.x + i * 256, rr = c / 16, row = r0 + rr, col = c0 + c % 16 * 8;
+    for (int t = 0; t < 3; ++t) {
       uint32_t h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        h[e] = pack_bf16x2(v[i][2 * e], v[i][2 * e + 1]);
-        v[i][2 * e] -= __uint_as_float(h[e] << 16);
-        v[i][2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+        h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        v[2 * e] -= __uint_as_float(h[e] << 16);
+        v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
       }
-      const uint4 x = make_uint4(h[0], h[1], h[2], h[3]);
-      if (a.out && row < rows && col < a.cols)
-        *reinterpret_cast<uint4*>(a.out + t * a.plane + row * a.ldo + col) = x;
-      if (a.outt) *reinterpret_cast<uint4*>(lds + tile_at(rr, c % 16, 16)) = x;
+      *reinterpret_cast<uint4*>(o + t * a.plane) = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    if (!a.outt) continue;
-    __syncthreads();
-    tile_transposed<128, 128, 256>(lds, a.outt + t * a.plane_t + (int64_t)c0 * a.ldt + r0, a.ldt,
-                                   min(128, padded - r0), min(128, a.cols - c0));
   }
 }
+
+// Two matrices in one launch, the first in `first` workgroups.
+template <typename T>
+__global__ __launch_bounds__(256) void planes_kernel(Planes<T> a, Planes<T> b, int first) {
+  if ((int)blockIdx.x < first) make_planes(a, (int64_t)blockIdx.x * 256 + threadIdx.x);
+  else make_planes(b, (int64_t)(blockIdx.x - first) * 256 + threadIdx.x);
+}
+
+// planes of an operand of type T
+template <typename T> constexpr int planes_of() { return sizeof(T) == 2 ? 1 : 3; }
 
 // ---------------------------------------------------------------------------
 // host side
@@ -511,14 +538,17 @@ __global__ __launch_bounds__(256) void planes_kernel(Planes<T> a, int blocks_c) 
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// live: what the rows of A (live_k: the reduction) are found to be, or null.
-inline Job job(Operand a, Operand b, int64_t K, int terms, uint32_t pairs, const int32_t* live = nullptr,
+// K: the reduction; Kb: as long as it is in memory where it lies contiguous (a
+// multiple of 8).  live: what the rows of A (live_k: the reduction) are found to
+// be, or null.
+inline Job job(Operand a, Operand b, int64_t K, int64_t Kb, int terms, uint32_t pairs, const int32_t* live = nullptr,
                bool live_k = false) {
   Job j{};
   j.a = a;
   j.b = b;
-  j.kbytes = (int32_t)(2 * K);
-  j.nk = (int32_t)cdiv(2 * K, 128);
+  j.kbytes = (int32_t)(2 * Kb);
+  j.krows = (int32_t)K;
+  j.nk = (int32_t)cdiv(K, 64);
   j.terms = terms;
   j.pairs = pairs;
   j.may_split = 1;
@@ -557,24 +587,28 @@ inline int64_t part_bytes(Shape s, const Job& j) {
   return s == BIG ? part_bytes_as<Big>(j) : s == SMALL ? part_bytes_as<Small>(j) : part_bytes_as<Thin>(j);
 }
 
-template <class C, class E>
+template <class C, bool TA, bool TB, class E>
 inline void launch(const Job& j, const E& e, hipStream_t st) {
   const Layout y = layout<C>(j, -1);
   // fewer live rows or steps may leave another number of tiles to split, into 2 SLOTS parts at most
   const int64_t grid = j.live ? (int64_t)y.tiles_m * y.tiles_n + (j.may_split ? 2 * C::SLOTS : 0) : y.count;
   if (!grid) return;
-  hipLaunchKernelGGL((product_kernel<C, E>), dim3((unsigned)grid), dim3(C::NT), 0, st, j, e);
+  hipLaunchKernelGGL((product_kernel<C, TA, TB, E>), dim3((unsigned)grid), dim3(C::NT), 0, st, j, e);
   const int64_t tail = j.live ? (j.may_split ? std::min(C::SLOTS, y.tiles_m * y.tiles_n) : 0) : y.tail;
   if (tail)
     hipLaunchKernelGGL((join_kernel<C, E>), dim3((unsigned)(tail * C::NW * C::FM)), dim3(64), 0, st, j, e);
 }
 
-template <bool MAY_BE_BIG = true, class E>
+// TA, TB: operands that lie turned.
+template <bool TA, bool TB, bool MAY_BE_BIG = true, class E>
 void launch_as(Shape s, const Job& j, const E& e, hipStream_t st) {
   if (MAY_BE_BIG && s == BIG) {
-    if constexpr (MAY_BE_BIG) launch<Big>(j, e, st);
-  } else if (s == SMALL) launch<Small>(j, e, st);
-  else launch<Thin>(j, e, st);
+    if constexpr (MAY_BE_BIG) launch<Big, TA, TB>(j, e, st);
+  } else if (s == SMALL) {
+    launch<Small, TA, TB>(j, e, st);
+  } else {
+    launch<Thin, TA, TB>(j, e, st);
+  }
 }
 
 inline bool misaligned(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
@@ -584,12 +618,16 @@ inline bool bad_stride(int64_t ld, int64_t c, int dtype) {
 }
 
 template <typename T>
-void launch_planes(const T* in, int64_t ld, int64_t rows, int64_t cols, bf16_t* out, bf16_t* outt, int64_t ldt,
-                   int64_t plane, int64_t plane_t, const int32_t* map, const int32_t* live, hipStream_t st) {
-  const int64_t padded = outt ? ldt : rows;
-  const Planes<T> a{in, ld, out, outt, cols, ldt, plane, plane_t, map, live, (int32_t)rows, (int32_t)cols};
-  const int64_t bc = cdiv(cols, 128), grid = cdiv(padded, 128) * bc;
-  hipLaunchKernelGGL((planes_kernel<T>), dim3((unsigned)grid), dim3(256), 0, st, a, (int)bc);
+Planes<T> planes(const T* in, int64_t ld, int64_t rows, int64_t cols, void* out, int64_t plane,
+                 const int32_t* map = nullptr, const int32_t* live = nullptr) {
+  return {in, ld, plane, reinterpret_cast<bf16_t*>(out), map, live, (int32_t)rows, (int32_t)cols};
+}
+
+template <typename T>
+void launch_planes(const Planes<T>& a, const Planes<T>& b, hipStream_t st) {
+  const int64_t na = cdiv((int64_t)a.rows * (a.cols / 8), 256), nb = cdiv((int64_t)b.rows * (b.cols / 8), 256);
+  if (na + nb)
+    hipLaunchKernelGGL((planes_kernel<T>), dim3((unsigned)(na + nb)), dim3(256), 0, st, a, b, (int)na);
 }
 
 }  // namespace

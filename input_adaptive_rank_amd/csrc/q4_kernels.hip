@@ -16,8 +16,8 @@
 //   sum_k x (128 + code) - (128 + zero) sum_k x,
 // the last sum from one more product with ones, and scales each group's sum.
 // Many rows: W is written out once as bf16 (rounded: at most 2^-8 of a weight, like
-// the rounding of the result) and multiplied tile by tile; for fp32 operands
-// as two bf16 planes, which hold it exactly (8 bits of scale times 5).
+// the rounding of the result) and multiplied tile by tile, for the backward pass
+// turned on its way; for fp32 operands as two bf16 planes, which hold it exactly (8 bits of scale times 5).
 #include "mfma_product.h"
 
 namespace {
@@ -312,55 +312,53 @@ __global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
 // the weight written out
 // ---------------------------------------------------------------------------
 
-// W as NP bf16 planes, row by row [c2][c1] or (TURN) transposed [c1][c2]; 128 x
-// 128 a workgroup.  One plane rounds W, two hold it exactly.
-template <int NP, bool TURN, int GPB>
-__global__ __launch_bounds__(256) void dense_kernel(Weight w, bf16_t* out, int64_t plane) {
-  __shared__ __attribute__((aligned(1024))) char lds[128 * 256];
+// W as NP bf16 planes [c2][c1]; 16 x 128 a wave.  One plane rounds W, two hold it
+// exactly.
+template <int NP, int GPB>
+__global__ __launch_bounds__(256) void dense_kernel(Weight w, bf16_t* out, int64_t plane, int waves) {
+  __shared__ __attribute__((aligned(1024))) char lds[4][4096];
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4, wv = threadIdx.x >> 6;
-  const int b = blockIdx.x % w.kt, o0 = blockIdx.x / w.kt * 128;
-  float v[2][4][8];
+  const int id = blockIdx.x * 4 + wv, cb = id / w.kt, b = id - cb * w.kt;
+  if (id >= waves) return;   // waves work apart
+  char* mine = lds[wv];
+  const uint4 q = w.codes[(int64_t)id * 64 + lane];
+  const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+  float v[4][8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int cb = o0 / 16 + wv * 2 + i;
-    const bool in = cb * 16 < w.c2;
-    const uint4 q = in ? w.codes[((int64_t)cb * w.kt + b) * 64 + lane] : zero4();
-    const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t p = w.params[((int64_t)id * GPB + s * GPB / 4) * 16 + j];
+    const float sc = scale_of(p), zo = zero_of(p);
+    const uint4 x = widen(words[s]);
+    const uint32_t h[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint32_t p = in ? w.params[((int64_t)cb * w.kt * GPB + b * GPB + s * GPB / 4) * 16 + j] : 0;
-      const float sc = scale_of(p), zo = zero_of(p);
-      const uint4 x = widen(words[s]);
-      const uint32_t h[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[i][s][2 * e] = sc * (__uint_as_float(h[e] << 16) - zo);
-        v[i][s][2 * e + 1] = sc * (__uint_as_float(h[e] & 0xffff0000u) - zo);
-      }
+    for (int e = 0; e < 4; ++e) {
+      v[s][2 * e] = sc * (__uint_as_float(h[e] << 16) - zo);
+      v[s][2 * e + 1] = sc * (__uint_as_float(h[e] & 0xffff0000u) - zo);
     }
   }
 #pragma unroll
   for (int t = 0; t < NP; ++t) {
-    if (t) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int s = 0; s < 4; ++s) {
+      uint32_t h[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[e] = pack_bf16x2(v[i][s][2 * e], v[i][s][2 * e + 1]);
-          v[i][s][2 * e] -= __uint_as_float(h[e] << 16);
-          v[i][s][2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-        }
-        *reinterpret_cast<uint4*>(lds + tile_at((wv * 2 + i) * 16 + j, 4 * s + g, 16)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
+      for (int e = 0; e < 4; ++e) {
+        h[e] = pack_bf16x2(v[s][2 * e], v[s][2 * e + 1]);
+        v[s][2 * e] -= __uint_as_float(h[e] << 16);
+        v[s][2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
       }
-    __syncthreads();
-    const int rows = min(128, w.c2 - o0), cols = min(128, w.c1 - b * 128);
-    if constexpr (TURN)
-      tile_transposed<128, 128, 256>(lds, out + t * plane + (int64_t)b * 128 * w.c2 + o0, w.c2, rows, cols);
-    else tile_rows<128, 128, 256>(lds, out + t * plane + (int64_t)o0 * w.c1 + b * 128, w.c1, rows, cols);
+      // row j, chunk 4 s + g at chunk ^ j: 16 rows of a chunk in 16 places
+      *reinterpret_cast<uint4*>(mine + j * 256 + (((4 * s + g) ^ j) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // four rows of whole lines
+      const int row = 4 * i + (lane >> 4), k = b * 128 + j * 8;
+      const uint4 x = *reinterpret_cast<const uint4*>(mine + row * 256 + ((j ^ row) << 4));
+      if (cb * 16 + row < w.c2 && k < w.c1)
+        *reinterpret_cast<uint4*>(out + t * plane + (int64_t)(cb * 16 + row) * w.c1 + k) = x;
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -543,7 +541,7 @@ struct Plan {
 Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
   Plan q{};
   const bool wide = dtype == DYRA_F32;
-  const Job j = job({nullptr, 0, 0, (int32_t)n}, {nullptr, 0, 0, (int32_t)out}, in, wide ? 5 : 1, 0);
+  const Job j = job({nullptr, 0, 0, (int32_t)n}, {nullptr, 0, 0, (int32_t)out}, in, in, wide ? 5 : 1, 0);
   q.tile = shape_of(j);
   if (!backward) {
     // many rows: the weight is written out and read again, two or three launches.
@@ -591,32 +589,31 @@ void launch_rows(const RowsArgs& a, int ob, int group, hipStream_t st) {
   }
 }
 
-template <int NP, bool TURN>
+template <int NP>
 void launch_dense(const Weight& w, int group, bf16_t* out, hipStream_t st) {
-  const dim3 grid((unsigned)(cdiv(w.c2, 128) * w.kt)), nt(256);
-  const int64_t plane = (int64_t)w.c1 * w.c2;
-  if (group == 128) hipLaunchKernelGGL((dense_kernel<NP, TURN, 1>), grid, nt, 0, st, w, out, plane);
-  else if (group == 64) hipLaunchKernelGGL((dense_kernel<NP, TURN, 2>), grid, nt, 0, st, w, out, plane);
-  else hipLaunchKernelGGL((dense_kernel<NP, TURN, 4>), grid, nt, 0, st, w, out, plane);
+  const int64_t waves = cdiv(w.c2, 16) * w.kt, plane = (int64_t)w.c1 * w.c2;
+  const dim3 grid((unsigned)cdiv(waves, 4)), nt(256);
+  if (group == 128) hipLaunchKernelGGL((dense_kernel<NP, 1>), grid, nt, 0, st, w, out, plane, (int)waves);
+  else if (group == 64) hipLaunchKernelGGL((dense_kernel<NP, 2>), grid, nt, 0, st, w, out, plane, (int)waves);
+  else hipLaunchKernelGGL((dense_kernel<NP, 4>), grid, nt, 0, st, w, out, plane, (int)waves);
 }
 
-// out [n][cout] = in [n][cin] times the weight (TURN: its transpose was the forward's)
-template <typename T, bool TURN>
+// out [n][cout] = in [n][cin] times the weight, transposed or (BACK) as it is
+template <typename T, bool BACK>
 int many(const dyra_q4& w, const T* in, int64_t ldi, const T* bias, T* out, int64_t ldo, int64_t n, const Plan& q,
          char* ws, hipStream_t st) {
   constexpr bool wide = sizeof(T) == 4;
-  const int64_t cin = TURN ? w.c2 : w.c1, cout = TURN ? w.c1 : w.c2;
+  const int64_t cin = BACK ? w.c2 : w.c1, cout = BACK ? w.c1 : w.c2;
   bf16_t* dense = reinterpret_cast<bf16_t*>(ws + q.dense);
-  launch_dense<wide ? 2 : 1, TURN>(weight_of(w), w.group, dense, st);
+  launch_dense<wide ? 2 : 1>(weight_of(w), w.group, dense, st);
   Operand a{in, 2 * ldi, 0, (int32_t)n};
   if constexpr (wide) {
-    bf16_t* planes = reinterpret_cast<bf16_t*>(ws + q.planes);
-    launch_planes<T>(in, ldi, n, cin, planes, nullptr, 0, n * cin, 0, nullptr, nullptr, st);
-    a = {planes, 2 * cin, 2 * n * cin, (int32_t)n};
+    launch_planes<T>(planes(in, ldi, n, cin, ws + q.planes, n * cin), Planes<T>{}, st);
+    a = {ws + q.planes, 2 * cin, 2 * n * cin, (int32_t)n};
   }
-  Job j = job(a, {dense, 2 * cin, 2 * cin * cout, (int32_t)cout}, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
+  Job j = job(a, {dense, 2 * w.c1, 2 * w.c1 * w.c2, (int32_t)cout}, cin, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
   j.part = reinterpret_cast<float4*>(ws + q.part);
-  launch_as(q.tile, j, Store<T>{out, ldo, (int32_t)cout, bias, nullptr, nullptr}, st);
+  launch_as<false, BACK>(q.tile, j, Store<T>{out, ldo, (int32_t)cout, bias, nullptr, nullptr}, st);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 
@@ -683,7 +680,7 @@ extern "C" int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* s
   if (rc) return rc;
   if (misaligned(w->packed, 15) || misaligned(out, 15)) return DYRA_EINVAL;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == DYRA_BF16) launch_dense<1, false>(weight_of(*w), w->group, reinterpret_cast<bf16_t*>(out), st);
+  if (dtype == DYRA_BF16) launch_dense<1>(weight_of(*w), w->group, reinterpret_cast<bf16_t*>(out), st);
   else
     hipLaunchKernelGGL(dense_f32_kernel, dim3((unsigned)cdiv(w->c2 * (w->c1 / 8), 256)), dim3(256), 0, st,
                        weight_of(*w), reinterpret_cast<float*>(out), 128 / w->group);

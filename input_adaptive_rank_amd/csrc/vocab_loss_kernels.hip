@@ -167,12 +167,12 @@ __global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ 
   if (tid == 0) *live = base;
 }
 
-// d of a tile, in NP bf16 planes, row by row and transposed.  Columns past the
-// piece's and rows past the last are zero up to the padded sizes.
+// d of a tile, in NP bf16 planes; columns past the piece's are zero up to the
+// padded width.
 template <int NP>
 struct Gradient {
-  bf16_t *d, *dt;               // [NP][rows][ldd], [NP][cols][ldt]; null: not wanted
-  int64_t ldd, ldt, plane, plane_t;
+  bf16_t* d;                    // [NP][rows][ldd]
+  int64_t ldd, plane;
   const float *lse, *dloss;
   const int32_t *targets, *map;
   float scale;
@@ -196,10 +196,13 @@ struct Gradient {
         v[i / 16][i % 16] -= has && i == ((at >> 5) * 16 + (at >> 3 & 3) * 4 + (at & 3)) ? 1.f : 0.f;
     }
     const int edge = in ? cols - col0 - 4 * g : 0;   // columns from here on are none
+    if (__all(edge >= C::WN)) {
 #pragma unroll
-    for (int i = 0; i < 16 * C::FN; ++i) {
-      const int c = i / 16 * 32 + (i % 16 / 4) * 8 + i % 4;
-      v[i / 16][i % 16] = edge >= C::WN || c < edge ? v[i / 16][i % 16] * w : 0.f;
+      for (int i = 0; i < 16 * C::FN; ++i) v[i / 16][i % 16] *= w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16 * C::FN; ++i)
+        v[i / 16][i % 16] = i / 16 * 32 + (i % 16 / 4) * 8 + i % 4 < edge ? v[i / 16][i % 16] * w : 0.f;
     }
   }
 
@@ -213,74 +216,38 @@ struct Gradient {
     return h;
   }
 
-  template <class C>
-  __device__ __forceinline__ void tile(Acc<C>& acc, char* lds, int m0, int n0, int rows, int wm, int wn) const {
-    static_assert(C::BM * C::BN * 2 <= C::LDS && C::BN % 128 == 0, "the tile fits the ring");
-    constexpr int CPR = C::BN / 8;
-    const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5;
-#pragma unroll
-    for (int fm = 0; fm < C::FM; ++fm) {
-      values<C>(acc[fm], m0 + wm * C::WM + fm * 32 + l, n0 + wn * C::WN, rows);
-      __builtin_amdgcn_sched_barrier(0);   // one block after the other: registers
-    }
-    const int valid = min(C::BM, rows - m0), padded = min(C::BM, ((rows + 63) & ~63) - m0);
-    const int wide = min(C::BN, (int)ldd - n0);
-#pragma unroll
-    for (int t = 0; t < NP; ++t) {
-      if (t) __syncthreads();   // the plane before has been copied out
-#pragma unroll
-      for (int fm = 0; fm < C::FM; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < C::FN; ++fn)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int row = wm * C::WM + fm * 32 + l, col = wn * C::WN + fn * 32 + 8 * q + 4 * g;
-            const uint32_t x = peel(acc[fm][fn], 4 * q), y = peel(acc[fm][fn], 4 * q + 2);
-            *reinterpret_cast<uint2*>(lds + tile_at(row, col / 8, CPR) + 8 * g) = make_uint2(x, y);
-          }
-      __syncthreads();
-      if (d) tile_rows<C::BM, C::BN, C::NT>(lds, d + t * plane + (int64_t)m0 * ldd + n0, ldd, valid, wide);
-      if (dt) tile_transposed<C::BM, C::BN, C::NT>(lds, dt + t * plane_t + (int64_t)n0 * ldt + m0, ldt, padded, wide);
-    }
-  }
-
-  // one wave's 32 x 64 results
+  // 32 rows of one line
   template <class C>
   __device__ __forceinline__ void block(f32x16 (&v)[C::FN], char* lds, int row0, int col0, int rows) const {
     const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5;
     values<C>(v, row0 + l, col0, rows);
-    auto at = [](int row, int chunk) { return row * 128 + (((chunk ^ row ^ row >> 3) & 7) << 4); };
-    const int padded = (rows + 63) & ~63, wide = (int)ldd;
 #pragma unroll
     for (int t = 0; t < NP; ++t) {
-      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int fn = 0; fn < C::FN; ++fn)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t x = peel(v[fn], 4 * q), y = peel(v[fn], 4 * q + 2);
-          *reinterpret_cast<uint2*>(lds + at(l, fn * 4 + q) + 8 * g) = make_uint2(x, y);
+          *reinterpret_cast<uint2*>(lds + lds_off(l, fn * 4 + q) + 8 * g) = make_uint2(x, y);
         }
       __builtin_amdgcn_wave_barrier();
-      if (d) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 3), k = lane & 7, col = col0 + k * 8;
-          if (row0 + rr < rows && col < wide)
-            *reinterpret_cast<uint4*>(d + t * plane + (row0 + rr) * ldd + col) =
-                *reinterpret_cast<const uint4*>(lds + at(rr, k));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 3), k = lane & 7, col = col0 + k * 8;
+        const uint4 x = *reinterpret_cast<const uint4*>(lds + lds_off(rr, k));
+        if (row0 + rr < rows && col < ldd) *reinterpret_cast<uint4*>(d + t * plane + (row0 + rr) * ldd + col) = x;
       }
-      const int r0 = (lane & 3) * 8, k = lane >> 2;   // 8 x 8 elements a lane of the first half
-      if (dt && k < 8 && row0 + r0 < padded && col0 + k * 8 < wide) {
-        uint4 in[8], out[8];
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+
+  template <class C>
+  __device__ __forceinline__ void tile(Acc<C>& acc, char* lds, int m0, int n0, int rows, int wm, int wn) const {
+    char* mine = lds + (wm * C::NWN + wn) * 4096;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) in[e] = *reinterpret_cast<const uint4*>(lds + at(r0 + e, k));
-        transpose8x8_b16(in, out);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(dt + t * plane_t + (col0 + k * 8 + e) * ldt + row0 + r0) = out[e];
-      }
+    for (int fm = 0; fm < C::FM; ++fm) {
+      block<C>(acc[fm], mine, m0 + wm * C::WM + fm * 32, n0 + wn * C::WN, rows);
+      __builtin_amdgcn_sched_barrier(0);   // one block after the other: registers
     }
   }
 };
@@ -300,10 +267,10 @@ Operand rows_of(int64_t rows) { return {nullptr, 0, 0, (int32_t)rows}; }
 
 // Sizes of a call.
 struct Plan {
-  int64_t np, nrow;                     // planes; rows padded for the transposed forms
+  int64_t np;                           // planes of an operand
   int64_t piece;                        // columns of the vocabulary at a time
   Shape logits, dh, dw;
-  size_t part, mine, live, map, hp, ht, wp, wt, d, dt, acc, parts, total;
+  size_t part, mine, live, map, hp, wp, d, acc, parts, total;
 };
 
 const int32_t* const SOME = reinterpret_cast<const int32_t*>(4);   // "found on the device", for sizes alone
@@ -313,16 +280,15 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
   const bool wide = dtype == DYRA_F32;
   q.np = wide ? 3 : 1;
   const int terms = wide ? 6 : 1;
-  q.nrow = up(n, 64);
-  // d of a piece, both ways, is at most 2^26 elements a plane pair (256 MB in
-  // bf16, the last-level cache); planes of fp32 weights at most 2^28
-  int64_t most = (int64_t)1 << 24;
-  if (backward) most = std::min<int64_t>(most, ((int64_t)1 << 26) / q.nrow);
+  // d of a piece is at most 2^27 elements a plane (256 MB in bf16, the last-level
+  // cache), planes of fp32 weights at most 2^28
+  int64_t most = (int64_t)1 << 20;
+  if (backward) most = std::min<int64_t>(most, ((int64_t)1 << 27) / n);
   if (wide) most = std::min<int64_t>(most, ((int64_t)1 << 28) / (3 * C));
   most = std::max<int64_t>(256, most & ~(int64_t)255);
   q.piece = std::min(up(V, 64), up(cdiv(V, cdiv(V, most)), 256));
   const int32_t* live = backward ? SOME : nullptr;
-  const Job logits = job(rows_of(n), rows_of(q.piece), C, terms, 0, live);
+  const Job logits = job(rows_of(n), rows_of(q.piece), C, C, terms, 0, live);
   // a 256 x 256 tile's d in three planes leaves the registers
   q.logits = shape_of(logits, !(wide && backward));
   int64_t parts = part_bytes(q.logits, logits);
@@ -340,20 +306,17 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
   } else {
     q.live = take(4);
     q.map = take(4 * n);
+    q.d = take(2 * q.np * n * q.piece);
     if (need_dh) {
-      const Job j = job(rows_of(n), rows_of(C), q.piece, terms, 0, live);
+      const Job j = job(rows_of(n), rows_of(C), q.piece, q.piece, terms, 0, live);
       q.dh = shape_of(j);
       parts = std::max(parts, part_bytes(q.dh, j));
-      q.wt = take(2 * q.np * C * q.piece);
-      q.d = take(2 * q.np * n * q.piece);
       if (q.piece < V) q.acc = take(4 * n * C);
     }
     if (need_dw) {
-      const Job j = job(rows_of(q.piece), rows_of(C), q.nrow, terms, 0, live, true);
+      const Job j = job(rows_of(q.piece), rows_of(C), n, n, terms, 0, live, true);
       q.dw = shape_of(j);
       parts = std::max(parts, part_bytes(q.dw, j));
-      q.ht = take(2 * q.np * C * q.nrow);
-      q.dt = take(2 * q.np * q.piece * q.nrow);
     }
   }
   q.parts = take(parts);
@@ -375,8 +338,8 @@ template <typename T>
 Job logits_job(Operand h, const T* W, int64_t v0, int64_t cols, int64_t C, const Plan& q, char* ws,
                const int32_t* live) {
   Job j;
-  if constexpr (sizeof(T) == 2) j = job(h, {W + v0 * C, 2 * C, 0, (int32_t)cols}, C, 1, TERMS_1, live);
-  else j = job(h, {ws + q.wp, 2 * C, 2 * q.piece * C, (int32_t)cols}, C, 6, TERMS_33, live);
+  if constexpr (sizeof(T) == 2) j = job(h, {W + v0 * C, 2 * C, 0, (int32_t)cols}, C, C, 1, TERMS_1, live);
+  else j = job(h, {ws + q.wp, 2 * C, 2 * q.piece * C, (int32_t)cols}, C, C, 6, TERMS_33, live);
   j.part = reinterpret_cast<float4*>(ws + q.parts);
   return j;
 }
@@ -388,16 +351,13 @@ int forward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, fl
   float2* part = reinterpret_cast<float2*>(ws + q.part);
   float* mine = reinterpret_cast<float*>(ws + q.mine);
   Operand h{H, 2 * ldh, 0, (int32_t)n};
-  if constexpr (wide) {
-    h = {ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
-    launch_planes<T>(H, ldh, n, C, reinterpret_cast<bf16_t*>(ws + q.hp), nullptr, 0, n * C, 0, nullptr, nullptr, st);
-  }
+  if constexpr (wide) h = {ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
     const int64_t cols = std::min(q.piece, V - v0);
     if constexpr (wide)
-      launch_planes<T>(W + v0 * C, C, cols, C, reinterpret_cast<bf16_t*>(ws + q.wp), nullptr, 0, q.piece * C, 0,
-                       nullptr, nullptr, st);
-    launch_as(q.logits, logits_job<T>(h, W, v0, cols, C, q, ws, nullptr),
+      launch_planes<T>(planes(H, ldh, v0 ? 0 : n, C, ws + q.hp, n * C),
+                       planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C), st);
+    launch_as<false, false>(q.logits, logits_job<T>(h, W, v0, cols, C, q, ws, nullptr),
               RowStats{part, mine, targets, scale, (int32_t)cols, (int32_t)v0}, st);
   }
   hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)cdiv(n, 32)), dim3(1024), 0, st, part, mine, targets, loss, lse,
@@ -411,36 +371,35 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
                   hipStream_t st) {
   constexpr int NP = planes_of<T>(), terms = NP == 3 ? 6 : 1;
   constexpr uint32_t pairs = NP == 3 ? TERMS_33 : TERMS_1;
-  auto at = [&](size_t o) { return reinterpret_cast<bf16_t*>(ws + o); };
   int32_t *live = reinterpret_cast<int32_t*>(ws + q.live), *map = reinterpret_cast<int32_t*>(ws + q.map);
   float* acc = reinterpret_cast<float*>(ws + q.acc);
-  bf16_t *wp = NP == 3 ? at(q.wp) : nullptr, *wt = dH ? at(q.wt) : nullptr, *ht = dW ? at(q.ht) : nullptr;
+  bf16_t* d = reinterpret_cast<bf16_t*>(ws + q.d);
   hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets, (int)n,
                      (int)V, live, map, dH, lddh, (int)C);
-  launch_planes<T>(H, ldh, n, C, at(q.hp), ht, ht ? q.nrow : 0, n * C, C * q.nrow, map, live, st);
-  const Operand h{at(q.hp), 2 * C, 2 * n * C, (int32_t)n};
+  const Operand h{ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
     const int64_t cols = std::min(q.piece, V - v0), ldd = up(cols, 64);
-    if (wp || wt)
-      launch_planes<T>(W + v0 * C, C, cols, C, wp, wt, wt ? ldd : 0, q.piece * C, C * q.piece, nullptr, nullptr, st);
-    const Gradient<NP> e{dH ? at(q.d) : nullptr, dW ? at(q.dt) : nullptr, ldd,     q.nrow, n * q.piece,
-                         q.piece * q.nrow,       lse,                     dloss,   targets, map,
-                         scale,                  (int32_t)cols,           (int32_t)v0};
-    launch_as<NP == 1>(q.logits, logits_job<T>(h, W, v0, cols, C, q, ws, live), e, st);
+    const Planes<T> hp = planes(H, ldh, v0 ? 0 : n, C, ws + q.hp, n * C, map, live);
+    launch_planes<T>(hp, NP == 3 ? planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C) : Planes<T>{}, st);
+    const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, scale, (int32_t)cols, (int32_t)v0};
+    const Job lj = logits_job<T>(h, W, v0, cols, C, q, ws, live);
+    launch_as<false, false, NP == 1>(q.logits, lj, e, st);
     if (dH) {
-      Job j = job({at(q.d), 2 * ldd, 2 * n * q.piece, (int32_t)n}, {wt, 2 * ldd, 2 * C * q.piece, (int32_t)C}, ldd, terms,
-                  pairs, live);
-      j.part = reinterpret_cast<float4*>(ws + q.parts);
+      Operand w = lj.b;   // turned: its rows are the reduction
+      w.rows = (int32_t)C;
+      Job j = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)n}, w, cols, ldd, terms, pairs, live);
+      j.part = lj.part;
       // pieces add up in fp32; the last rounds and puts the rows in their places
       const float* prior = v0 ? acc : nullptr;
-      if (v0 + cols < V) launch_as(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr}, st);
-      else launch_as(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map}, st);
+      if (v0 + cols < V) launch_as<false, true>(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr}, st);
+      else launch_as<false, true>(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map}, st);
     }
     if (dW) {
-      Job j = job({at(q.dt), 2 * q.nrow, 2 * q.piece * q.nrow, (int32_t)cols},
-                  {ht, 2 * q.nrow, 2 * C * q.nrow, (int32_t)C}, q.nrow, terms, pairs, live, true);
-      j.part = reinterpret_cast<float4*>(ws + q.parts);
-      launch_as(q.dw, j, Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr}, st);
+      Operand hr = h;   // both turned
+      hr.rows = (int32_t)C;
+      Job j = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)cols}, hr, n, n, terms, pairs, live, true);
+      j.part = lj.part;
+      launch_as<true, true>(q.dw, j, Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr}, st);
     }
   }
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
