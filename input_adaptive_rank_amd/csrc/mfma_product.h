@@ -59,10 +59,11 @@ struct Job {
   float4* part;        // partial tiles, if may_split (part_bytes)
 };
 
-// STEP: tenths of a microsecond that a k-step takes with the card full.
-template <int BM_, int BN_, int NWM_, int NWN_, int NS_, int WGS_, int STEP_>
+// A k-step takes ALONE hundredths of a microsecond with one workgroup on the card,
+// ALONE + SHARED with all its places taken (the clock falls with the load).
+template <int BM_, int BN_, int NWM_, int NWN_, int NS_, int WGS_, int ALONE_, int SHARED_>
 struct Tile {
-  static constexpr int STEP = STEP_;
+  static constexpr int ALONE = ALONE_, SHARED = SHARED_;
   static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_, NS = NS_;
   static constexpr int NW = NWM * NWN, NT = NW * 64;
   static constexpr int WM = BM / NWM, WN = BN / NWN, FM = WM / 32, FN = WN / 32;
@@ -79,11 +80,11 @@ struct Tile {
 
 // 256 x 256: 128 flop a byte loaded, one workgroup a CU (128 KB of LDS); 1.27
 // PFLOP/s in whole rounds
-typedef Tile<256, 256, 2, 4, 2, 1, 17> Big;
+typedef Tile<256, 256, 2, 4, 2, 1, 100, 75> Big;
 // 128 x 128: four times the tiles, two workgroups a CU
-typedef Tile<128, 128, 2, 2, 2, 2, 11> Small;
+typedef Tile<128, 128, 2, 2, 2, 2, 45, 55> Small;
 // 64 x 128: a few rows against a matrix that is read once; a deeper ring
-typedef Tile<64, 128, 2, 2, 3, 2, 6> Thin;
+typedef Tile<64, 128, 2, 2, 3, 2, 30, 33> Thin;
 
 // How a product's tiles are laid over the workgroups.  The card holds SLOTS of
 // them at once: whole rounds of tiles are computed by one workgroup each.  The
@@ -95,7 +96,7 @@ struct Layout {
   int rows, tiles_m, tiles_n, kbytes, krows, nk;
   int whole, tail, split, per;   // tiles computed whole, tiles split, parts of one, steps of a part
   int count;                     // workgroups
-  double cost;                   // tenths of a microsecond, estimated
+  double cost;                   // microseconds, estimated
 };
 
 template <class C>
@@ -117,12 +118,14 @@ __host__ __device__ inline Layout layout(const Job& j, int live) {
   y.tiles_m = (y.rows + C::BM - 1) / C::BM;
   y.tiles_n = (j.b.rows + C::BN - 1) / C::BN;
   const int tiles = y.tiles_m * y.tiles_n, steps = j.terms * y.nk, rest = tiles % C::SLOTS;
-  int split = 1, least = rest ? steps * C::STEP : 0;
+  // hundredths of a microsecond of a step of n workgroups
+  auto step = [](int n) { return n / C::SLOTS * (C::ALONE + C::SHARED) +
+                                 (n % C::SLOTS ? C::ALONE + C::SHARED * (n % C::SLOTS) / C::SLOTS : 0); };
+  int split = 1, least = steps * step(rest);
   if (j.may_split && rest) {
     for (int s = 2; s <= 16 && s * 4 <= steps && rest * s <= 2 * C::SLOTS; ++s) {   // at least four steps a part
-      // the rounds of the parts, their way through memory at 5 TB/s, a launch
-      const int cost = (rest * s + C::SLOTS - 1) / C::SLOTS * ((steps + s - 1) / s) * C::STEP +
-                       rest * s * (C::BM * C::BN / 1024) / 61 + 60;
+      // the parts, their way through memory at 5 TB/s, a launch
+      const int cost = (steps + s - 1) / s * step(rest * s) + rest * s * (C::BM * C::BN / 1024) / 6 + 600;
       if (cost < least) {
         least = cost;
         split = s;
@@ -134,7 +137,7 @@ __host__ __device__ inline Layout layout(const Job& j, int live) {
   y.tail = split > 1 ? rest : 0;
   y.whole = tiles - y.tail;
   y.count = y.whole + y.tail * y.split;
-  y.cost = (double)(tiles / C::SLOTS) * steps * C::STEP + least;
+  y.cost = 0.01 * ((double)(tiles / C::SLOTS) * steps * (C::ALONE + C::SHARED) + least);
   return y;
 }
 
@@ -570,7 +573,7 @@ inline Shape shape_of(const Job& j, bool may_be_big = true) {
 
 // Estimated microseconds of a product.
 inline double cost(Shape s, const Job& j) {
-  return 0.1 * (s == BIG ? layout<Big>(j, -1).cost : s == SMALL ? layout<Small>(j, -1).cost : layout<Thin>(j, -1).cost);
+  return s == BIG ? layout<Big>(j, -1).cost : s == SMALL ? layout<Small>(j, -1).cost : layout<Thin>(j, -1).cost;
 }
 
 // Bytes of partial tiles that a product may leave.

@@ -312,15 +312,12 @@ __global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
 // the weight written out
 // ---------------------------------------------------------------------------
 
-// W as NP bf16 planes [c2][c1]; 16 x 128 a wave.  One plane rounds W, two hold it
-// exactly.
+// 16 x 128 of W as NP bf16 planes [c2][c1], a wave's work.  One plane rounds W, two
+// hold it exactly.
 template <int NP, int GPB>
-__global__ __launch_bounds__(256) void dense_kernel(Weight w, bf16_t* out, int64_t plane, int waves) {
-  __shared__ __attribute__((aligned(1024))) char lds[4][4096];
-  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4, wv = threadIdx.x >> 6;
-  const int id = blockIdx.x * 4 + wv, cb = id / w.kt, b = id - cb * w.kt;
-  if (id >= waves) return;   // waves work apart
-  char* mine = lds[wv];
+__device__ __forceinline__ void write_dense(const Weight& w, bf16_t* out, int64_t plane, int id, char* mine) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int cb = id / w.kt, b = id - cb * w.kt;
   const uint4 q = w.codes[(int64_t)id * 64 + lane];
   const uint32_t words[4] = {q.x, q.y, q.z, q.w};
   float v[4][8];
@@ -360,6 +357,24 @@ __global__ __launch_bounds__(256) void dense_kernel(Weight w, bf16_t* out, int64
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+template <int GPB>
+__global__ __launch_bounds__(256) void dense_kernel(Weight w, bf16_t* out, int waves) {
+  __shared__ __attribute__((aligned(1024))) char lds[4][4096];
+  const int id = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id < waves) write_dense<1, GPB>(w, out, 0, id, lds[threadIdx.x >> 6]);
+}
+
+// The operands of an fp32 product: the weight's two planes in the first
+// workgroups, the rows' three in the others.
+template <int GPB>
+__global__ __launch_bounds__(256) void operands_kernel(Weight w, bf16_t* out, int64_t plane, int waves, int first,
+                                                       Planes<float> x) {
+  __shared__ __attribute__((aligned(1024))) char lds[4][4096];
+  if ((int)blockIdx.x >= first) return make_planes(x, (int64_t)(blockIdx.x - first) * 256 + threadIdx.x);
+  const int id = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id < waves) write_dense<2, GPB>(w, out, plane, id, lds[threadIdx.x >> 6]);
 }
 
 // W in fp32, exact; eight columns a thread.
@@ -589,13 +604,21 @@ void launch_rows(const RowsArgs& a, int ob, int group, hipStream_t st) {
   }
 }
 
-template <int NP>
 void launch_dense(const Weight& w, int group, bf16_t* out, hipStream_t st) {
-  const int64_t waves = cdiv(w.c2, 16) * w.kt, plane = (int64_t)w.c1 * w.c2;
+  const int64_t waves = cdiv(w.c2, 16) * w.kt;
   const dim3 grid((unsigned)cdiv(waves, 4)), nt(256);
-  if (group == 128) hipLaunchKernelGGL((dense_kernel<NP, 1>), grid, nt, 0, st, w, out, plane, (int)waves);
-  else if (group == 64) hipLaunchKernelGGL((dense_kernel<NP, 2>), grid, nt, 0, st, w, out, plane, (int)waves);
-  else hipLaunchKernelGGL((dense_kernel<NP, 4>), grid, nt, 0, st, w, out, plane, (int)waves);
+  if (group == 128) hipLaunchKernelGGL((dense_kernel<1>), grid, nt, 0, st, w, out, (int)waves);
+  else if (group == 64) hipLaunchKernelGGL((dense_kernel<2>), grid, nt, 0, st, w, out, (int)waves);
+  else hipLaunchKernelGGL((dense_kernel<4>), grid, nt, 0, st, w, out, (int)waves);
+}
+
+void launch_operands(const Weight& w, int group, bf16_t* out, const Planes<float>& x, hipStream_t st) {
+  const int64_t waves = cdiv(w.c2, 16) * w.kt, plane = (int64_t)w.c1 * w.c2, first = cdiv(waves, 4);
+  const dim3 grid((unsigned)(first + cdiv((int64_t)x.rows * (x.cols / 8), 256))), nt(256);
+  if (group == 128) hipLaunchKernelGGL((operands_kernel<1>), grid, nt, 0, st, w, out, plane, (int)waves, (int)first, x);
+  else if (group == 64)
+    hipLaunchKernelGGL((operands_kernel<2>), grid, nt, 0, st, w, out, plane, (int)waves, (int)first, x);
+  else hipLaunchKernelGGL((operands_kernel<4>), grid, nt, 0, st, w, out, plane, (int)waves, (int)first, x);
 }
 
 // out [n][cout] = in [n][cin] times the weight, transposed or (BACK) as it is
@@ -605,11 +628,12 @@ int many(const dyra_q4& w, const T* in, int64_t ldi, const T* bias, T* out, int6
   constexpr bool wide = sizeof(T) == 4;
   const int64_t cin = BACK ? w.c2 : w.c1, cout = BACK ? w.c1 : w.c2;
   bf16_t* dense = reinterpret_cast<bf16_t*>(ws + q.dense);
-  launch_dense<wide ? 2 : 1>(weight_of(w), w.group, dense, st);
   Operand a{in, 2 * ldi, 0, (int32_t)n};
   if constexpr (wide) {
-    launch_planes<T>(planes(in, ldi, n, cin, ws + q.planes, n * cin), Planes<T>{}, st);
+    launch_operands(weight_of(w), w.group, dense, planes(in, ldi, n, cin, ws + q.planes, n * cin), st);
     a = {ws + q.planes, 2 * cin, 2 * n * cin, (int32_t)n};
+  } else {
+    launch_dense(weight_of(w), w.group, dense, st);
   }
   Job j = job(a, {dense, 2 * w.c1, 2 * w.c1 * w.c2, (int32_t)cout}, cin, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
   j.part = reinterpret_cast<float4*>(ws + q.part);
@@ -680,7 +704,7 @@ extern "C" int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* s
   if (rc) return rc;
   if (misaligned(w->packed, 15) || misaligned(out, 15)) return DYRA_EINVAL;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == DYRA_BF16) launch_dense<1>(weight_of(*w), w->group, reinterpret_cast<bf16_t*>(out), st);
+  if (dtype == DYRA_BF16) launch_dense(weight_of(*w), w->group, reinterpret_cast<bf16_t*>(out), st);
   else
     hipLaunchKernelGGL(dense_f32_kernel, dim3((unsigned)cdiv(w->c2 * (w->c1 / 8), 256)), dim3(256), 0, st,
                        weight_of(*w), reinterpret_cast<float*>(out), 128 / w->group);

@@ -136,8 +136,9 @@ def q4_pack(codes, scale, zero=None, group=128, stream=None) -> Q4Weight:
     return Q4Weight(c1, c2, group, packed)
 
 
-def _call(t, name, weight, width):
-    """Checks the rows of a call; type, device, rows."""
+def _call(t, name, weight, back):
+    """Checks the rows of a call against the weight; type, device, rows, the
+    stride of its rows and where they lie."""
     if not isinstance(weight, Q4Weight):
         raise ValueError("weight must be a Q4Weight (q4_pack)")
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -145,11 +146,25 @@ def _call(t, name, weight, width):
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if t.device != weight.device:
-        raise ValueError(f"{name} is on {t.device}, the weight on {weight.device}")
-    if t.shape[1] != width:
+    dev, width = weight.device, weight.c2 if back else weight.c1
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the weight on {dev}")
+    n, c = t.shape
+    if c != width:
         raise ValueError(f"{name} must have {width} columns, got {tuple(t.shape)}")
-    return dt, t.device, t.shape[0]
+    p = t.data_ptr()
+    if p & 15 or not t.is_contiguous():
+        return dt, dev, n, *_rows(t, name, n, width, t.dtype, dev)
+    return dt, dev, n, p, width
+
+
+def _result(t, out, name, n, width, stream):
+    """Where a result goes: out, or a new tensor beside t."""
+    if out is None and stream is None:
+        out = t.new_empty((n, width))
+        return out, out.data_ptr(), width
+    out = _output(out, (n, width), t.dtype, t.device, stream)
+    return out, *_rows(out, name, n, width, t.dtype, t.device)
 
 
 def _workspace(workspace, need, device, stream):
@@ -165,15 +180,15 @@ def _workspace(workspace, need, device, stream):
 
 def q4_forward(X, weight, bias=None, out=None, workspace=None, stream=None):
     """Y = X W^T + bias (asynchronous).  out: receives Y."""
-    dt, dev, n = _call(X, "X", weight, weight.c1 if isinstance(weight, Q4Weight) else 0)
+    dt, dev, n, xp, ldx = _call(X, "X", weight, False)
     c1, c2 = weight.c1, weight.c2
     handle = _on(dev, stream)
-    xp, ldx = _rows(X, "X", n, c1, X.dtype, dev)
-    bp = _flat(bias, "bias", (c2,), X.dtype, dev)
-    if bp is not None and bp & 15:
-        raise ValueError("bias must be 16-byte aligned")
-    Y = _output(out, (n, c2), X.dtype, dev, stream)
-    yp, ldy = _rows(Y, "out", n, c2, X.dtype, dev)
+    bp = None
+    if bias is not None:
+        bp = _flat(bias, "bias", (c2,), X.dtype, dev)
+        if bp & 15:
+            raise ValueError("bias must be 16-byte aligned")
+    Y, yp, ldy = _result(X, out, "out", n, c2, stream)
     if out is not None:
         _apart(out, "out", [("X", X), ("bias", bias), ("weight", weight.packed)])
     wp, wn, workspace = _workspace(workspace, q4_workspace_size(c1, c2, n, dt), dev, stream)
@@ -185,14 +200,12 @@ def q4_forward(X, weight, bias=None, out=None, workspace=None, stream=None):
 def q4_backward(dY, weight, dX=None, workspace=None, stream=None):
     """dX = dY W, the gradient of q4_forward's X (asynchronous).  dX: a tensor
     that receives it."""
-    dt, dev, n = _call(dY, "dY", weight, weight.c2 if isinstance(weight, Q4Weight) else 0)
+    dt, dev, n, gp, ldg = _call(dY, "dY", weight, True)
     c1, c2 = weight.c1, weight.c2
     handle = _on(dev, stream)
-    gp, ldg = _rows(dY, "dY", n, c2, dY.dtype, dev)
-    given = dX is not None
-    dX = _output(dX, (n, c1), dY.dtype, dev, stream)
-    op, ldo = _rows(dX, "dX", n, c1, dY.dtype, dev)
-    if given:
+    given = dX
+    dX, op, ldo = _result(dY, dX, "dX", n, c1, stream)
+    if given is not None:
         _apart(dX, "dX", [("dY", dY), ("weight", weight.packed)])
     wp, wn, workspace = _workspace(workspace, q4_workspace_size(c1, c2, n, dt, True), dev, stream)
     D._check("dyra_q4_backward",
