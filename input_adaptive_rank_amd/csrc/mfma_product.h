@@ -593,11 +593,15 @@ inline int64_t part_bytes(Shape s, const Job& j) {
 template <class C, bool TA, bool TB, class E>
 inline void launch(const Job& j, const E& e, hipStream_t st) {
   const Layout y = layout<C>(j, -1);
-  // fewer live rows or steps may leave another number of tiles to split, into 2 SLOTS parts at most
-  const int64_t grid = j.live ? (int64_t)y.tiles_m * y.tiles_n + (j.may_split ? 2 * C::SLOTS : 0) : y.count;
+  int64_t grid = y.count, tail = y.tail;
+  // fewer live rows or steps may leave other tiles to split, into 2 SLOTS parts at
+  // most; but not where one tile row is all or none, or too short to be split
+  if (j.live && j.may_split && j.terms * y.nk >= 8 && (j.live_k || y.tiles_m > 1)) {
+    grid = (int64_t)y.tiles_m * y.tiles_n + 2 * C::SLOTS;
+    tail = std::min(C::SLOTS, y.tiles_m * y.tiles_n);
+  }
   if (!grid) return;
   hipLaunchKernelGGL((product_kernel<C, TA, TB, E>), dim3((unsigned)grid), dim3(C::NT), 0, st, j, e);
-  const int64_t tail = j.live ? (j.may_split ? std::min(C::SLOTS, y.tiles_m * y.tiles_n) : 0) : y.tail;
   if (tail)
     hipLaunchKernelGGL((join_kernel<C, E>), dim3((unsigned)(tail * C::NW * C::FM)), dim3(64), 0, st, j, e);
 }

@@ -35,10 +35,13 @@ struct Weight {
 __device__ __forceinline__ float scale_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 __device__ __forceinline__ float zero_of(uint32_t p) { return __uint_as_float(p << 16); }   // 128 + zero
 
-// 128 + code of a word's eight columns, as bf16.
+// 128 + code of a word's eight columns, as bf16.  The constants are held in
+// registers, where one v_and_or_b32 can take them both.
 __device__ __forceinline__ uint4 widen(uint32_t w) {
-  return make_uint4((w & 0x000f000fu) | 0x43004300u, (w >> 4 & 0x000f000fu) | 0x43004300u,
-                    (w >> 8 & 0x000f000fu) | 0x43004300u, (w >> 12 & 0x000f000fu) | 0x43004300u);
+  uint32_t mask = 0x000f000fu, bias = 0x43004300u;
+  asm("" : "+v"(mask));
+  asm("" : "+s"(bias));
+  return make_uint4((w & mask) | bias, (w >> 4 & mask) | bias, (w >> 8 & mask) | bias, (w >> 12 & mask) | bias);
 }
 
 // code - zero of a word's eight columns, as bf16 (whole numbers below 16: exact).
@@ -202,22 +205,29 @@ __global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
   auto load_x = [&](int b, auto half) __attribute__((always_inline)) {
     constexpr int H = decltype(half)::value;
     const int at = b * 256 + H * 128;
-    const bool all = b + 1 < kt;
-    static_for<0, 2 * RT>([&](auto d) __attribute__((always_inline)) {
-      constexpr int D = decltype(d)::value;
-      const int ch = ((lane & 7) ^ ((8 * D + row8) >> 1 & 7)) << 4;
-      dma16k<H * XH + D * 1024>(rx, all || at + ch < end ? vx[D] : OUT, at, base);
-    });
+    if (b + 1 < kt) {
+      static_for<0, 2 * RT>([&](auto d) __attribute__((always_inline)) {
+        constexpr int D = decltype(d)::value;
+        dma16k<H * XH + D * 1024>(rx, vx[D], at, base);
+      });
+    } else {
+      static_for<0, 2 * RT>([&](auto d) __attribute__((always_inline)) {
+        constexpr int D = decltype(d)::value;
+        const int ch = ((lane & 7) ^ ((8 * D + row8) >> 1 & 7)) << 4;
+        dma16k<H * XH + D * 1024>(rx, at + ch < end ? vx[D] : OUT, at, base);
+      });
+    }
   };
   auto load_w = [&](int b) __attribute__((always_inline)) {
-    const bool in = b < kt;
+    const int vc = b < kt ? lane * 16 : OUT, v = b < kt ? vp : OUT;
     static_for<0, OB>([&](auto o) __attribute__((always_inline)) {
       constexpr int O = decltype(o)::value;
-      dma16k<CODES + O * 1024>(rc, in && O < blocks ? lane * 16 : OUT, (O * kt + b) * 1024, base);
+      // past the last block of W: nothing that would be stored
+      dma16k<CODES + O * 1024>(rc, vc, (min(O, blocks - 1) * kt + b) * 1024, base);
     });
     static_for<0, GPB>([&](auto i) __attribute__((always_inline)) {
       constexpr int I = decltype(i)::value;
-      dma4(rp, in ? vp : OUT, (b * GPB + I) * 64, base + PARAMS + I * 256);
+      dma4(rp, v, (b * GPB + I) * 64, base + PARAMS + I * 256);
     });
   };
   f32x4 sum[OB][RT], acc[OB][RT], all[RT];
