@@ -569,10 +569,10 @@ int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* stream);
  *   Y: device [n][c2], rows ldy apart; overlaps no operand.  Strides are
  *   multiples of 8 (bf16) or 4 (fp32), at most 2^20.  n: 0 .. 2^24, n c1 and n
  *   c2 < 2^33.
- * Up to 64 rows need no workspace (0 bytes; the pointer may be NULL) and
- * multiply the codes exactly; more rows read W rounded to bf16 (bf16) or
- * exactly (fp32) from the workspace.  Sums are fp32; fp32 operands enter as
- * three bf16 terms (2^-24).  An infinity in X may give NaN where the formula
+ * A few rows (up to some hundreds, by the widths) need no workspace (0 bytes; the
+ * pointer may be NULL) and multiply the codes exactly; more rows read W rounded
+ * to bf16 (bf16) or exactly (fp32) from the workspace.  Sums are fp32; fp32
+ * operands enter as three bf16 terms (2^-24).  An infinity in X may give NaN where the formula
  * has an infinity.  Sums have a fixed order: the same call gives the same bits.
  * Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
  */

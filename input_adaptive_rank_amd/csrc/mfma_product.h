@@ -426,7 +426,7 @@ __global__ __launch_bounds__(64) void join_kernel(Job j, E e) {
 // epilogue: the tile to memory
 // ---------------------------------------------------------------------------
 
-// out[row][col] (rows ld elements apart) = acc + bias[col] + prior[row][col].
+// out[row][col] (rows ld elements apart) = (acc + prior[row][col]) * factor + bias[col].
 // 32 rows at a time go through LDS, so that every store covers whole 128-byte
 // lines.  map: the result's row is out's row map[row].
 template <typename T>
@@ -437,25 +437,32 @@ struct Store {
   const T* bias;          // or null
   const float* prior;     // fp32 [rows][cols], or null
   const int32_t* map;     // or null
+  const float* weight;    // of the factor, or null: 1
+  float scale;
 
   template <class C>
   __device__ __forceinline__ void block(const f32x16 (&v)[C::FN], char* lds, int row0, int col0, int rows) const {
     constexpr int E = 16 / sizeof(T), CPR = C::WN / E;   // elements a chunk, chunks a staged row
     const int lane = threadIdx.x & 63, l = lane & 31, g = lane >> 5;
     const bool old = prior && row0 + l < rows;
+    const float factor = weight ? *weight * scale : 1.f;
 #pragma unroll
     for (int fn = 0; fn < C::FN; ++fn)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int col = fn * 32 + 8 * q + 4 * g;
         float x[4] = {v[fn][4 * q], v[fn][4 * q + 1], v[fn][4 * q + 2], v[fn][4 * q + 3]};
-        if (bias && col0 + col < cols) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] += TT<T>::to_f(bias[col0 + col + e]);
-        }
         if (old && col0 + col < cols) {
           const float4 o = *reinterpret_cast<const float4*>(prior + (int64_t)(row0 + l) * cols + col0 + col);
           x[0] += o.x, x[1] += o.y, x[2] += o.z, x[3] += o.w;
+        }
+        if (weight) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] *= factor;
+        }
+        if (bias && col0 + col < cols) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] += TT<T>::to_f(bias[col0 + col + e]);
         }
         char* at = lds + l * (CPR * 16) + stage_chunk<CPR>(l, col / E) * 16;
         if constexpr (sizeof(T) == 2)

@@ -574,7 +574,7 @@ Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
     // and 54; 4096 -> 12288, 384 rows 68 and 73, 512 95 and 78; fp32, 4096 -> 4096, 128 rows 42
     // and 61, 256 81 and 75.
     q.rows = few_rows(in, out, n, dtype);
-    q.few = q.rows.us <= 8 + (wide ? 4 + in * out / 2e6 : in * out / 3e6) + cost(q.tile, j);
+    q.few = n <= (int64_t)1 << 16 && q.rows.us <= 8 + (wide ? 4 + in * out / 2e6 : in * out / 3e6) + cost(q.tile, j);
     if (q.few) return q;
   }
   size_t at = 0;
@@ -647,7 +647,7 @@ int many(const dyra_q4& w, const T* in, int64_t ldi, const T* bias, T* out, int6
   }
   Job j = job(a, {dense, 2 * w.c1, 2 * w.c1 * w.c2, (int32_t)cout}, cin, cin, wide ? 5 : 1, wide ? TERMS_32 : TERMS_1);
   j.part = reinterpret_cast<float4*>(ws + q.part);
-  launch_as<false, BACK>(q.tile, j, Store<T>{out, ldo, (int32_t)cout, bias, nullptr, nullptr}, st);
+  launch_as<false, BACK>(q.tile, j, Store<T>{out, ldo, (int32_t)cout, bias, nullptr, nullptr, nullptr, 1.f}, st);
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
 

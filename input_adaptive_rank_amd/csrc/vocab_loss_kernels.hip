@@ -119,11 +119,18 @@ __global__ __launch_bounds__(1024) void row_loss_kernel(const float2* __restrict
 // backward
 // ---------------------------------------------------------------------------
 
-// The rows that count: map[0 .. *live - 1], ascending, by the first workgroup;
+// What the device finds out about a backward call.
+struct Found {
+  int32_t live;     // rows that count
+  float weight;     // the largest finite |dloss| among them, or 1: what d is relative to
+};
+
+// The rows that count: map[0 .. live - 1], ascending, by the first workgroup;
 // the others set the rest's gradients to zero.
 template <typename T>
-__global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ targets, int n, int vocab,
-                                                    int32_t* __restrict__ live, int32_t* __restrict__ map,
+__global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ targets,
+                                                    const float* __restrict__ dloss, int n, int vocab,
+                                                    Found* __restrict__ found, int32_t* __restrict__ map,
                                                     T* __restrict__ dH, int64_t ld, int C) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   if (blockIdx.x) {
@@ -137,13 +144,18 @@ __global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ 
   }
   constexpr int PER = 8;
   __shared__ int sums[2][16];
+  __shared__ float tops[16];
   int base = 0, flip = 0;
+  float top = 0.f;
   for (int r0 = 0; r0 < n; r0 += 1024 * PER, flip ^= 1) {
     uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int row = r0 + tid * PER + i, t = row < n ? targets[row] : -1;
-      bits |= (uint32_t)(t >= 0 && t < vocab) << i;
+      const bool in = t >= 0 && t < vocab;
+      const float g = in ? fabsf(dloss[row]) : 0.f;
+      bits |= (uint32_t)in << i;
+      if (g < INFINITY) top = fmaxf(top, g);
     }
     const int mine = __popc(bits);
     int upto = mine;
@@ -164,17 +176,27 @@ __global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ 
     for (int i = 0; i < PER; ++i)
       if (bits >> i & 1) map[at++] = r0 + tid * PER + i;
   }
-  if (tid == 0) *live = base;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane == 0) tops[w] = top;
+  __syncthreads();
+  if (tid) return;
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, tops[i]);
+  *found = Found{base, top > 0.f ? top : 1.f};
 }
 
-// d of a tile, in NP bf16 planes; columns past the piece's are zero up to the
-// padded width.
+// d of a tile over scale times the largest weight, in NP bf16 planes; columns past
+// the piece's are zero up to the padded width.  So the entry of a target that is
+// far from likely is 1 whatever the weights are, if they are all the same (the
+// mean's): rounded with its weight it would be off by the same part of itself in
+// every row, and the gradients with it.
 template <int NP>
 struct Gradient {
   bf16_t* d;                    // [NP][rows][ldd]
   int64_t ldd, plane;
   const float *lse, *dloss;
   const int32_t *targets, *map;
+  const Found* found;
   float scale;
   int32_t cols, v0;             // of this piece
 
@@ -185,7 +207,7 @@ struct Gradient {
     const float k2 = scale * LOG2E;
     const bool in = row < rows;
     const int r = in ? map[row] : 0;
-    const float w = in ? dloss[r] * scale : 0.f, l2 = in ? -lse[r] * LOG2E : 0.f;
+    const float w = in ? dloss[r] / found->weight : 0.f, l2 = in ? -lse[r] * LOG2E : 0.f;
     const int at = in ? targets[r] - v0 - col0 : -1;
     const bool has = (unsigned)at < (unsigned)C::WN && (at >> 2 & 1) == g;
 #pragma unroll
@@ -304,7 +326,7 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
     q.part = take(8 * cdiv(V, 64) * n);
     q.mine = take(4 * n);
   } else {
-    q.live = take(4);
+    q.live = take(sizeof(Found));
     q.map = take(4 * n);
     q.d = take(2 * q.np * n * q.piece);
     if (need_dh) {
@@ -371,17 +393,19 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
                   hipStream_t st) {
   constexpr int NP = planes_of<T>(), terms = NP == 3 ? 6 : 1;
   constexpr uint32_t pairs = NP == 3 ? TERMS_33 : TERMS_1;
-  int32_t *live = reinterpret_cast<int32_t*>(ws + q.live), *map = reinterpret_cast<int32_t*>(ws + q.map);
+  Found* found = reinterpret_cast<Found*>(ws + q.live);
+  int32_t *live = &found->live, *map = reinterpret_cast<int32_t*>(ws + q.map);
   float* acc = reinterpret_cast<float*>(ws + q.acc);
   bf16_t* d = reinterpret_cast<bf16_t*>(ws + q.d);
-  hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets, (int)n,
-                     (int)V, live, map, dH, lddh, (int)C);
+  hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets, dloss,
+                     (int)n, (int)V, found, map, dH, lddh, (int)C);
   const Operand h{ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
     const int64_t cols = std::min(q.piece, V - v0), ldd = up(cols, 64);
     const Planes<T> hp = planes(H, ldh, v0 ? 0 : n, C, ws + q.hp, n * C, map, live);
     launch_planes<T>(hp, NP == 3 ? planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C) : Planes<T>{}, st);
-    const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, scale, (int32_t)cols, (int32_t)v0};
+    const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, found, scale, (int32_t)cols,
+                         (int32_t)v0};
     const Job lj = logits_job<T>(h, W, v0, cols, C, q, ws, live);
     launch_as<false, false, NP == 1>(q.logits, lj, e, st);
     if (dH) {
@@ -391,15 +415,16 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
       j.part = lj.part;
       // pieces add up in fp32; the last rounds and puts the rows in their places
       const float* prior = v0 ? acc : nullptr;
-      if (v0 + cols < V) launch_as<false, true>(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr}, st);
-      else launch_as<false, true>(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map}, st);
+      if (v0 + cols < V) launch_as<false, true>(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f}, st);
+      else launch_as<false, true>(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map, &found->weight, scale}, st);
     }
     if (dW) {
       Operand hr = h;   // both turned
       hr.rows = (int32_t)C;
       Job j = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)cols}, hr, n, n, terms, pairs, live, true);
       j.part = lj.part;
-      launch_as<true, true>(q.dw, j, Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr}, st);
+      launch_as<true, true>(q.dw, j,
+                            Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr, &found->weight, scale}, st);
     }
   }
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
