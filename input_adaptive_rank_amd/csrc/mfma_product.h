@@ -603,9 +603,9 @@ inline int64_t up(int64_t a, int64_t m) { return cdiv(a, m) * m; }
 // The tile of a product, by the estimated time.
 enum Shape { BIG, SMALL, THIN };
 
-inline Shape shape_of(const Job& j, bool may_be_big = true) {
+inline Shape shape_of(const Job& j) {
   if (j.a.rows <= 64) return THIN;
-  return may_be_big && layout<Big>(j, -1).cost <= layout<Small>(j, -1).cost ? BIG : SMALL;
+  return layout<Big>(j, -1).cost <= layout<Small>(j, -1).cost ? BIG : SMALL;
 }
 
 // Estimated microseconds of a product.
@@ -644,15 +644,11 @@ inline void launch(const Job& j, const E& e, hipStream_t st) {
 }
 
 // TA, TB: operands that lie turned.
-template <bool TA, bool TB, bool MAY_BE_BIG = true, class E>
+template <bool TA, bool TB, class E>
 void launch_as(Shape s, const Job& j, const E& e, hipStream_t st) {
-  if (MAY_BE_BIG && s == BIG) {
-    if constexpr (MAY_BE_BIG) launch<Big, TA, TB>(j, e, st);
-  } else if (s == SMALL) {
-    launch<Small, TA, TB>(j, e, st);
-  } else {
-    launch<Thin, TA, TB>(j, e, st);
-  }
+  if (s == BIG) launch<Big, TA, TB>(j, e, st);
+  else if (s == SMALL) launch<Small, TA, TB>(j, e, st);
+  else launch<Thin, TA, TB>(j, e, st);
 }
 
 inline bool misaligned(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }

@@ -311,8 +311,7 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
   q.piece = std::min(up(V, 64), up(cdiv(V, cdiv(V, most)), 256));
   const int32_t* live = backward ? SOME : nullptr;
   const Job logits = job(rows_of(n), rows_of(q.piece), C, C, terms, 0, live);
-  // a 256 x 256 tile's d in three planes leaves the registers
-  q.logits = shape_of(logits, !(wide && backward));
+  q.logits = shape_of(logits);
   int64_t parts = part_bytes(q.logits, logits);
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
@@ -407,7 +406,7 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
     const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, found, scale, (int32_t)cols,
                          (int32_t)v0};
     const Job lj = logits_job<T>(h, W, v0, cols, C, q, ws, live);
-    launch_as<false, false, NP == 1>(q.logits, lj, e, st);
+    launch_as<false, false>(q.logits, lj, e, st);
     if (dH) {
       Operand w = lj.b;   // turned: its rows are the reduction
       w.rows = (int32_t)C;

@@ -221,6 +221,26 @@ def test_bad_rows_stay_in_their_row(dtype):
         assert torch.equal(got[keep], want[keep]) and not bool(torch.isfinite(got[150]).all())
 
 
+@pytest.mark.parametrize("weight", [1.0, 1 + 2.0 ** -8, 1 / 3279, 3e-5])
+def test_equal_weights_cost_no_rounding(weight):
+    """Two words and rows of zeros: every probability is 1/2 and d an exact half
+    of the weight, so that a gradient is rounded once, as it is stored.  Rounded
+    with its weight, d would be off by as much again, in every row alike."""
+    import torch
+    from input_adaptive_rank_amd import vocab_loss as L
+    n, c = 96, 72
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    W = torch.randn((2, c), generator=gen, device="cuda").bfloat16()
+    t = (torch.arange(n, device="cuda") % 3 - 1).int()   # none, the first, the second
+    H, g = torch.zeros((n, c), dtype=torch.bfloat16, device="cuda"), torch.full((n,), weight, device="cuda")
+    lse = L.vocab_loss_forward(H, W, t)[1]
+    dH, dW = L.vocab_loss_backward(H, W, t, lse, g)
+    half = 0.5 * g.double()[0] * (W[1] - W[0].double())
+    want = torch.stack([half * 0, half, -half])[(t.long() + 1)]
+    assert bool(((dH.double() - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -12) * want.abs()).all())
+    assert not bool(dW.any())
+
+
 def test_a_word_that_is_masked_by_its_weights():
     """Rows of W of the type's lowest value give logits of -inf or of its
     size: such words have no probability, and the others keep theirs."""
