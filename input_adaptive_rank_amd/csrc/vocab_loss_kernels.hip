@@ -312,7 +312,9 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
   const int32_t* live = backward ? SOME : nullptr;
   const Job logits = job(rows_of(n), rows_of(q.piece), C, C, terms, 0, live);
   q.logits = shape_of(logits);
-  int64_t parts = part_bytes(q.logits, logits);
+  // a last piece of fewer columns may be split into more parts
+  const Job rest = job(rows_of(n), rows_of(V - (cdiv(V, q.piece) - 1) * q.piece), C, C, terms, 0, live);
+  int64_t parts = std::max(part_bytes(q.logits, logits), part_bytes(q.logits, rest));
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
     const size_t here = at;

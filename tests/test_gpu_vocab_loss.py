@@ -221,6 +221,29 @@ def test_bad_rows_stay_in_their_row(dtype):
         assert torch.equal(got[keep], want[keep]) and not bool(torch.isfinite(got[150]).all())
 
 
+@pytest.mark.parametrize("n", [8, 65, 130])
+def test_a_last_piece_stays_within_the_workspace(n):
+    """fp32 weights are taken in pieces; of these two the last has fewer tiles, split
+    into more parts than the first's."""
+    import torch
+    from input_adaptive_rank_amd import vocab_loss as L
+    c, v = 8192, 10816
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    H, W = (torch.randn(s, generator=gen, device="cuda") / c ** 0.5 for s in ((n, c), (v, c)))
+    t = torch.randint(0, v, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    size = L.vocab_loss_workspace_size(n, c, v, F32)
+    ws = torch.full((size + (1 << 23),), 90, dtype=torch.uint8, device="cuda")
+    loss, lse = L.vocab_loss_forward(H, W, t, workspace=ws)
+    assert bool((ws[size:] == 90).all())
+    a = H.double() @ W.double().t()
+    want = torch.logsumexp(a, 1)
+    # logits of 8192 products in six terms; the bounds of check_forward
+    mag = (H.double().abs() @ W.double().abs().t()).amax(1)
+    bound = (6 * (c / 16 + 2) + 67) * U * mag + U * (4 * a.abs().amax(1) + 132 + v / 2048 + 4 * want.abs())
+    assert bool(((lse - want).abs() <= bound).all())
+    assert bool(((loss - (want - a.gather(1, t.long()[:, None])[:, 0])).abs() <= 2 * bound + U * 4 * a.abs().amax(1)).all())
+
+
 @pytest.mark.parametrize("weight", [1.0, 1 + 2.0 ** -8, 1 / 3279, 3e-5])
 def test_equal_weights_cost_no_rounding(weight):
     """Two words and rows of zeros: every probability is 1/2 and d an exact half
