@@ -82,6 +82,9 @@ struct Tile {
 // 256 x 256: 128 flop a byte loaded, one workgroup a CU (128 KB of LDS); 1.27
 // PFLOP/s in whole rounds
 typedef Tile<256, 256, 2, 4, 2, 1, 100, 75> Big;
+// 320 x 256: 142 flop a byte, and other sizes that fill whole rounds (5003 x 4096
+// results are 256 of its tiles: 140 us instead of 174 with 320 tiles of 256 x 256)
+typedef Tile<320, 256, 2, 4, 2, 1, 125, 94> Tall;
 // 128 x 128: four times the tiles, two workgroups a CU
 typedef Tile<128, 128, 2, 2, 2, 2, 45, 55> Small;
 // 64 x 128: a few rows against a matrix that is read once; a deeper ring
@@ -601,16 +604,23 @@ inline size_t align256(int64_t b) { return ((size_t)b + 255) & ~(size_t)255; }
 inline int64_t up(int64_t a, int64_t m) { return cdiv(a, m) * m; }
 
 // The tile of a product, by the estimated time.
-enum Shape { BIG, SMALL, THIN };
+enum Shape { BIG, SMALL, THIN, TALL };
 
 inline Shape shape_of(const Job& j) {
   if (j.a.rows <= 64) return THIN;
-  return layout<Big>(j, -1).cost <= layout<Small>(j, -1).cost ? BIG : SMALL;
+  const double big = layout<Big>(j, -1).cost, small = layout<Small>(j, -1).cost;
+  // where rows or steps are counted on the device, the least padding: 256 (3280 of
+  // 4099 rows, gradients of 4096 x 32000: 2240 us instead of 2310)
+  if (!j.live && layout<Tall>(j, -1).cost < std::min(big, small)) return TALL;
+  return big <= small ? BIG : SMALL;
 }
 
 // Estimated microseconds of a product.
 inline double cost(Shape s, const Job& j) {
-  return s == BIG ? layout<Big>(j, -1).cost : s == SMALL ? layout<Small>(j, -1).cost : layout<Thin>(j, -1).cost;
+  return s == TALL    ? layout<Tall>(j, -1).cost
+         : s == BIG   ? layout<Big>(j, -1).cost
+         : s == SMALL ? layout<Small>(j, -1).cost
+                      : layout<Thin>(j, -1).cost;
 }
 
 // Bytes of partial tiles that a product may leave.
@@ -624,7 +634,10 @@ inline int64_t part_bytes_as(const Job& j) {
 }
 
 inline int64_t part_bytes(Shape s, const Job& j) {
-  return s == BIG ? part_bytes_as<Big>(j) : s == SMALL ? part_bytes_as<Small>(j) : part_bytes_as<Thin>(j);
+  return s == TALL    ? part_bytes_as<Tall>(j)
+         : s == BIG   ? part_bytes_as<Big>(j)
+         : s == SMALL ? part_bytes_as<Small>(j)
+                      : part_bytes_as<Thin>(j);
 }
 
 template <class C, bool TA, bool TB, class E>
@@ -643,9 +656,11 @@ inline void launch(const Job& j, const E& e, hipStream_t st) {
     hipLaunchKernelGGL((join_kernel<C, E>), dim3((unsigned)(tail * C::NW * C::FM)), dim3(64), 0, st, j, e);
 }
 
-// TA, TB: operands that lie turned.
-template <bool TA, bool TB, class E>
+// TA, TB: operands that lie turned; COUNTED: rows or steps are counted on the device.
+template <bool TA, bool TB, bool COUNTED = false, class E>
 void launch_as(Shape s, const Job& j, const E& e, hipStream_t st) {
+  if constexpr (!COUNTED)
+    if (s == TALL) return launch<Tall, TA, TB>(j, e, st);
   if (s == BIG) launch<Big, TA, TB>(j, e, st);
   else if (s == SMALL) launch<Small, TA, TB>(j, e, st);
   else launch<Thin, TA, TB>(j, e, st);

@@ -408,7 +408,7 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
     const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, found, scale, (int32_t)cols,
                          (int32_t)v0};
     const Job lj = logits_job<T>(h, W, v0, cols, C, q, ws, live);
-    launch_as<false, false>(q.logits, lj, e, st);
+    launch_as<false, false, true>(q.logits, lj, e, st);
     if (dH) {
       Operand w = lj.b;   // turned: its rows are the reduction
       w.rows = (int32_t)C;
@@ -416,15 +416,15 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
       j.part = lj.part;
       // pieces add up in fp32; the last rounds and puts the rows in their places
       const float* prior = v0 ? acc : nullptr;
-      if (v0 + cols < V) launch_as<false, true>(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f}, st);
-      else launch_as<false, true>(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map, &found->weight, scale}, st);
+      if (v0 + cols < V) launch_as<false, true, true>(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f}, st);
+      else launch_as<false, true, true>(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map, &found->weight, scale}, st);
     }
     if (dW) {
       Operand hr = h;   // both turned
       hr.rows = (int32_t)C;
       Job j = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)cols}, hr, n, n, terms, pairs, live, true);
       j.part = lj.part;
-      launch_as<true, true>(q.dw, j,
+      launch_as<true, true, true>(q.dw, j,
                             Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr, &found->weight, scale}, st);
     }
   }

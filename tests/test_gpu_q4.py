@@ -124,7 +124,8 @@ def test_forward_and_backward_match_the_oracle(n, c1, c2, group, dtype):
 
 
 @pytest.mark.parametrize("n,c1,c2,dtype", [(5003, 512, 1024, BF16), (2048, 4096, 1024, BF16), (4099, 1024, 4096, BF16),
-                                           (2100, 1024, 1024, F32), (600, 12288, 256, BF16)])
+                                           (2100, 1024, 1024, F32), (600, 12288, 256, BF16), (5003, 264, 4096, BF16),
+                                           (5003, 4096, 264, BF16), (2900, 264, 6000, F32)])
 def test_many_rows_whose_last_round_is_split(n, c1, c2, dtype):
     """Against float64 products on the device, forward and backward."""
     import torch

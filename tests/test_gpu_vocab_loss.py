@@ -147,6 +147,15 @@ def test_forward_and_backward_match_the_oracle(n, c, v, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+@pytest.mark.parametrize("n,v", [(640, 32000), (620, 31000), (1270, 9001)])
+def test_forward_of_many_columns(n, v, dtype):
+    case = make(n, 136, v, dtype, seed=n)
+    from input_adaptive_rank_amd import vocab_loss as L
+    loss, lse = L.vocab_loss_forward(put(case["H"], dtype), put(case["W"], dtype), ints(case["t"]))
+    check_forward(case, dtype, loss, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
 def test_large_and_small_logits(dtype):
     """Logits in the thousands (the exponentials of most underflow) and none
     above 1e-6: the maximum is taken off, the loss keeps its digits."""
