@@ -572,8 +572,9 @@ int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* stream);
  * A few rows (up to some hundreds, by the widths) need no workspace (0 bytes; the
  * pointer may be NULL) and multiply the codes exactly; more rows read W rounded
  * to bf16 (bf16) or exactly (fp32) from the workspace.  Sums are fp32; fp32
- * operands enter as three bf16 terms (2^-24).  An infinity in X may give NaN where the formula
- * has an infinity.  Sums have a fixed order: the same call gives the same bits.
+ * operands enter as three bf16 terms (2^-24).  An infinity in X, or a value above
+ * 2^112, may give NaN or an infinity where the formula has a number or an
+ * infinity.  Sums have a fixed order: the same call gives the same bits.
  * Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
  */
 int dyra_q4_workspace_size(int64_t c1, int64_t c2, int64_t n, int32_t dtype, int32_t backward, size_t* bytes);
@@ -597,7 +598,7 @@ int dyra_q4_backward(const dyra_q4* w, const void* dY, int64_t lddy, void* dX, i
  * loss 0 (its lse is computed).
  *   H: device [n][C], rows ldh elements apart (a multiple of 8 in bf16, 4 in
  *   fp32, at most 2^20).  W: device [V][C].  targets: device int32[n].
- *   loss, lse: device float[n].  scale: positive and finite.
+ *   loss, lse: device float[n].  scale: positive, at most 2^126.
  *   n: 0 .. 2^20;  C: a multiple of 8, <= 2^17;  V: 1 .. 2^24;  n C < 2^33 and
  *   n V < 2^37.
  * Asynchronous on `stream`; no output overlaps another operand.  bf16: exact
@@ -622,7 +623,9 @@ int dyra_vocab_loss_forward(const void* H, int64_t ldh, const void* W, const int
  *   [V][C], or NULL.  One of them must be given; every element is written (n
  *   may be 0).  need_dh, need_dw above: whether they are.
  * The logits are multiplied again for one piece of the vocabulary after the
- * other; a piece's d lies in the workspace, in bf16 (fp32: three bf16 terms).
+ * other; a piece's d lies in the workspace, in bf16 (fp32: three bf16 terms),
+ * relative to scale times the largest finite |dloss| that counts: an entry below
+ * 2^-126 of that loses digits.
  * Sums are fp32 in a fixed order: the same call gives the same bits.
  * Errors as for dyra_vocab_loss_forward.
  */

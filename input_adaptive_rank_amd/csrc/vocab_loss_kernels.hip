@@ -16,8 +16,6 @@
 // the two products of the backward pass (at most 2^-8 of a term, like the
 // rounding of the gradients, which are bf16).  fp32: every operand is three
 // bf16 planes (24 bits), a product the six pairs of planes that reach 2^-24.
-#include <cmath>
-
 #include "mfma_product.h"
 
 namespace {
@@ -347,6 +345,9 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
   return q;
 }
 
+// exponents are taken in base two, so that scale / log 2 has to be a number
+bool bad_scale(float scale) { return !(scale > 0.f && scale <= 0x1p126f); }
+
 int validate(int64_t n, int64_t C, int64_t V, int dtype) {
   if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_EINVAL;
   if (n < 0 || n > (int64_t)1 << 20 || C <= 0 || C % 8 || C > (int64_t)1 << 17 || V <= 0 || V > (int64_t)1 << 24)
@@ -455,7 +456,7 @@ extern "C" int dyra_vocab_loss_forward(const void* H, int64_t ldh, const void* W
                                        void* workspace, size_t ws_bytes, void* stream) {
   const int rc = validate(n, C, V, dtype);
   if (rc) return rc;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DYRA_EINVAL;
+  if (bad_scale(scale)) return DYRA_EINVAL;
   if (n == 0) return DYRA_OK;
   if (!H || !W || !targets || !loss || !lse || !workspace) return DYRA_EINVAL;
   if (misaligned(H, 15) || misaligned(W, 15) || misaligned(workspace, 15) || misaligned(targets, 3) ||
@@ -479,7 +480,7 @@ extern "C" int dyra_vocab_loss_backward(const void* H, int64_t ldh, const void* 
                                         size_t ws_bytes, void* stream) {
   const int rc = validate(n, C, V, dtype);
   if (rc) return rc;
-  if (!(scale > 0.f) || !std::isfinite(scale) || (!dH && !dW)) return DYRA_EINVAL;
+  if (bad_scale(scale) || (!dH && !dW)) return DYRA_EINVAL;
   if (misaligned(dW, 15)) return DYRA_EINVAL;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (n == 0) {

@@ -13,7 +13,9 @@ lse and dloss hold; its lse is computed.  A mean over the rows that count is
 the caller's: dloss = 1 / their number gives its gradient.
 
 The backward pass multiplies the logits again, one piece of the vocabulary at
-a time, and rounds d to W's precision for the two products.  Results do not
+a time, and rounds d to W's precision for the two products, relative to the
+largest weight logit_scale |dloss_t|: rows of equal weights, as a mean's are, lose
+nothing by the weight.  Results do not
 depend on the order in which workgroups run: the same call gives the same bits.
 
 Tensors (GPU, bf16 or fp32, one type throughout):
@@ -67,8 +69,8 @@ def _operands(H, W, targets, logit_scale):
     if not c or c % 8 or not v:
         raise ValueError(f"the width must be a multiple of 8 and the vocabulary not empty: H is {tuple(H.shape)}, "
                          f"W {tuple(W.shape)}")
-    if not 0.0 < logit_scale < float("inf"):
-        raise ValueError(f"logit_scale must be positive and finite, got {logit_scale}")
+    if not 0.0 < logit_scale <= 2.0 ** 126:
+        raise ValueError(f"logit_scale must be positive and finite, at most 2^126, got {logit_scale}")
     hp, ldh = _rows(H, "H", n, c, H.dtype, dev)
     wp = _flat(W, "W", (v, c), H.dtype, dev)
     if wp & 15:

@@ -49,7 +49,7 @@ def _forward(H=P, ldh=64, W=P, targets=P, scale=1.0, loss=P, lse=P, n=10, C=64, 
     (dict(H=None), -1), (dict(W=None), -1), (dict(targets=None), -1), (dict(loss=None), -1), (dict(lse=None), -1),
     (dict(ws=None), -1), (dict(H=P + 2), -1), (dict(W=P + 8), -1), (dict(targets=P + 2), -1), (dict(loss=P + 1), -1),
     (dict(ws=P + 8), -1), (dict(dtype=5), -1), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
-    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(scale=2.0 ** 127), -1),
     (dict(ldh=56), -2), (dict(ldh=68), -2), (dict(ldh=(1 << 20) + 8), -2), (dict(C=12), -2), (dict(V=0), -2),
     (dict(n=-2), -2), (dict(ws_bytes=64), -3),
 ])
@@ -66,7 +66,7 @@ def _backward(H=P, ldh=64, W=P, targets=P, lse=P, dloss=P, scale=1.0, dH=P, lddh
 @pytest.mark.parametrize("kw,code", [
     (dict(H=None), -1), (dict(W=None), -1), (dict(targets=None), -1), (dict(lse=None), -1), (dict(dloss=None), -1),
     (dict(dH=None, dW=None), -1), (dict(ws=None), -1), (dict(dH=P + 2), -1), (dict(dW=P + 4), -1),
-    (dict(lse=P + 2), -1), (dict(scale=0.0), -1), (dict(dtype=3), -1),
+    (dict(lse=P + 2), -1), (dict(scale=0.0), -1), (dict(scale=2.0 ** 127), -1), (dict(dtype=3), -1),
     (dict(lddh=60), -2), (dict(ldh=60), -2), (dict(V=-1), -2), (dict(ws_bytes=1 << 8), -3),
 ])
 def test_backward_rejects_before_any_hip_call(kw, code):
