@@ -422,10 +422,9 @@ __global__ __launch_bounds__(C::NT, C::WPE) void product_kernel(Job j, E e) {
 
 // Adds the parts of the split tiles, in their order; one wave for 32 x WN results.
 template <class C, class E>
-__global__ __launch_bounds__(64) void join_kernel(Job j, E e) {
-  __shared__ __attribute__((aligned(1024))) char lds[32 * C::WN * 4];
+__device__ __forceinline__ void join(const Job& j, const E& e, int block, char* lds) {
   const Layout y = layout<C>(j, j.live ? *j.live : -1);
-  const int tail = blockIdx.x / (C::NW * C::FM), sub = blockIdx.x - tail * (C::NW * C::FM);
+  const int tail = block / (C::NW * C::FM), sub = block - tail * (C::NW * C::FM);
   if (tail >= y.tail) return;
   const int w = sub / C::FM, fm = sub - w * C::FM;
   int m0, n0;
@@ -453,6 +452,14 @@ __global__ __launch_bounds__(64) void join_kernel(Job j, E e) {
       }
   }
   e.template block<C>(v, lds, row0, col0, y.rows);
+}
+
+constexpr int JOIN_LDS = 32 * 64 * 4;   // every tile's WN is 64
+
+template <class C, class E>
+__global__ __launch_bounds__(64) void join_kernel(Job j, E e) {
+  __shared__ __attribute__((aligned(1024))) char lds[JOIN_LDS];
+  join<C>(j, e, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -538,14 +545,11 @@ struct Planes {
   int32_t rows, cols;
 };
 
+// Eight elements from row `from` to row `to`.
 template <typename T>
-__device__ __forceinline__ void make_planes(const Planes<T>& a, int64_t i) {
-  const int per = a.cols / 8;
-  const int64_t row = i / per;
-  const int col = (int)(i - row * per) * 8;
-  if (row >= (a.live ? min(*a.live, a.rows) : a.rows)) return;
-  const T* p = a.in + (a.map ? a.map[row] : row) * a.ld + col;
-  bf16_t* o = a.out + row * a.cols + col;
+__device__ __forceinline__ void split_eight(const Planes<T>& a, int64_t from, int64_t to, int col) {
+  const T* p = a.in + from * a.ld + col;
+  bf16_t* o = a.out + to * a.cols + col;
   if constexpr (sizeof(T) == 2) {
     *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(p);
   } else {
@@ -563,6 +567,14 @@ __device__ __forceinline__ void make_planes(const Planes<T>& a, int64_t i) {
       *reinterpret_cast<uint4*>(o + t * a.plane) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void make_planes(const Planes<T>& a, int64_t i) {
+  const int per = a.cols / 8;
+  const int64_t row = i / per;
+  if (row >= (a.live ? min(*a.live, a.rows) : a.rows)) return;
+  split_eight(a, a.map ? a.map[row] : row, row, (int)(i - row * per) * 8);
 }
 
 // Two matrices in one launch, the first in `first` workgroups.
@@ -640,8 +652,13 @@ inline int64_t part_bytes(Shape s, const Job& j) {
                       : part_bytes_as<Thin>(j);
 }
 
-template <class C, bool TA, bool TB, class E>
-inline void launch(const Job& j, const E& e, hipStream_t st) {
+// Workgroups of a product and of its join.
+struct Grids {
+  int64_t product, join;
+};
+
+template <class C>
+inline Grids grids_as(const Job& j) {
   const Layout y = layout<C>(j, -1);
   int64_t grid = y.count, tail = y.tail;
   // fewer live rows or steps may leave other tiles to split, into 2 SLOTS parts at
@@ -650,20 +667,53 @@ inline void launch(const Job& j, const E& e, hipStream_t st) {
     grid = (int64_t)y.tiles_m * y.tiles_n + 2 * C::SLOTS;
     tail = std::min(C::SLOTS, y.tiles_m * y.tiles_n);
   }
-  if (!grid) return;
-  hipLaunchKernelGGL((product_kernel<C, TA, TB, E>), dim3((unsigned)grid), dim3(C::NT), 0, st, j, e);
-  if (tail)
-    hipLaunchKernelGGL((join_kernel<C, E>), dim3((unsigned)(tail * C::NW * C::FM)), dim3(64), 0, st, j, e);
+  return {grid, tail * C::NW * C::FM};
+}
+
+template <class C, bool TA, bool TB, class E>
+inline void launch(const Job& j, const E& e, bool joined, hipStream_t st) {
+  const Grids g = grids_as<C>(j);
+  if (!g.product) return;
+  hipLaunchKernelGGL((product_kernel<C, TA, TB, E>), dim3((unsigned)g.product), dim3(C::NT), 0, st, j, e);
+  if (joined && g.join) hipLaunchKernelGGL((join_kernel<C, E>), dim3((unsigned)g.join), dim3(64), 0, st, j, e);
 }
 
 // TA, TB: operands that lie turned; COUNTED: rows or steps are counted on the device.
+// joined: with the join, else the caller launches join_two.
 template <bool TA, bool TB, bool COUNTED = false, class E>
-void launch_as(Shape s, const Job& j, const E& e, hipStream_t st) {
+void launch_as(Shape s, const Job& j, const E& e, hipStream_t st, bool joined = true) {
   if constexpr (!COUNTED)
-    if (s == TALL) return launch<Tall, TA, TB>(j, e, st);
-  if (s == BIG) launch<Big, TA, TB>(j, e, st);
-  else if (s == SMALL) launch<Small, TA, TB>(j, e, st);
-  else launch<Thin, TA, TB>(j, e, st);
+    if (s == TALL) return launch<Tall, TA, TB>(j, e, joined, st);
+  if (s == BIG) launch<Big, TA, TB>(j, e, joined, st);
+  else if (s == SMALL) launch<Small, TA, TB>(j, e, joined, st);
+  else launch<Thin, TA, TB>(j, e, joined, st);
+}
+
+// The joins of two products whose sizes are counted on the device, in one launch.
+template <class E>
+__device__ __forceinline__ void join_as(Shape s, const Job& j, const E& e, int block, char* lds) {
+  if (s == BIG) join<Big>(j, e, block, lds);
+  else if (s == SMALL) join<Small>(j, e, block, lds);
+  else join<Thin>(j, e, block, lds);
+}
+
+template <class E>
+__global__ __launch_bounds__(64) void join_two_kernel(Shape s, Job j, E e, int first, Shape s2, Job j2, E e2) {
+  __shared__ __attribute__((aligned(1024))) char lds[JOIN_LDS];
+  if ((int)blockIdx.x < first) join_as(s, j, e, blockIdx.x, lds);
+  else join_as(s2, j2, e2, blockIdx.x - first, lds);
+}
+
+inline int64_t joins_of(Shape s, const Job& j) {
+  return s == BIG ? grids_as<Big>(j).join : s == SMALL ? grids_as<Small>(j).join : grids_as<Thin>(j).join;
+}
+
+template <class E>
+void launch_join_two(Shape s, const Job& j, const E& e, Shape s2, const Job& j2, const E& e2, hipStream_t st) {
+  const int64_t first = joins_of(s, j), second = joins_of(s2, j2);
+  if (first + second)
+    hipLaunchKernelGGL((join_two_kernel<E>), dim3((unsigned)(first + second)), dim3(64), 0, st, s, j, e, (int)first, s2, j2,
+                       e2);
 }
 
 inline bool misaligned(const void* p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }

@@ -183,6 +183,69 @@ __global__ __launch_bounds__(1024) void live_kernel(const int32_t* __restrict__ 
   *found = Found{base, top > 0.f ? top : 1.f};
 }
 
+// The same for a few thousand rows, and their planes, in one launch: `per` rows a
+// workgroup, which counts the rows before them itself; workgroup `groups` finds the
+// rest out, and those behind it make the planes of W.
+template <typename T>
+__global__ __launch_bounds__(256) void gather_kernel(const int32_t* __restrict__ targets,
+                                                     const float* __restrict__ dloss, int n, int vocab,
+                                                     Found* __restrict__ found, int32_t* __restrict__ map,
+                                                     T* __restrict__ dH, int64_t ld, Planes<T> h, int per, int groups,
+                                                     Planes<T> w) {
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (b > groups) return make_planes(w, (int64_t)(b - groups - 1) * 256 + tid);
+  __shared__ int sums[4], place[64];
+  __shared__ float tops[4];
+  const bool all = b == groups;
+  const int r0 = all ? n : b * per;
+  int count = 0;
+  float top = 0.f;
+#pragma unroll 4
+  for (int i = tid; i < r0; i += 256) {
+    const int t = targets[i];
+    const bool in = t >= 0 && t < vocab;
+    count += in;
+    const float g = all && in ? fabsf(dloss[i]) : 0.f;
+    if (g < INFINITY) top = fmaxf(top, g);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    count += __shfl_xor(count, d);
+    top = fmaxf(top, __shfl_xor(top, d));
+  }
+  if (lane == 0) {
+    sums[wave] = count;
+    tops[wave] = top;
+  }
+  __syncthreads();
+  const int base = sums[0] + sums[1] + sums[2] + sums[3];
+  if (all) {
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    if (tid == 0) *found = Found{base, top > 0.f ? top : 1.f};
+    return;
+  }
+  const int rows = min(per, n - r0);
+  if (wave == 0) {
+    const int t = lane < rows ? targets[r0 + lane] : -1;
+    const bool in = t >= 0 && t < vocab;
+    const uint64_t ins = __ballot(in);
+    const int at = base + __popcll(ins & (((uint64_t)1 << lane) - 1));
+    place[lane] = in ? at : -1;
+    if (in) map[at] = r0 + lane;
+  }
+  __syncthreads();
+  const int chunks = h.cols / 8;
+  for (int i = tid; i < rows * chunks; i += 256) {
+    const int r = i / chunks, col = (i - r * chunks) * 8, at = place[r];
+    if (at >= 0) {
+      split_eight(h, r0 + r, at, col);
+    } else if (dH) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 16 / sizeof(T)) *reinterpret_cast<uint4*>(dH + (r0 + r) * ld + col + e) = zero4();
+    }
+  }
+}
+
 // d of a tile over scale times the largest weight, in NP bf16 planes; columns past
 // the piece's are zero up to the padded width.  So the entry of a target that is
 // far from likely is 1 whatever the weights are, if they are all the same (the
@@ -290,7 +353,7 @@ struct Plan {
   int64_t np;                           // planes of an operand
   int64_t piece;                        // columns of the vocabulary at a time
   Shape logits, dh, dw;
-  size_t part, mine, live, map, hp, wp, d, acc, parts, total;
+  size_t part, mine, live, map, hp, wp, d, acc, parts, dw_parts, total;
 };
 
 const int32_t* const SOME = reinterpret_cast<const int32_t*>(4);   // "found on the device", for sizes alone
@@ -337,10 +400,13 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
     if (need_dw) {
       const Job j = job(rows_of(q.piece), rows_of(C), n, n, terms, 0, live, true);
       q.dw = shape_of(j);
-      parts = std::max(parts, part_bytes(q.dw, j));
+      // both gradients' parts are joined in one launch
+      if (need_dh) q.dw_parts = take(part_bytes(q.dw, j));
+      else parts = std::max(parts, part_bytes(q.dw, j));
     }
   }
   q.parts = take(parts);
+  if (!(need_dh && need_dw)) q.dw_parts = q.parts;
   q.total = at;
   return q;
 }
@@ -399,35 +465,54 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
   int32_t *live = &found->live, *map = reinterpret_cast<int32_t*>(ws + q.map);
   float* acc = reinterpret_cast<float*>(ws + q.acc);
   bf16_t* d = reinterpret_cast<bf16_t*>(ws + q.d);
-  hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets, dloss,
-                     (int)n, (int)V, found, map, dH, lddh, (int)C);
+  // Counting anew in each workgroup costs less than a launch up to some thousand rows,
+  // us (in two launches): 8 x 1024 x 4000 41 (44), fp32 1031 x 512 x 5003 147 (150), 8192 x
+  // 256 x 256 54 (58), 16384 x 4096 x 256 297 (254)
+  const bool few = n <= 8192;
+  if (!few)
+    hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets,
+                       dloss, (int)n, (int)V, found, map, dH, lddh, (int)C);
   const Operand h{ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
     const int64_t cols = std::min(q.piece, V - v0), ldd = up(cols, 64);
-    const Planes<T> hp = planes(H, ldh, v0 ? 0 : n, C, ws + q.hp, n * C, map, live);
-    launch_planes<T>(hp, NP == 3 ? planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C) : Planes<T>{}, st);
+    const Planes<T> wp = NP == 3 ? planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C) : Planes<T>{};
+    if (few && v0 == 0) {
+      const int per = (int)std::min<int64_t>(64, std::max<int64_t>(1, 8192 / C)), groups = (int)cdiv(n, per);
+      const int64_t grid = groups + 1 + cdiv((int64_t)wp.rows * (wp.cols / 8), 256);
+      hipLaunchKernelGGL((gather_kernel<T>), dim3((unsigned)grid), dim3(256), 0, st, targets, dloss, (int)n, (int)V,
+                         found, map, dH, lddh, planes(H, ldh, n, C, ws + q.hp, n * C), per, groups, wp);
+    } else {
+      launch_planes<T>(planes(H, ldh, v0 ? 0 : n, C, ws + q.hp, n * C, map, live), wp, st);
+    }
     const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, found, scale, (int32_t)cols,
                          (int32_t)v0};
     const Job lj = logits_job<T>(h, W, v0, cols, C, q, ws, live);
     launch_as<false, false, true>(q.logits, lj, e, st);
+    const bool last = v0 + cols == V, both = dH && dW && last;
+    Job hj, wj;
+    Store<T> he, we;
     if (dH) {
       Operand w = lj.b;   // turned: its rows are the reduction
       w.rows = (int32_t)C;
-      Job j = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)n}, w, cols, ldd, terms, pairs, live);
-      j.part = lj.part;
+      hj = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)n}, w, cols, ldd, terms, pairs, live);
+      hj.part = lj.part;
       // pieces add up in fp32; the last rounds and puts the rows in their places
       const float* prior = v0 ? acc : nullptr;
-      if (v0 + cols < V) launch_as<false, true, true>(q.dh, j, Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f}, st);
-      else launch_as<false, true, true>(q.dh, j, Store<T>{dH, lddh, (int32_t)C, nullptr, prior, map, &found->weight, scale}, st);
+      he = {dH, lddh, (int32_t)C, nullptr, prior, map, &found->weight, scale};
+      if (last) launch_as<false, true, true>(q.dh, hj, he, st, !both);
+      else
+        launch_as<false, true, true>(q.dh, hj,
+                                     Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f}, st);
     }
     if (dW) {
       Operand hr = h;   // both turned
       hr.rows = (int32_t)C;
-      Job j = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)cols}, hr, n, n, terms, pairs, live, true);
-      j.part = lj.part;
-      launch_as<true, true, true>(q.dw, j,
-                            Store<T>{dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr, &found->weight, scale}, st);
+      wj = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)cols}, hr, n, n, terms, pairs, live, true);
+      wj.part = reinterpret_cast<float4*>(ws + q.dw_parts);
+      we = {dW + v0 * C, C, (int32_t)C, nullptr, nullptr, nullptr, &found->weight, scale};
+      launch_as<true, true, true>(q.dw, wj, we, st, !both);
     }
+    if (both) launch_join_two(q.dh, hj, he, q.dw, wj, we, st);
   }
   return hipGetLastError() == hipSuccess ? DYRA_OK : DYRA_EHIP;
 }
