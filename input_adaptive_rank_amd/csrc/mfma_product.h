@@ -661,11 +661,22 @@ template <class C>
 inline Grids grids_as(const Job& j) {
   const Layout y = layout<C>(j, -1);
   int64_t grid = y.count, tail = y.tail;
-  // fewer live rows or steps may leave other tiles to split, into 2 SLOTS parts at
-  // most; but not where one tile row is all or none, or too short to be split
+  // Fewer live rows or steps may leave other tiles to split; but not where one tile
+  // row is all or none, or too short to be split.  A workgroup that finds nothing to
+  // do costs its place for some microseconds (300 x 1024 x 2000: 1024 of them 5 us),
+  // so that a few sizes are gone through, and only for many the bound is taken:
+  // all tiles and 2 SLOTS parts.
   if (j.live && j.may_split && j.terms * y.nk >= 8 && (j.live_k || y.tiles_m > 1)) {
-    grid = (int64_t)y.tiles_m * y.tiles_n + 2 * C::SLOTS;
-    tail = std::min(C::SLOTS, y.tiles_m * y.tiles_n);
+    const int sizes = j.live_k ? y.nk : y.tiles_m, each = j.live_k ? 64 : C::BM;
+    for (int i = 1; i < sizes && sizes <= 32; ++i) {
+      const Layout z = layout<C>(j, i * each);
+      grid = std::max<int64_t>(grid, z.count);
+      tail = std::max<int64_t>(tail, z.tail);
+    }
+    if (sizes > 32) {
+      grid = (int64_t)y.tiles_m * y.tiles_n + 2 * C::SLOTS;
+      tail = std::min(C::SLOTS, y.tiles_m * y.tiles_n);
+    }
   }
   return {grid, tail * C::NW * C::FM};
 }

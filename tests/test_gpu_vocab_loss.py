@@ -167,6 +167,16 @@ def test_large_and_small_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+@pytest.mark.parametrize("n,v", [(300, 1100), (1031, 700), (2500, 130)])
+@pytest.mark.parametrize("ignored", [0.0, 0.4, 0.7, 0.9, 0.99])
+def test_any_number_of_rows_that_count(ignored, n, v, dtype):
+    """How tiles are split is worked out from the rows found on the device."""
+    case = make(n, 520, v, dtype, seed=int(100 * ignored), ignored=ignored)
+    loss, lse, dH, dW = run(case, dtype)
+    check_backward(case, dtype, lse, dH, dW)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
 @pytest.mark.parametrize("n", [9, 300])
 def test_ignored_rows_count_for_nothing(n, dtype):
     """Whatever an ignored row's H, lse and dloss hold, every other result has
