@@ -79,11 +79,11 @@ struct Tile {
   static_assert(FM * 32 == WM && WN == 64, "a wave's part is made of 32 x 64 blocks");
 };
 
-// 256 x 256: 128 flop a byte loaded, one workgroup a CU (128 KB of LDS); 1.27
-// PFLOP/s in whole rounds
+// 256 x 256: 128 flop a byte loaded, one workgroup a CU (128 KB of LDS)
 typedef Tile<256, 256, 2, 4, 2, 1, 100, 75> Big;
 // 320 x 256: 142 flop a byte, and other sizes that fill whole rounds (5003 x 4096
-// results are 256 of its tiles: 140 us instead of 174 with 320 tiles of 256 x 256)
+// results of 64 steps are 256 of its tiles: 142 us instead of 174 with 320 tiles of
+// 256 x 256; 1.28 PFLOP/s in whole rounds)
 typedef Tile<320, 256, 2, 4, 2, 1, 125, 94> Tall;
 // 128 x 128: four times the tiles, two workgroups a CU
 typedef Tile<128, 128, 2, 2, 2, 2, 45, 55> Small;
@@ -93,9 +93,9 @@ typedef Tile<64, 128, 2, 2, 3, 2, 30, 33> Thin;
 // How a product's tiles are laid over the workgroups.  The card holds SLOTS of
 // them at once: whole rounds of tiles are computed by one workgroup each.  The
 // tiles of a last round that would leave much of the card idle are split along
-// the reduction, if that saves more than the join costs (272 tiles of 192 steps:
-// 434 us instead of 568).  Product and join work it out from the sizes that
-// they find.
+// the reduction, if that saves more than the join costs (600 x 4096 results of 192
+// steps: 94 us instead of 145).  Product and join work it out from the sizes
+// that they find.
 struct Layout {
   int rows, tiles_m, tiles_n, kbytes, krows, nk;
   int whole, tail, split, per;   // tiles computed whole, tiles split, parts of one, steps of a part
@@ -622,7 +622,7 @@ inline Shape shape_of(const Job& j) {
   if (j.a.rows <= 64) return THIN;
   const double big = layout<Big>(j, -1).cost, small = layout<Small>(j, -1).cost;
   // where rows or steps are counted on the device, the least padding: 256 (3280 of
-  // 4099 rows, gradients of 4096 x 32000: 2240 us instead of 2310)
+  // 4099 rows, gradients of 4096 x 32000: 2245 us instead of 2315)
   if (!j.live && layout<Tall>(j, -1).cost < std::min(big, small)) return TALL;
   return big <= small ? BIG : SMALL;
 }

@@ -17,7 +17,11 @@
 // the last sum from one more product with ones, and scales each group's sum.
 // Many rows: W is written out once as bf16 (rounded: at most 2^-8 of a weight, like
 // the rounding of the result) and multiplied tile by tile, for the backward pass
-// turned on its way; for fp32 operands as two bf16 planes, which hold it exactly (8 bits of scale times 5).
+// turned on its way; for fp32 operands as two bf16 planes, which hold it exactly (8
+// bits of scale times 5).
+//
+// 4096 -> 4096, group 128: one row 4.5 us (6.8 with the call), 5003 rows 140 (a product
+// at 1.3 PFLOP/s alone 129).
 #include "mfma_product.h"
 
 namespace {
@@ -176,7 +180,7 @@ __global__ __launch_bounds__(ROW_WAVES * 64) void rows_f32_kernel(RowsArgs a) {
 // of 128 bytes a load) into its own part of LDS, half a block at a time, the next
 // one while this one is multiplied, and its codes and parameters beside it.
 // Nothing is shared between the waves before their sums.  48 rows, 4096 ->
-// 12288: 13.5 us (operands straight from memory 28, one block of W a workgroup 41).
+// 12288: 12.6 us (operands straight from memory 28, one block of W a workgroup 41).
 template <int RT, int OB, int GPB>
 __global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
   constexpr int XH = RT * 2048, CODES = 2 * XH, PARAMS = CODES + OB * 1024, WAVE = PARAMS + GPB * 256;
@@ -532,8 +536,8 @@ struct FewRows {
 
 // In bf16 a workgroup fills a CU's LDS, so that workgroups run in rounds of 256;
 // a round's time is made of its turns of eight column blocks, of its sums' way
-// through LDS and, but for the first, of its start.  Measured at 4096 -> 4096 (us): 1 row, RT OB = 1 1 4.7, 1 2
-// 5.2, 1 4 6.7; 64 rows, 2 1 9.7, 2 2 7.0, 2 4 9.4, 3 2 8.4; 384 rows, 2 4 28.7, 3 4 26.3.  fp32
+// through LDS and, but for the first, of its start.  Measured at 4096 -> 4096 (us): 1 row, RT OB = 1 1 4.2, 1 2
+// 4.7, 1 4 6.3; 64 rows, 2 1 9.9, 2 2 7.0, 2 4 8.9, 3 2 8.6; 384 rows, 2 4 26.1, 3 4 24.3.  fp32
 // splits X anew for each pair of blocks of W.
 FewRows few_rows(int64_t c1, int64_t c2, int64_t n, int dtype) {
   const int64_t blocks = cdiv(c2, 16), turns_k = cdiv(cdiv(c1, 128), ROW_WAVES);
@@ -570,9 +574,9 @@ Plan make_plan(int64_t in, int64_t out, int64_t n, int dtype, bool backward) {
   q.tile = shape_of(j);
   if (!backward) {
     // many rows: the weight is written out and read again, two or three launches.
-    // Few and many, measured, us: 4096 -> 4096, 384 rows 23 and 38, 768 45 and 49, 1024 64
-    // and 54; 4096 -> 12288, 384 rows 68 and 73, 512 95 and 78; fp32, 4096 -> 4096, 128 rows 42
-    // and 61, 256 81 and 75.
+    // Few and many, measured, us: 4096 -> 4096, 384 rows 24 and 38, 768 48 and 56, 1024 69
+    // and 58; 4096 -> 12288, 384 rows 72 and 73, 512 104 and 78; fp32, 4096 -> 4096, 128 rows
+    // 42 and 60, 256 80 and 73.
     q.rows = few_rows(in, out, n, dtype);
     q.few = n <= (int64_t)1 << 16 && q.rows.us <= 8 + (wide ? 4 + in * out / 2e6 : in * out / 3e6) + cost(q.tile, j);
     if (q.few) return q;

@@ -4,13 +4,14 @@
 //   d_tv = scale dloss_t (exp(a_tv - lse_t) - [v = target_t])
 //   dH = d W,  dW = d^T H
 //
-// Forward: one product whose epilogue leaves, for each row and tile of
-// columns, the maximum and the sum of exponentials below it; a second launch
-// joins them.  Backward: for one piece of the vocabulary after the other the
-// logits are multiplied again, d goes to memory as bf16 (row by row for dH,
-// transposed for dW, so that both products find their reduction axis
-// contiguous), and the two gradients are products of the piece.  The pieces
-// keep d within what the last-level cache holds.
+// Forward: one product whose epilogue leaves, for each row and 64 columns, the
+// maximum and the sum of exponentials below it; a second launch joins them.  4099 x
+// 4096 x 32000: 870 us, a library's product alone 830 to 870.  Backward: the rows
+// that count are gathered; for one piece of the vocabulary after the other their
+// logits are multiplied again, d goes to memory as bf16, and the two gradients are
+// products of the piece, whose operands the LDS turns where they lie across the
+// reduction.  The pieces keep d within what the last-level cache holds.  The same
+// sizes, 3280 rows that count: 2275 us, 1.13 PFLOP/s.
 //
 // bf16: logits are sums of exact products in fp32; d is rounded to bf16 for
 // the two products of the backward pass (at most 2^-8 of a term, like the
