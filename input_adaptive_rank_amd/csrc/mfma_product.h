@@ -89,6 +89,10 @@ typedef Tile<320, 256, 2, 4, 2, 1, 125, 94> Tall;
 typedef Tile<128, 128, 2, 2, 2, 2, 45, 55> Small;
 // 64 x 128: a few rows against a matrix that is read once; a deeper ring
 typedef Tile<64, 128, 2, 2, 3, 2, 30, 33> Thin;
+// The same of an fp32 matrix that is split into its planes on the way (direct_kernel)
+struct Direct : Tile<64, 128, 2, 2, 2, 1, 125, 125> {
+  static constexpr int A_SLOT = BM * 128, SLOT = 3 * A_SLOT + BN * 256, LDS = NS * SLOT;
+};
 
 // How a product's tiles are laid over the workgroups.  The card holds SLOTS of
 // them at once: whole rounds of tiles are computed by one workgroup each.  The
@@ -159,6 +163,21 @@ __device__ __forceinline__ void corner(const Layout& y, int t, int& m0, int& n0)
 
 template <class C>
 using Acc = f32x16[C::FM][C::FN];
+
+// Eight numbers in three bf16 planes.
+__device__ __forceinline__ void split3(float (&v)[8], uint4 (&out)[3]) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+      v[2 * e] -= __uint_as_float(h[e] << 16);
+      v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+    }
+    out[t] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
 
 // A turned operand in a slot: 64 rows of W = BM or BN elements.  A 16-byte chunk
 // lies at chunk ^ turn(row): the four rows that 32 lanes read together lie in four
@@ -420,6 +439,163 @@ __global__ __launch_bounds__(C::NT, C::WPE) void product_kernel(Job j, E e) {
                                                            acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3]);
 }
 
+// The B of direct_kernel: 64 fp32 elements of 128 rows, or (turned) 64 rows of 128
+// elements, 32 KB a step, eight loads a wave.
+template <bool TURNED>
+struct Fp32 {
+  static constexpr int LOADS = 8;
+  int v[LOADS], edge;
+  const char* p;
+  int64_t ld;
+
+  __device__ __forceinline__ void open(const Operand& o, int at, int w, int lane) {
+    const int count = o.rows - at;
+    ld = o.ld;
+    p = reinterpret_cast<const char*>(o.p) + (TURNED ? 4 * (int64_t)at : at * ld);
+    if constexpr (TURNED) {
+      // row 2 w + 8 i + lane / 32; chunk ^ 8 in every other eight rows, which the two
+      // halves of a wave read together
+      edge = 2 * w + (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int row = edge + 8 * i, ch = (lane & 31) ^ ((row & 8));
+        v[i] = ch * 4 < count ? row * (int)ld + ch * 16 : OUT;
+      }
+    } else {
+      // row 4 w + 16 i + lane / 16, chunk (lane % 16) ^ (row % 16)
+      const int row0 = 4 * w + (lane >> 4);
+      edge = ((lane & 15) ^ row0) << 4;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int row = row0 + 16 * i;
+        v[i] = row < count ? row * (int)ld + edge : OUT;
+      }
+    }
+  }
+  // bytes: of a row; rows: that count
+  template <int OFF>
+  __device__ __forceinline__ void step(int kt, int bytes, int rows, bool live, uint32_t to) const {
+    const i32x4v rs = rsrc_words(TURNED ? p + (int64_t)kt * 64 * ld : p, 0x7fffffffu);
+    const int kb = TURNED ? 0 : kt * 256, left = live ? (TURNED ? rows - kt * 64 : bytes - kb) : 0;
+    static_for<0, LOADS>([&](auto i) __attribute__((always_inline)) {
+      constexpr int I = decltype(i)::value;
+      dma16k<OFF + I * 4096>(rs, edge + (TURNED ? 8 * I : 0) < left ? v[I] : OUT, kb, to);
+    });
+  }
+  // 8 elements of row or column `at` for sub-step s
+  __device__ __forceinline__ static void read(const char* slot, int s, int at, int g, float (&x)[8]) {
+    if constexpr (TURNED) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int row = 16 * s + 8 * g + e;
+        x[e] = *reinterpret_cast<const float*>(slot + row * 512 + (((at >> 2) ^ (8 * g)) << 4) + (at & 3) * 4);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 f = *reinterpret_cast<const float4*>(slot + at * 256 + (((4 * s + 2 * g + h) ^ (at & 15)) << 4));
+        x[4 * h] = f.x, x[4 * h + 1] = f.y, x[4 * h + 2] = f.z, x[4 * h + 3] = f.w;
+      }
+    }
+  }
+};
+
+// A few rows, in three planes, by an fp32 matrix that is read once, as it lies: each
+// wave splits what it multiplies, which takes about as long as the six products do,
+// and both less than the matrix takes to arrive.  Loss of fp32 rows, us (with planes
+// of W in memory first): 4 x 2048 x 30000 72 (233), 100 x 1024 x 8000 43 (51); with more
+// rows the splitting costs more than the planes, 700 x 1024 x 5000 77 (72).
+template <bool TB, class E>
+__global__ __launch_bounds__(Direct::NT, 1) void direct_kernel(Job j, E e) {
+  typedef Direct C;
+  __shared__ __attribute__((aligned(1024))) char ring[C::LDS];
+  const Layout y = layout<C>(j, j.live ? *j.live : -1);
+  if ((int)blockIdx.x >= y.count) return;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 31, g = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / C::NWN, wn = w % C::NWN;
+  const int over = (int)blockIdx.x - y.whole, part = over < 0 ? over : xcd_tile_id(over, y.count - y.whole);
+  int m0, n0, kt = 0, steps = y.nk;
+  if (part < 0) {
+    corner<C>(y, xcd_tile_id(blockIdx.x, y.whole), m0, n0);
+  } else {
+    const int z = part / y.tail;
+    corner<C>(y, y.whole + part - z * y.tail, m0, n0);
+    kt = z * y.per;
+    steps = max(0, min(y.per, y.nk - kt));
+  }
+  Bring<C::BM, C::LA, C::NW, false> a[3];
+  Fp32<TB> b;
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    a[t].open(j.a, y.rows - m0, w, lane);
+    a[t].aim(j.a, m0, t);
+  }
+  b.open(j.b, n0, w, lane);
+  const uint32_t base = lds_addr(ring) + w * 1024;
+  int left = steps;
+  auto issue = [&](uint32_t slot) __attribute__((always_inline)) {
+    static_for<0, 3>([&](auto t) __attribute__((always_inline)) {
+      constexpr int T = decltype(t)::value;
+      a[T].template step<T * C::A_SLOT>(kt, y.kbytes, y.krows, left > 0, base + slot);
+    });
+    b.template step<3 * C::A_SLOT>(kt, 2 * y.kbytes, y.krows, left > 0, base + slot);
+    --left;
+    ++kt;
+  };
+  Acc<C> acc;
+#pragma unroll
+  for (int fn = 0; fn < C::FN; ++fn)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[0][fn][v] = 0.f;
+  const bool busy = m0 + wm * C::WM < y.rows && n0 + wn * C::WN < j.b.rows;
+  const Feed<C::BM, C::FM, false> fa(wm * C::WM, lane);
+  uint32_t at = 0;
+  issue(0);
+  auto walk = [&](auto multiplies) __attribute__((always_inline)) {
+    for (int t = 0; t < steps; ++t) {
+      wait_vm_lgkm0<0>();   // this wave's loads of step t have landed
+      bare_barrier();       // everyone's; the other slot is free
+      issue(C::SLOT - at);  // step t + 1
+      if constexpr (decltype(multiplies)::value) {
+        const char* slot = ring + at;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint4 x[3], q[C::FN][3];
+#pragma unroll
+          for (int t3 = 0; t3 < 3; ++t3) x[t3] = fa.read(slot + t3 * C::A_SLOT, s, 0);
+#pragma unroll
+          for (int fn = 0; fn < C::FN; ++fn) {
+            float f[8];
+            Fp32<TB>::read(slot + 3 * C::A_SLOT, s, wn * C::WN + fn * 32 + l, g, f);
+            split3(f, q[fn]);
+          }
+#pragma unroll
+          for (int i = 0; i < 6; ++i) {
+            const uint32_t pr = TERMS_33 >> (4 * i);
+#pragma unroll
+            for (int fn = 0; fn < C::FN; ++fn) TT<bf16_t>::mma(acc[0][fn], q[fn][pr >> 2 & 3], x[pr & 3]);
+          }
+        }
+      }
+      at = C::SLOT - at;
+    }
+  };
+  if (busy) walk(std::true_type());
+  else walk(std::false_type());
+  wait_vm_lgkm0<0>();
+  bare_barrier();
+  if (part < 0) {
+    e.template tile<C>(acc, ring, m0, n0, y.rows, wm, wn);
+    return;
+  }
+  float4* mine = j.part + ((int64_t)part * C::NW + w) * C::QUADS * 64 + lane;
+#pragma unroll
+  for (int i = 0; i < C::FN * 4; ++i)
+    mine[i * 64] = make_float4(acc[0][i / 4][i % 4 * 4], acc[0][i / 4][i % 4 * 4 + 1], acc[0][i / 4][i % 4 * 4 + 2],
+                               acc[0][i / 4][i % 4 * 4 + 3]);
+}
+
 // Adds the parts of the split tiles, in their order; one wave for 32 x WN results.
 template <class C, class E>
 __device__ __forceinline__ void join(const Job& j, const E& e, int block, char* lds) {
@@ -555,17 +731,10 @@ __device__ __forceinline__ void split_eight(const Planes<T>& a, int64_t from, in
   } else {
     const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
     float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint4 q[3];
+    split3(v, q);
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      uint32_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-        v[2 * e] -= __uint_as_float(h[e] << 16);
-        v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-      }
-      *reinterpret_cast<uint4*>(o + t * a.plane) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(o + t * a.plane) = q[t];
   }
 }
 
@@ -616,7 +785,7 @@ inline size_t align256(int64_t b) { return ((size_t)b + 255) & ~(size_t)255; }
 inline int64_t up(int64_t a, int64_t m) { return cdiv(a, m) * m; }
 
 // The tile of a product, by the estimated time.
-enum Shape { BIG, SMALL, THIN, TALL };
+enum Shape { BIG, SMALL, THIN, TALL, DIRECT };
 
 inline Shape shape_of(const Job& j) {
   if (j.a.rows <= 64) return THIN;
@@ -629,7 +798,8 @@ inline Shape shape_of(const Job& j) {
 
 // Estimated microseconds of a product.
 inline double cost(Shape s, const Job& j) {
-  return s == TALL    ? layout<Tall>(j, -1).cost
+  return s == DIRECT  ? layout<Direct>(j, -1).cost
+         : s == TALL  ? layout<Tall>(j, -1).cost
          : s == BIG   ? layout<Big>(j, -1).cost
          : s == SMALL ? layout<Small>(j, -1).cost
                       : layout<Thin>(j, -1).cost;
@@ -646,7 +816,8 @@ inline int64_t part_bytes_as(const Job& j) {
 }
 
 inline int64_t part_bytes(Shape s, const Job& j) {
-  return s == TALL    ? part_bytes_as<Tall>(j)
+  return s == DIRECT  ? part_bytes_as<Direct>(j)
+         : s == TALL  ? part_bytes_as<Tall>(j)
          : s == BIG   ? part_bytes_as<Big>(j)
          : s == SMALL ? part_bytes_as<Small>(j)
                       : part_bytes_as<Thin>(j);
@@ -700,10 +871,20 @@ void launch_as(Shape s, const Job& j, const E& e, hipStream_t st, bool joined = 
   else launch<Thin, TA, TB>(j, e, joined, st);
 }
 
+// The same with B in fp32 (DIRECT): three planes of A in one walk.
+template <bool TB, class E>
+void launch_direct(const Job& j, const E& e, hipStream_t st, bool joined = true) {
+  const Grids g = grids_as<Direct>(j);
+  if (!g.product) return;
+  hipLaunchKernelGGL((direct_kernel<TB, E>), dim3((unsigned)g.product), dim3(Direct::NT), 0, st, j, e);
+  if (joined && g.join) hipLaunchKernelGGL((join_kernel<Direct, E>), dim3((unsigned)g.join), dim3(64), 0, st, j, e);
+}
+
 // The joins of two products whose sizes are counted on the device, in one launch.
 template <class E>
 __device__ __forceinline__ void join_as(Shape s, const Job& j, const E& e, int block, char* lds) {
-  if (s == BIG) join<Big>(j, e, block, lds);
+  if (s == DIRECT) join<Direct>(j, e, block, lds);
+  else if (s == BIG) join<Big>(j, e, block, lds);
   else if (s == SMALL) join<Small>(j, e, block, lds);
   else join<Thin>(j, e, block, lds);
 }
@@ -716,7 +897,10 @@ __global__ __launch_bounds__(64) void join_two_kernel(Shape s, Job j, E e, int f
 }
 
 inline int64_t joins_of(Shape s, const Job& j) {
-  return s == BIG ? grids_as<Big>(j).join : s == SMALL ? grids_as<Small>(j).join : grids_as<Thin>(j).join;
+  return s == DIRECT  ? grids_as<Direct>(j).join
+         : s == BIG   ? grids_as<Big>(j).join
+         : s == SMALL ? grids_as<Small>(j).join
+                      : grids_as<Thin>(j).join;
 }
 
 template <class E>

@@ -16,7 +16,8 @@
 // bf16: logits are sums of exact products in fp32; d is rounded to bf16 for
 // the two products of the backward pass (at most 2^-8 of a term, like the
 // rounding of the gradients, which are bf16).  fp32: every operand is three
-// bf16 planes (24 bits), a product the six pairs of planes that reach 2^-24.
+// bf16 planes (24 bits), a product the six pairs of planes that reach 2^-24; W is
+// split on its way where few rows read it, else written out as planes first.
 #include "mfma_product.h"
 
 namespace {
@@ -353,29 +354,32 @@ Operand rows_of(int64_t rows) { return {nullptr, 0, 0, (int32_t)rows}; }
 struct Plan {
   int64_t np;                           // planes of an operand
   int64_t piece;                        // columns of the vocabulary at a time
-  Shape logits, dh, dw;
+  Shape logits, dh, dw;                 // logits and dh both DIRECT: W is read as it is
+  double us;                            // estimated, of what depends on that
   size_t part, mine, live, map, hp, wp, d, acc, parts, dw_parts, total;
 };
 
 const int32_t* const SOME = reinterpret_cast<const int32_t*>(4);   // "found on the device", for sizes alone
 
-Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool need_dh, bool need_dw) {
+Plan plan_as(bool direct, int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool need_dh, bool need_dw) {
   Plan q{};
   const bool wide = dtype == DYRA_F32;
   q.np = wide ? 3 : 1;
-  const int terms = wide ? 6 : 1;
+  const int terms = wide ? 6 : 1, once = direct ? 1 : terms;
   // d of a piece is at most 2^27 elements a plane (256 MB in bf16, the last-level
   // cache), planes of fp32 weights at most 2^28
   int64_t most = (int64_t)1 << 20;
   if (backward) most = std::min<int64_t>(most, ((int64_t)1 << 27) / n);
-  if (wide) most = std::min<int64_t>(most, ((int64_t)1 << 28) / (3 * C));
+  if (wide && !direct) most = std::min<int64_t>(most, ((int64_t)1 << 28) / (3 * C));
   most = std::max<int64_t>(256, most & ~(int64_t)255);
   q.piece = std::min(up(V, 64), up(cdiv(V, cdiv(V, most)), 256));
   const int32_t* live = backward ? SOME : nullptr;
-  const Job logits = job(rows_of(n), rows_of(q.piece), C, C, terms, 0, live);
-  q.logits = shape_of(logits);
+  const Job logits = job(rows_of(n), rows_of(q.piece), C, C, once, 0, live);
+  q.logits = direct ? DIRECT : shape_of(logits);
   // a last piece of fewer columns may be split into more parts
-  const Job rest = job(rows_of(n), rows_of(V - (cdiv(V, q.piece) - 1) * q.piece), C, C, terms, 0, live);
+  const Job rest = job(rows_of(n), rows_of(V - (cdiv(V, q.piece) - 1) * q.piece), C, C, once, 0, live);
+  // the planes of W go to memory at 5 TB/s, 10 bytes an element, after a launch
+  q.us = cost(q.logits, logits) + (wide && !direct ? 4 + 2e-6 * q.piece * C : 0.);
   int64_t parts = std::max(part_bytes(q.logits, logits), part_bytes(q.logits, rest));
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
@@ -383,7 +387,7 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
     at += align256(bytes);
     return here;
   };
-  if (wide) q.wp = take(2 * q.np * q.piece * C);
+  if (wide && !direct) q.wp = take(2 * q.np * q.piece * C);
   if (wide || backward) q.hp = take(2 * q.np * n * C);
   if (!backward) {
     q.part = take(8 * cdiv(V, 64) * n);
@@ -392,9 +396,10 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
     q.live = take(sizeof(Found));
     q.map = take(4 * n);
     q.d = take(2 * q.np * n * q.piece);
+    const Job j = job(rows_of(n), rows_of(C), q.piece, q.piece, once, 0, live);
+    q.dh = direct ? DIRECT : shape_of(j);
+    q.us += cost(q.dh, j);   // wanted or not, so that dW does not depend on it
     if (need_dh) {
-      const Job j = job(rows_of(n), rows_of(C), q.piece, q.piece, terms, 0, live);
-      q.dh = shape_of(j);
       parts = std::max(parts, part_bytes(q.dh, j));
       if (q.piece < V) q.acc = take(4 * n * C);
     }
@@ -409,7 +414,15 @@ Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool n
   q.parts = take(parts);
   if (!(need_dh && need_dw)) q.dw_parts = q.parts;
   q.total = at;
+  q.us *= (double)V / q.piece;
   return q;
+}
+
+Plan make_plan(int64_t n, int64_t C, int64_t V, int dtype, bool backward, bool need_dh, bool need_dw) {
+  const Plan q = plan_as(false, n, C, V, dtype, backward, need_dh, need_dw);
+  if (dtype != DYRA_F32) return q;
+  const Plan d = plan_as(true, n, C, V, dtype, backward, need_dh, need_dw);
+  return d.us < q.us ? d : q;
 }
 
 // exponents are taken in base two, so that scale / log 2 has to be a number
@@ -430,6 +443,7 @@ Job logits_job(Operand h, const T* W, int64_t v0, int64_t cols, int64_t C, const
                const int32_t* live) {
   Job j;
   if constexpr (sizeof(T) == 2) j = job(h, {W + v0 * C, 2 * C, 0, (int32_t)cols}, C, C, 1, TERMS_1, live);
+  else if (q.logits == DIRECT) j = job(h, {W + v0 * C, 4 * C, 0, (int32_t)cols}, C, C, 1, 0, live);
   else j = job(h, {ws + q.wp, 2 * C, 2 * q.piece * C, (int32_t)cols}, C, C, 6, TERMS_33, live);
   j.part = reinterpret_cast<float4*>(ws + q.parts);
   return j;
@@ -447,9 +461,11 @@ int forward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, fl
     const int64_t cols = std::min(q.piece, V - v0);
     if constexpr (wide)
       launch_planes<T>(planes(H, ldh, v0 ? 0 : n, C, ws + q.hp, n * C),
-                       planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C), st);
-    launch_as<false, false>(q.logits, logits_job<T>(h, W, v0, cols, C, q, ws, nullptr),
-              RowStats{part, mine, targets, scale, (int32_t)cols, (int32_t)v0}, st);
+                       q.logits == DIRECT ? Planes<T>{} : planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C), st);
+    const Job j = logits_job<T>(h, W, v0, cols, C, q, ws, nullptr);
+    const RowStats e{part, mine, targets, scale, (int32_t)cols, (int32_t)v0};
+    if (wide && q.logits == DIRECT) launch_direct<false>(j, e, st);
+    else launch_as<false, false>(q.logits, j, e, st);
   }
   hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)cdiv(n, 32)), dim3(1024), 0, st, part, mine, targets, loss, lse,
                      (int)n, (int)V, (int)cdiv(V, 64));
@@ -470,13 +486,14 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
   // us (in two launches): 8 x 1024 x 4000 41 (44), fp32 1031 x 512 x 5003 147 (150), 8192 x
   // 256 x 256 54 (58), 16384 x 4096 x 256 297 (254)
   const bool few = n <= 8192;
+  const bool direct = NP == 3 && q.logits == DIRECT;
   if (!few)
     hipLaunchKernelGGL((live_kernel<T>), dim3((unsigned)(1 + (dH ? cdiv(n, 16) : 0))), dim3(1024), 0, st, targets,
                        dloss, (int)n, (int)V, found, map, dH, lddh, (int)C);
   const Operand h{ws + q.hp, 2 * C, 2 * n * C, (int32_t)n};
   for (int64_t v0 = 0; v0 < V; v0 += q.piece) {
     const int64_t cols = std::min(q.piece, V - v0), ldd = up(cols, 64);
-    const Planes<T> wp = NP == 3 ? planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C) : Planes<T>{};
+    const Planes<T> wp = NP == 3 && !direct ? planes(W + v0 * C, C, cols, C, ws + q.wp, q.piece * C) : Planes<T>{};
     if (few && v0 == 0) {
       const int per = (int)std::min<int64_t>(64, std::max<int64_t>(1, 8192 / C)), groups = (int)cdiv(n, per);
       const int64_t grid = groups + 1 + cdiv((int64_t)wp.rows * (wp.cols / 8), 256);
@@ -488,22 +505,27 @@ int backward_impl(const T* H, int64_t ldh, const T* W, const int32_t* targets, c
     const Gradient<NP> e{d, ldd, n * q.piece, lse, dloss, targets, map, found, scale, (int32_t)cols,
                          (int32_t)v0};
     const Job lj = logits_job<T>(h, W, v0, cols, C, q, ws, live);
-    launch_as<false, false, true>(q.logits, lj, e, st);
+    if constexpr (NP == 3) {
+      if (direct) launch_direct<false>(lj, e, st);
+    }
+    if (!direct) launch_as<false, false, true>(q.logits, lj, e, st);
     const bool last = v0 + cols == V, both = dH && dW && last;
     Job hj, wj;
     Store<T> he, we;
     if (dH) {
       Operand w = lj.b;   // turned: its rows are the reduction
       w.rows = (int32_t)C;
-      hj = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)n}, w, cols, ldd, terms, pairs, live);
+      hj = job({d, 2 * ldd, 2 * n * q.piece, (int32_t)n}, w, cols, ldd, direct ? 1 : terms, pairs, live);
       hj.part = lj.part;
       // pieces add up in fp32; the last rounds and puts the rows in their places
       const float* prior = v0 ? acc : nullptr;
       he = {dH, lddh, (int32_t)C, nullptr, prior, map, &found->weight, scale};
-      if (last) launch_as<false, true, true>(q.dh, hj, he, st, !both);
-      else
-        launch_as<false, true, true>(q.dh, hj,
-                                     Store<float>{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f}, st);
+      const Store<float> add{acc, C, (int32_t)C, nullptr, prior, nullptr, nullptr, 1.f};
+      if constexpr (NP == 3) {
+        if (direct) launch_direct<true>(hj, last ? he : add, st, !both);
+      }
+      if (!direct && last) launch_as<false, true, true>(q.dh, hj, he, st, !both);
+      else if (!direct) launch_as<false, true, true>(q.dh, hj, add, st);
     }
     if (dW) {
       Operand hr = h;   // both turned
