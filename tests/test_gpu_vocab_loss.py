@@ -167,7 +167,7 @@ def test_large_and_small_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
-@pytest.mark.parametrize("n,v", [(300, 1100), (1031, 700), (2500, 130)])
+@pytest.mark.parametrize("n,v", [(300, 1100), (1031, 700), (2500, 130), (9001, 65)])
 @pytest.mark.parametrize("ignored", [0.0, 0.4, 0.7, 0.9, 0.99])
 def test_any_number_of_rows_that_count(ignored, n, v, dtype):
     """How tiles are split is worked out from the rows found on the device."""
@@ -403,13 +403,15 @@ def test_gradients_match_differences():
         assert abs(slope - (dev * step).sum()) <= 2.0 ** -14 * np.abs(dev * step).sum()
 
 
-def test_same_bits_on_every_call_and_in_graph_replays():
+@pytest.mark.parametrize("dtype,n,c,v", [(BF16, 300, 136, 3000), (BF16, 9001, 72, 515), (F32, 40, 136, 3000),
+                                         (F32, 900, 520, 1500)])
+def test_same_bits_on_every_call_and_in_graph_replays(dtype, n, c, v):
     """Two captured graphs with their own workspaces; targets and rows change
     between replays, and with them how many rows count."""
     import torch
     from input_adaptive_rank_amd import vocab_loss as L
-    c = make(300, 136, 3000, BF16, seed=14)
-    H, W, t, g, keep = put(c["H"], BF16), put(c["W"], BF16), ints(c["t"]), floats(c["dloss"]), {}
+    c = make(n, c, v, dtype, seed=14)
+    H, W, t, g, keep = put(c["H"], dtype), put(c["W"], dtype), ints(c["t"]), floats(c["dloss"]), {}
 
     def step():
         keep["f"] = L.vocab_loss_forward(H, W, t)
@@ -429,7 +431,7 @@ def test_same_bits_on_every_call_and_in_graph_replays():
         graphs.append((graph, dict(keep)))
     for rep in range(4):
         H.mul_(0.75)
-        t.copy_(torch.randint(-1 - 1000 * rep, 3000, (300,), device="cuda", dtype=torch.int32))
+        t.copy_(torch.randint(-1 - v // 3 * rep, v, (n,), device="cuda", dtype=torch.int32))
         f = L.vocab_loss_forward(H, W, t)
         want = f + L.vocab_loss_backward(H, W, t, f[1], g)
         torch.cuda.synchronize()
