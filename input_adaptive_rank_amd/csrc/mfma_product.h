@@ -164,14 +164,22 @@ __device__ __forceinline__ void corner(const Layout& y, int t, int& m0, int& n0)
 template <class C>
 using Acc = f32x16[C::FM][C::FN];
 
-// Eight numbers in three bf16 planes.
-__device__ __forceinline__ void split3(float (&v)[8], uint4 (&out)[3]) {
+// Eight numbers in N bf16 planes.  The first of several is at most bf16's largest
+// number: rounded, a finite number above 2^128 (1 - 2^-9) would become an infinity
+// and the next planes NaN; what is cut off fits the other two as well.  A single
+// plane is rounded as usual.
+template <int N>
+__device__ __forceinline__ void split(float (&v)[8], uint4 (&out)[N]) {
+  constexpr float TOP = 0x1.fep127f;
 #pragma unroll
-  for (int t = 0; t < 3; ++t) {
+  for (int t = 0; t < N; ++t) {
     uint32_t h[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+      if (N > 1 && t == 0)
+        h[e] = pack_bf16x2(__builtin_amdgcn_fmed3f(v[2 * e], -TOP, TOP),
+                           __builtin_amdgcn_fmed3f(v[2 * e + 1], -TOP, TOP));
+      else h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
       v[2 * e] -= __uint_as_float(h[e] << 16);
       v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
     }
@@ -568,7 +576,7 @@ __global__ __launch_bounds__(Direct::NT, 1) void direct_kernel(Job j, E e) {
           for (int fn = 0; fn < C::FN; ++fn) {
             float f[8];
             Fp32<TB>::read(slot + 3 * C::A_SLOT, s, wn * C::WN + fn * 32 + l, g, f);
-            split3(f, q[fn]);
+            split(f, q[fn]);
           }
 #pragma unroll
           for (int i = 0; i < 6; ++i) {
@@ -732,7 +740,7 @@ __device__ __forceinline__ void split_eight(const Planes<T>& a, int64_t from, in
     const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
     float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     uint4 q[3];
-    split3(v, q);
+    split(v, q);
 #pragma unroll
     for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(o + t * a.plane) = q[t];
   }

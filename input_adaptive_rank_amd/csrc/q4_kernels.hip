@@ -143,18 +143,12 @@ __global__ __launch_bounds__(ROW_WAVES * 64) void rows_f32_kernel(RowsArgs a) {
         for (int r = 0; r < RT; ++r) {
           float v[8] = {x[r][s][0].x, x[r][s][0].y, x[r][s][0].z, x[r][s][0].w,
                         x[r][s][1].x, x[r][s][1].y, x[r][s][1].z, x[r][s][1].w};
+          uint4 planes[3];
+          split(v, planes);
 #pragma unroll
-          for (int t = 0; t < 3; ++t) {
-            uint32_t h[4];
+          for (int t = 0; t < 3; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-              v[2 * e] -= __uint_as_float(h[e] << 16);
-              v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-            }
-#pragma unroll
-            for (int o = 0; o < OB; ++o) mma16(acc[o][r], make_uint4(h[0], h[1], h[2], h[3]), wq[o]);
-          }
+            for (int o = 0; o < OB; ++o) mma16(acc[o][r], planes[t], wq[o]);
         }
       }
 #pragma unroll
@@ -347,20 +341,14 @@ __device__ __forceinline__ void write_dense(const Weight& w, bf16_t* out, int64_
       v[s][2 * e + 1] = sc * (__uint_as_float(h[e] & 0xffff0000u) - zo);
     }
   }
+  uint4 planes[4][NP];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) split(v[s], planes[s]);
 #pragma unroll
   for (int t = 0; t < NP; ++t) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint32_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = pack_bf16x2(v[s][2 * e], v[s][2 * e + 1]);
-        v[s][2 * e] -= __uint_as_float(h[e] << 16);
-        v[s][2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
-      }
-      // row j, chunk 4 s + g at chunk ^ j: 16 rows of a chunk in 16 places
-      *reinterpret_cast<uint4*>(mine + j * 256 + (((4 * s + g) ^ j) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    for (int s = 0; s < 4; ++s)   // row j, chunk 4 s + g at chunk ^ j: 16 rows of a chunk in 16 places
+      *reinterpret_cast<uint4*>(mine + j * 256 + (((4 * s + g) ^ j) << 4)) = planes[s][t];
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {   // four rows of whole lines
