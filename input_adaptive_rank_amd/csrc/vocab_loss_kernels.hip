@@ -24,14 +24,17 @@ namespace {
 
 using namespace product;
 
-constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+constexpr float LOG2E = 1.44269504088896340736f;
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 
-// Each row's softmax over 64 columns, in powers of two: the maximum m and the
-// sum of 2^(a - m); and the target's logit where it lies among them.
+// Each row's softmax over 64 columns: the largest logit m and the sum of
+// exp(a - m), and the target's logit where it lies among them.  Every exponent
+// is a difference times log2 e, never a difference of rounded products, and m is
+// rounded as the target's logit is: a sum of exponentials is at least 1, m at
+// least the target's logit, so that no loss is negative.
 struct RowStats {
   float2* part;             // [blocks of 64 columns][rows]
   float* mine;              // [rows] logit of the target
@@ -63,12 +66,11 @@ struct RowStats {
     for (int i = 0; i < 16 * C::FN; ++i) top = fmaxf(top, a[i]);
     top = fmaxf(top, __shfl_xor(top, 32));
     // nothing above -inf: exponents are taken from 0, so that a NaN stays
-    const float m2 = top == -INFINITY ? 0.f : top * k2;
+    const float from = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int i = 0; i < 16 * C::FN; ++i) sum += __builtin_amdgcn_exp2f(fmaf(a[i], k2, -m2));
+    for (int i = 0; i < 16 * C::FN; ++i) sum += __builtin_amdgcn_exp2f((a[i] - from) * k2);
     sum += __shfl_xor(sum, 32);
-    if (g == 0 && row < rows)
-      part[(int64_t)((v0 + col0) / 64) * rows + row] = make_float2(top == -INFINITY ? -INFINITY : m2, sum);
+    if (g == 0 && row < rows) part[(int64_t)((v0 + col0) / 64) * rows + row] = make_float2(top * scale, sum);
   }
 
   template <class C>
@@ -90,8 +92,8 @@ __global__ __launch_bounds__(1024) void row_loss_kernel(const float2* __restrict
   float top = -INFINITY, sum = 0.f;
   auto join = [&](float2 s) {
     const float t = fmaxf(top, s.x);
-    sum = (top == -INFINITY ? sum : sum * __builtin_amdgcn_exp2f(top - t)) +
-          (s.x == -INFINITY ? s.y : s.y * __builtin_amdgcn_exp2f(s.x - t));
+    sum = (top == -INFINITY ? sum : sum * __builtin_amdgcn_exp2f((top - t) * LOG2E)) +
+          (s.x == -INFINITY ? s.y : s.y * __builtin_amdgcn_exp2f((s.x - t) * LOG2E));
     top = t;
   };
   if (row < rows) {
@@ -109,10 +111,10 @@ __global__ __launch_bounds__(1024) void row_loss_kernel(const float2* __restrict
   if (k || row >= rows) return;
 #pragma unroll
   for (int i = 1; i < 4; ++i) join(st[i][rr]);
-  const float all = top == -INFINITY ? logf(sum) : fmaf(top, LN2, logf(sum));
-  lse[row] = all;
+  const float rest = logf(sum);
+  lse[row] = top == -INFINITY ? rest : top + rest;
   const int t = targets[row];
-  loss[row] = t >= 0 && t < vocab ? all - mine[row] : 0.f;
+  loss[row] = t >= 0 && t < vocab ? (top - mine[row]) + rest : 0.f;
 }
 
 // ---------------------------------------------------------------------------

@@ -1,13 +1,15 @@
-"""The vocabulary loss at the ends of its range: fp32 values next to the largest.
-References in float64, bounds as in test_gpu_vocab_loss."""
+"""The vocabulary loss at the ends of its range: fp32 values next to the largest,
+words that are certain, the largest scale.  References in float64, bounds as in
+test_gpu_vocab_loss."""
 import numpy as np
 import pytest
 
 from input_adaptive_rank_amd import dyra as D
 from input_adaptive_rank_amd import synth
+from oracle import vocab_loss_oracle as O
 
 from gpu_cases import log
-from test_gpu_vocab_loss import check_backward, check_forward, floats, ints, make, put
+from test_gpu_vocab_loss import check_backward, check_forward, floats, host, ints, make, put
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +70,45 @@ def test_hidden_values_next_to_the_largest(n, c, v):
     check_forward(case, F32, loss, lse)
     dH, _ = L.vocab_loss_backward(H, W, t, lse, floats(case["dloss"]), case["scale"], need_dw=False)
     check_backward(case, F32, lse, dH, None, need=(True, False))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+@pytest.mark.parametrize("scale", [1.0, 0.7, 1 / 3])
+@pytest.mark.parametrize("size", [1.0, 10.0, 100.0])
+def test_the_loss_of_a_certain_word_is_not_negative(size, scale, dtype):
+    """lse is at least every logit, so no loss is below 0: the target's logit and
+    the largest one are rounded alike before they are subtracted.  Logits up to 7,
+    70 and 700, most targets far above the others."""
+    from input_adaptive_rank_amd import vocab_loss as L
+    g = np.random.default_rng(24)
+    n, c, v = 800, 64, 300
+    W = synth.round_storage(g.standard_normal((v, c)) / 8, dtype)
+    t = g.integers(0, v, n)
+    H = synth.round_storage(size * (1 + 6 * g.random((n, 1))) * W[t], dtype)
+    case = dict(H=H, W=W, t=t, scale=scale)
+    loss, lse = L.vocab_loss_forward(put(H, dtype), put(W, dtype), ints(t), scale)
+    check_forward(case, dtype, loss, lse)
+    log(f"    least loss {float(loss.min()):.3e}")
+    assert float(loss.min()) >= 0.0
+    # a single word: the logit itself, and no loss at all
+    for m in (1, 70, 800):
+        loss, lse = L.vocab_loss_forward(put(H[:m], dtype), put(W[:1], dtype), ints(np.zeros(m)), scale)
+        assert not bool(loss.any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+def test_the_largest_scale(dtype):
+    """A scale of 2^126: the largest logits are next to the type's end."""
+    from input_adaptive_rank_amd import vocab_loss as L
+    g = np.random.default_rng(25)
+    n, c, v = 40, 64, 130
+    W = synth.round_storage(g.standard_normal((v, c)) / 8, dtype)
+    H = synth.round_storage(g.standard_normal((n, c)), dtype)
+    H /= 2.0 ** np.ceil(np.log2(np.abs(H @ W.T).max(1, keepdims=True)) - 1.9)   # magnitudes up to 1.87 .. 3.74
+    t = g.integers(0, v, n)
+    loss, lse = L.vocab_loss_forward(put(H, dtype), put(W, dtype), ints(t), 2.0 ** 126)
+    # a target far below the largest logit: a loss past fp32's largest number
+    past = O.forward(H, W, t, 2.0 ** 126)[0] >= 2.0 ** 128
+    assert past.any() and not past.all() and np.array_equal(np.isinf(host(loss)), past)
+    at = np.nonzero(~past)[0]
+    check_forward(dict(H=H[at], W=W, t=t[at], scale=2.0 ** 126), dtype, loss[at], lse[at])
