@@ -269,14 +269,14 @@ struct Gradient {
   template <class C>
   __device__ __forceinline__ void values(f32x16 (&v)[C::FN], int row, int col0, int rows) const {
     const int g = (threadIdx.x & 63) >> 5;
-    const float k2 = scale * LOG2E;
     const bool in = row < rows;
     const int r = in ? map[row] : 0;
-    const float w = in ? dloss[r] / found->weight : 0.f, l2 = in ? -lse[r] * LOG2E : 0.f;
+    const float w = in ? dloss[r] / found->weight : 0.f, from = in ? lse[r] : 0.f;
     const int at = in ? targets[r] - v0 - col0 : -1;
     const bool has = (unsigned)at < (unsigned)C::WN && (at >> 2 & 1) == g;
 #pragma unroll
-    for (int i = 0; i < 16 * C::FN; ++i) v[i / 16][i % 16] = __builtin_amdgcn_exp2f(fmaf(v[i / 16][i % 16], k2, l2));
+    for (int i = 0; i < 16 * C::FN; ++i)
+      v[i / 16][i % 16] = __builtin_amdgcn_exp2f(fmaf(v[i / 16][i % 16], scale, -from) * LOG2E);
     if (__any(has)) {
 #pragma unroll
       for (int i = 0; i < 16 * C::FN; ++i)

@@ -97,6 +97,22 @@ def test_the_loss_of_a_certain_word_is_not_negative(size, scale, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+@pytest.mark.parametrize("scale", [1.0, 0.25, 2.0 ** 126])
+def test_the_gradient_of_a_single_word_is_zero(scale, dtype):
+    """Its probability is exp(a - lse) = 1, whatever its logit."""
+    from input_adaptive_rank_amd import vocab_loss as L
+    g = np.random.default_rng(25)
+    for n in (7, 700):
+        W = put(synth.round_storage(g.standard_normal((1, 64)), dtype), dtype)
+        H = g.standard_normal((n, 64)) * (10.0 if scale < 2 else 2.0 ** -7)
+        H, t = put(synth.round_storage(H, dtype), dtype), ints(np.zeros(n))
+        loss, lse = L.vocab_loss_forward(H, W, t, scale)
+        assert not bool(loss.any())
+        dH, dW = L.vocab_loss_backward(H, W, t, lse, floats(g.standard_normal(n)), scale)
+        assert not bool(dH.any()) and not bool(dW.any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
 def test_the_largest_scale(dtype):
     """A scale of 2^126: the largest logits are next to the type's end."""
     from input_adaptive_rank_amd import vocab_loss as L
