@@ -573,7 +573,7 @@ int dyra_q4_dense(const dyra_q4* w, void* out, int32_t dtype, void* stream);
  * pointer may be NULL) and multiply the codes exactly; more rows read W rounded
  * to bf16 (bf16) or exactly (fp32) from the workspace.  Sums are fp32; fp32
  * operands enter as three bf16 terms (2^-24).  An infinity in X, or a value above
- * 2^112, may give NaN or an infinity where the formula has a number or an
+ * 2^114, may give NaN or an infinity where the formula has a number or an
  * infinity.  Sums have a fixed order: the same call gives the same bits.
  * Errors (before any HIP call): EINVAL, ESHAPE, EWORKSPACE; EHIP.
  */

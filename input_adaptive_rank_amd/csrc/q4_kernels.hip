@@ -7,14 +7,17 @@
 // order in which the lanes of a wave read them as 16-column operands of
 // v_mfma_f32_16x16x32_bf16: lane (j, g) holds columns 32 s + 8 g + 0 .. 7 of
 // row j in its word s = 0 .. 3, the even columns in the low half.  A pair of
-// codes then becomes a pair of bf16 numbers 128 + code with one shift and one
-// and-or: 0x4300 is 128, whose last mantissa bit is worth 1.  Parameters lie as
-// [block of 16 rows][group][16] words, the bf16 scale above the bf16 number
-// 128 + zero.
+// codes then becomes a pair of bf16 numbers 16 + code with one shift and one
+// and-or: 0x4180 is 16, whose upper four mantissa bits are worth 1 to 8.
+// Parameters lie as [block of 16 rows][group][16] words, the bf16 scale above the
+// bf16 number 128 + zero.
 //
 // Few rows: each wave multiplies whole blocks of codes, in exact products,
-//   sum_k x (128 + code) - (128 + zero) sum_k x,
-// the last sum from one more product with ones, and scales each group's sum.
+//   sum_k x (16 + code) - (16 + zero) sum_k x,
+// the last sum from one more product with ones, and scales each group's sum.  What
+// is added and taken off again costs bits: 16 is the least number that an and-or
+// can add.  With 128 (a shift of eight less, 1 % at 48 rows) a column of 2^19 that
+// every weight meets with 0 moved results by whole units.
 // Many rows: W is written out once as bf16 (rounded: at most 2^-8 of a weight, like
 // the rounding of the result) and multiplied tile by tile, for the backward pass
 // turned on its way; for fp32 operands as two bf16 planes, which hold it exactly (8
@@ -37,15 +40,15 @@ struct Weight {
 };
 
 __device__ __forceinline__ float scale_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
-__device__ __forceinline__ float zero_of(uint32_t p) { return __uint_as_float(p << 16); }   // 128 + zero
+__device__ __forceinline__ float zero_of(uint32_t p) { return __uint_as_float(p << 16) - 112.f; }   // 16 + zero
 
-// 128 + code of a word's eight columns, as bf16.  The constants are held in
+// 16 + code of a word's eight columns, as bf16.  The constants are held in
 // registers, where one v_and_or_b32 can take them both.
 __device__ __forceinline__ uint4 widen(uint32_t w) {
-  uint32_t mask = 0x000f000fu, bias = 0x43004300u;
+  uint32_t mask = 0x00780078u, bias = 0x41804180u;
   asm("" : "+v"(mask));
   asm("" : "+s"(bias));
-  return make_uint4((w & mask) | bias, (w >> 4 & mask) | bias, (w >> 8 & mask) | bias, (w >> 12 & mask) | bias);
+  return make_uint4((w << 3 & mask) | bias, (w >> 1 & mask) | bias, (w >> 5 & mask) | bias, (w >> 9 & mask) | bias);
 }
 
 // code - zero of a word's eight columns, as bf16 (whole numbers below 16: exact).

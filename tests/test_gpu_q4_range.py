@@ -1,5 +1,5 @@
-"""The 4-bit projection at the ends of its range: fp32 values next to the largest.
-References in float64."""
+"""The 4-bit projection at the ends of its range: loud columns, fp32 values next to
+the largest.  References in float64."""
 import numpy as np
 import pytest
 
@@ -21,6 +21,28 @@ def _gpu():
     import torch
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     D.lib()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("n,c1,c2", [(1, 264, 72), (5, 2056, 136), (48, 520, 264), (197, 1024, 520)])
+def test_a_loud_column_of_no_weight_drowns_nothing(n, c1, c2, group, dtype):
+    """A column of 2^19 that every weight meets with 0, beside small whole numbers.
+    A few bf16 rows add x (16 + code) and take (16 + zero) sum x off: all of it whole
+    numbers up to 31 x 2^19 + 31 x 8 x 127 < 2^24, so nothing is rounded before the
+    result is stored.  The scale is 1, a group's sum at most 15 x 8 x 127."""
+    from input_adaptive_rank_amd import q4 as Q
+    c = make(n, c1, c2, group, True, dtype, seed=31)
+    g = np.random.default_rng(32)
+    c["scale"] = np.ones_like(c["scale"])
+    c["X"] = g.integers(-8, 9, (n, c1)).astype(np.float64)
+    for k in range(3, c1, group):   # one in each group
+        c["X"][:, k] = 2.0 ** 19 * g.choice([-1, 1], n)
+        c["codes"][:, k] = c["zero"][:, k // group]
+    W = O.weight(c["codes"], c["scale"], c["zero"], group)
+    want = c["X"] @ W.T
+    assert np.abs(want).max() < 2 ** 24 and Q.q4_workspace_size(c1, c2, n, dtype) == 0
+    assert np.array_equal(host(Q.q4_forward(put(c["X"], dtype), pack(c))), synth.round_storage(want, dtype))
 
 
 @pytest.mark.parametrize("n,c1,c2", [(900, 1024, 4096), (600, 264, 6000)])
