@@ -614,7 +614,7 @@ __device__ __forceinline__ void join(const Job& j, const E& e, int block, char* 
   int m0, n0;
   corner<C>(y, y.whole + tail, m0, n0);
   const int row0 = m0 + w / C::NWN * C::WM + fm * 32, col0 = n0 + w % C::NWN * C::WN;
-  if (row0 >= ((y.rows + 63) & ~63) || col0 >= j.b.rows) return;   // rows up to 64 more may be padding
+  if (row0 >= y.rows || col0 >= j.b.rows) return;
   f32x16 v[C::FN];
 #pragma unroll
   for (int fn = 0; fn < C::FN; ++fn)
