@@ -1,5 +1,5 @@
 """The 4-bit projection at the ends of its range: loud columns, fp32 values next to
-the largest.  References in float64."""
+the largest, weights and rows past 2^31 bytes.  References in float64."""
 import numpy as np
 import pytest
 
@@ -78,3 +78,76 @@ def test_weights_next_to_the_largest():
     want, mag = O.backward(c["dY"], c["W"])
     check("dX", Q.q4_backward(put(c["dY"], F32), pack(c)), want,
           (sums(4096, 5) + 3) * U * mag + HALF[F32] * np.abs(want) * (1 + 2.0 ** -7))
+
+
+@pytest.mark.parametrize("n,c1,c2,ld", [(2200, 72, 264, 1 << 20), (40, 72, 264, 1 << 20), (1 << 18, 64, 4104, 4104)])
+def test_rows_beyond_two_gibibytes(n, c1, c2, ld):
+    """Rows and results whose last bytes lie past 2^31 (2200 rows of 2^21 bytes: past
+    2^32), in bf16."""
+    import torch
+    from input_adaptive_rank_amd import q4 as Q
+    c = make(1, c1, c2, 64, True, BF16, seed=36)
+    w, W = pack(c), torch.from_numpy(synth.round_bf16(c["W"])).cuda()
+    few = Q.q4_workspace_size(c1, c2, n, BF16) == 0
+    gen = torch.Generator(device="cuda").manual_seed(37)
+    wide, out = (torch.empty((n, ld), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    step = torch.from_numpy(np.repeat(c["scale"], 64, axis=1)[:, :c1]).cuda()
+    exact = torch.from_numpy(c["W"]).cuda()
+    for back in (False, True):
+        cin, cout = (c2, c1) if back else (c1, c2)
+        x, y = wide[:, ld - cin:], out[:, ld - cout:]
+        x.copy_(torch.randn((n, cin), generator=gen, device="cuda"))
+        if back:
+            Q.q4_backward(x, w, dX=y)
+        else:
+            Q.q4_forward(x, w, out=y)
+        m = W if back else (exact if few else W).t().contiguous()
+        terms = 0.0 if back or not few else 62.0 * step.t()
+        for at in range(0, n, 1 << 16):
+            rows = slice(at, at + (1 << 16))
+            want, mag = x[rows].double() @ m, x[rows].double().abs() @ (m.abs() + terms)
+            bound = (sums(cin, 1) + 3) * U * mag + HALF[BF16] * want.abs() * (1 + 2.0 ** -7)
+            assert bool(((y[rows].double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("n", [3, 1500])
+def test_weights_beyond_two_gibibytes(n):
+    """A weight of 65544 x 65536: its codes pass 2^31 bytes, its bf16 form 2^33.
+    Compared at the last columns and some others."""
+    import torch
+    from input_adaptive_rank_amd import q4 as Q
+    c1, c2, group = 65544, 65536, 128
+    groups = -(-c1 // group)
+    gen = torch.Generator(device="cuda").manual_seed(38)
+    codes = torch.randint(0, 256, (c2, c1 // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scale = (0.5 + torch.rand((c2, groups), generator=gen, device="cuda")).bfloat16()
+    w = Q.q4_pack(codes, scale, group=group)
+    X = torch.randn((n, c1), generator=gen, device="cuda").bfloat16()
+    at = torch.cat([torch.arange(c2 - 40, c2, device="cuda"), torch.randint(0, c2, (200,), generator=gen, device="cuda")])
+
+    def rows(at):
+        q = codes[at]
+        v = torch.stack([q & 15, q >> 4], 2).flatten(1).double() - 8
+        s = scale[at].double().repeat_interleave(group, 1)[:, :c1]
+        return v * s, s
+
+    few = Q.q4_workspace_size(c1, c2, n, BF16) == 0
+    assert few == (n == 3)
+    W, s = rows(at)
+    if not few:
+        W = W.bfloat16().double()
+    want, mag = X.double() @ W.t().contiguous(), X.double().abs() @ (W.abs() + (62.0 * s if few else 0.0)).t().contiguous()
+    bound = (sums(c1, 1) + 3) * U * mag + HALF[BF16] * want.abs() * (1 + 2.0 ** -7)
+    got = Q.q4_forward(X, w)[:, at].double()
+    assert bool(((got - want).abs() <= bound).all())
+    if few:
+        return
+    # the gradient of rows that are zero but at those columns
+    dY = torch.zeros((n, c2), dtype=torch.bfloat16, device="cuda")
+    at = torch.unique(at)
+    dY[:, at] = torch.randn((n, len(at)), generator=gen, device="cuda").bfloat16()
+    W = rows(at)[0].bfloat16().double()
+    g = dY[:, at].double()
+    want, mag = g @ W, g.abs() @ W.abs()
+    bound = (sums(c2, 1) + 3) * U * mag + HALF[BF16] * want.abs() * (1 + 2.0 ** -7)
+    assert bool(((Q.q4_backward(dY, w).double() - want).abs() <= bound).all())

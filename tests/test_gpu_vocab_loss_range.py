@@ -1,6 +1,6 @@
 """The vocabulary loss at the ends of its range: fp32 values next to the largest,
-words that are certain, the largest scale.  References in float64, bounds as in
-test_gpu_vocab_loss."""
+words that are certain, the largest scale, operands past 2^31 bytes.  References in
+float64, bounds as in test_gpu_vocab_loss."""
 import numpy as np
 import pytest
 
@@ -128,3 +128,41 @@ def test_the_largest_scale(dtype):
     assert past.any() and not past.all() and np.array_equal(np.isinf(host(loss)), past)
     at = np.nonzero(~past)[0]
     check_forward(dict(H=H[at], W=W, t=t[at], scale=2.0 ** 126), dtype, loss[at], lse[at])
+
+
+@pytest.mark.parametrize("n,c,v,ldh", [(2200, 64, 300, 1 << 20), (4, 32768, 33000, 32768), (1100, 64, 300, 1 << 20)])
+def test_operands_beyond_two_gibibytes(n, c, v, ldh):
+    """Rows, weights and their gradients whose last bytes lie past 2^31 (2200 rows
+    2^21 bytes apart: past 2^32)."""
+    import torch
+    from input_adaptive_rank_amd import vocab_loss as L
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    W = (torch.randn((v, c), generator=gen, device="cuda") / c ** 0.5).bfloat16()
+    t = torch.randint(0, v, (n,), generator=gen, device="cuda")
+    t[-1] = v - 1
+    H = (torch.randn((n, c), generator=gen, device="cuda") + 3 * W[t].float()).bfloat16()
+    wide, dwide = (torch.empty((n, ldh), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    h, dh = wide[:, ldh - c:], dwide[:, ldh - c:]
+    h.copy_(H)
+    loss, lse = L.vocab_loss_forward(h, W, t.int())
+    g = torch.full((n,), 1.0 / n, device="cuda")
+    dW = L.vocab_loss_backward(h, W, t.int(), lse, g, dH=dh)[1]
+    a = H.double() @ W.double().t()
+    mag = (H.double().abs() @ W.double().abs().t()).amax(1)
+    want = torch.logsumexp(a, 1)
+    ea = (c / 16 + 66) * U * mag
+    bound = ea + U * (4 * a.abs().amax(1) + 132 + v / 2048 + 4 * want.abs())
+    assert bool(((lse - want).abs() <= bound).all())
+    rows = torch.arange(n, device="cuda")
+    assert bool(((loss - (want - a[rows, t])).abs() <= 2 * bound + U * 4 * a.abs().amax(1)).all())
+    p = torch.exp(a - lse.double()[:, None])
+    d = p.clone()
+    d[rows, t] -= 1
+    d /= n
+    e = p / n * (ea + U * (4 * a.abs().amax(1) + 4 * lse.double().abs() + 4))[:, None] + 3 * U * d.abs()
+    e += 2.0 ** -8 * (d.abs() + e)
+    lim = lambda err, mags, want, K: (err + (K / 16 + 70) * U * mags) * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()  # noqa: E731
+    Wd, Hd = W.double(), H.double()
+    dhw, dww = d @ Wd, d.t() @ Hd
+    assert bool(((dh.double() - dhw).abs() <= lim(e @ Wd.abs(), (d.abs() + e) @ Wd.abs(), dhw, v)).all())
+    assert bool(((dW.double() - dww).abs() <= lim(e.t() @ Hd.abs(), (d.abs() + e).t() @ Hd.abs(), dww, n)).all())
