@@ -82,8 +82,9 @@ struct Tile {
 // 256 x 256: 128 flop a byte loaded, one workgroup a CU (128 KB of LDS)
 typedef Tile<256, 256, 2, 4, 2, 1, 100, 75> Big;
 // 320 x 256: 142 flop a byte, and other sizes that fill whole rounds (5003 x 4096
-// results of 64 steps are 256 of its tiles: 142 us instead of 174 with 320 tiles of
-// 256 x 256; 1.28 PFLOP/s in whole rounds)
+// results of 64 steps are 256 of its tiles: a 4-bit projection 140 us instead of 166
+// with 320 tiles of 256 x 256, a gradient of 4099 x 4096 of 192 steps 354 instead of
+// 379; 1.28 PFLOP/s in whole rounds)
 typedef Tile<320, 256, 2, 4, 2, 1, 125, 94> Tall;
 // 128 x 128: four times the tiles, two workgroups a CU
 typedef Tile<128, 128, 2, 2, 2, 2, 45, 55> Small;
@@ -387,7 +388,7 @@ __global__ __launch_bounds__(C::NT, C::WPE) void product_kernel(Job j, E e) {
       // multiplies, and before the last one the wave waits for the next step's
       // loads and for the others to have read this step's slot, so that the last
       // one's products cover the next step's first reads and the loads into the
-      // slot that came free (4099 x 32000 x 4096: 927 against 960 us).
+      // slot that came free (4099 x 32000 x 4096 in 256 x 256 tiles: 927 against 960 us).
       wait_vm_lgkm0<(C::NS - 1) * LOADS>();   // this wave's loads of step 0 have landed
       bare_barrier();                          // everyone's
       if constexpr (MULTIPLIES) pull(ring, 0);
@@ -511,8 +512,10 @@ struct Fp32 {
 // A few rows, in three planes, by an fp32 matrix that is read once, as it lies: each
 // wave splits what it multiplies, which takes about as long as the six products do,
 // and both less than the matrix takes to arrive.  Loss of fp32 rows, us (with planes
-// of W in memory first): 4 x 2048 x 30000 72 (233), 100 x 1024 x 8000 43 (51); with more
-// rows the splitting costs more than the planes, 700 x 1024 x 5000 77 (72).
+// of W in memory first): 4 x 2048 x 30000 74 (232), 100 x 1024 x 8000 33 (49), 400 x 2048 x
+// 4000 75 (74); with more rows the splitting costs more than the planes, 1500 x 512 x
+// 8000 123 (85).  Between those the estimate of 128 x 128 tiles is some 15 % high: 700 x
+// 1024 x 5000 runs here, 79 (68).
 template <bool TB, class E>
 __global__ __launch_bounds__(Direct::NT, 1) void direct_kernel(Job j, E e) {
   typedef Direct C;

@@ -23,8 +23,8 @@
 // turned on its way; for fp32 operands as two bf16 planes, which hold it exactly (8
 // bits of scale times 5).
 //
-// 4096 -> 4096, group 128: one row 4.5 us (6.8 with the call), 5003 rows 140 (a product
-// at 1.3 PFLOP/s alone 129).
+// 4096 -> 4096, group 128: one row 4.5 us (7 with the call), 5003 rows 141 (a product
+// at 1.3 PFLOP/s alone 129).  (Times vary by 7 % with the card.)
 #include "mfma_product.h"
 
 namespace {
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(ROW_WAVES * 64) void rows_f32_kernel(RowsArgs a) {
 // of 128 bytes a load) into its own part of LDS, half a block at a time, the next
 // one while this one is multiplied, and its codes and parameters beside it.
 // Nothing is shared between the waves before their sums.  48 rows, 4096 ->
-// 12288: 12.6 us (operands straight from memory 28, one block of W a workgroup 41).
+// 12288: 13 us (operands straight from memory 28, one block of W a workgroup 41).
 template <int RT, int OB, int GPB>
 __global__ __launch_bounds__(ROW_WAVES * 64) void rows_kernel(RowsArgs a) {
   constexpr int XH = RT * 2048, CODES = 2 * XH, PARAMS = CODES + OB * 1024, WAVE = PARAMS + GPB * 256;
@@ -525,11 +525,12 @@ struct FewRows {
   double us;
 };
 
-// In bf16 a workgroup fills a CU's LDS, so that workgroups run in rounds of 256;
-// a round's time is made of its turns of eight column blocks, of its sums' way
-// through LDS and, but for the first, of its start.  Measured at 4096 -> 4096 (us): 1 row, RT OB = 1 1 4.2, 1 2
-// 4.7, 1 4 6.3; 64 rows, 2 1 9.9, 2 2 7.0, 2 4 8.9, 3 2 8.6; 384 rows, 2 4 26.1, 3 4 24.3.  fp32
-// splits X anew for each pair of blocks of W.
+// In bf16 workgroups are taken to run in rounds of 256, one a CU: a fit of the times
+// below (by its LDS, 43 to 139 KB, up to three of the smallest fit a CU).  A round's time is
+// made of its turns of eight column blocks, of its sums' way through LDS and, but for
+// the first, of its start.  Measured at 4096 -> 4096, groups of 128 (us): 1 row, RT OB = 1 1
+// 4.2, 1 2 4.7, 1 4 6.3; 64 rows, 2 1 9.9, 2 2 7.0, 2 4 8.9, 3 2 8.6; 384 rows, 2 4 26.1, 3 4
+// 24.3.  fp32 splits X anew for each pair of blocks of W.
 FewRows few_rows(int64_t c1, int64_t c2, int64_t n, int dtype) {
   const int64_t blocks = cdiv(c2, 16), turns_k = cdiv(cdiv(c1, 128), ROW_WAVES);
   FewRows best{0, 0, 1e30};

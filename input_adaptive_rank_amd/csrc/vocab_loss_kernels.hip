@@ -6,12 +6,14 @@
 //
 // Forward: one product whose epilogue leaves, for each row and 64 columns, the
 // maximum and the sum of exponentials below it; a second launch joins them.  4099 x
-// 4096 x 32000: 870 us, a library's product alone 830 to 870.  Backward: the rows
+// 4096 x 32000: 885 us, a library's product alone 830 to 870.  Backward: the rows
 // that count are gathered; for one piece of the vocabulary after the other their
 // logits are multiplied again, d goes to memory as bf16, and the two gradients are
 // products of the piece, whose operands the LDS turns where they lie across the
-// reduction.  The pieces keep d within what the last-level cache holds.  The same
-// sizes, 3280 rows that count: 2275 us, 1.13 PFLOP/s.
+// reduction.  The pieces keep d in bf16 within the 256 MB of the last-level cache, up to
+// 2^19 rows (a piece has at least 256 words); its three planes in fp32 take up to three
+// times that.  The same sizes, 3280 rows that count: 2310 us, 1.12 PFLOP/s.  (Times vary
+// by 7 % with the card.)
 //
 // bf16: logits are sums of exact products in fp32; d is rounded to bf16 for
 // the two products of the backward pass (at most 2^-8 of a term, like the
@@ -368,8 +370,8 @@ Plan plan_as(bool direct, int64_t n, int64_t C, int64_t V, int dtype, bool backw
   const bool wide = dtype == DYRA_F32;
   q.np = wide ? 3 : 1;
   const int terms = wide ? 6 : 1, once = direct ? 1 : terms;
-  // d of a piece is at most 2^27 elements a plane (256 MB in bf16, the last-level
-  // cache), planes of fp32 weights at most 2^28
+  // d of a piece is at most 2^27 elements a plane (in bf16 256 MB, the last-level cache)
+  // or 256 words of it, planes of fp32 weights at most 2^28 elements
   int64_t most = (int64_t)1 << 20;
   if (backward) most = std::min<int64_t>(most, ((int64_t)1 << 27) / n);
   if (wide && !direct) most = std::min<int64_t>(most, ((int64_t)1 << 28) / (3 * C));
