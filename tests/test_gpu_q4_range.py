@@ -45,6 +45,22 @@ def test_a_loud_column_of_no_weight_drowns_nothing(n, c1, c2, group, dtype):
     assert np.array_equal(host(Q.q4_forward(put(c["X"], dtype), pack(c))), synth.round_storage(want, dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=IDS.get)
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("n,c1,c2", [(1, 264, 72), (48, 520, 264), (197, 1024, 520)])
+def test_few_rows_of_the_largest_values(n, c1, c2, group, dtype):
+    """Whole numbers up to 8 times 2^111: a group's sums of x (16 + code) reach 31 x 8 x
+    128 x 2^111 < 2^126, without a rounding; the scale brings them back."""
+    from input_adaptive_rank_amd import q4 as Q
+    c = make(n, c1, c2, group, True, dtype, seed=39)
+    c["scale"][:] = 2.0 ** -40
+    c["X"] = np.random.default_rng(40).integers(-8, 9, (n, c1)) * 2.0 ** 111
+    c["X"][0] = 2.0 ** 114
+    want = c["X"] @ O.weight(c["codes"], c["scale"], c["zero"], group).T
+    assert Q.q4_workspace_size(c1, c2, n, dtype) == 0
+    assert np.array_equal(host(Q.q4_forward(put(c["X"], dtype), pack(c))), synth.round_storage(want, dtype))
+
+
 @pytest.mark.parametrize("n,c1,c2", [(900, 1024, 4096), (600, 264, 6000)])
 def test_values_next_to_the_largest(n, c1, c2):
     """Many fp32 rows with entries at the type's ends by small weights: the results
